@@ -20,6 +20,8 @@ ATTN_STATUS_CAPACITY = 1
 ATTN_STATUS_SEQLENS = 2
 ATTN_STATUS_TIMEOUT = 4
 ATTN_STATUS_BOUNDS = 8
+ATTN_STATUS_POSITION = 16
+ATTN_STATUS_PAGES = 32
 
 
 class AttnConfig(ctypes.Structure):
@@ -34,11 +36,18 @@ class AttnKV(ctypes.Structure):
                 ("cache_lens", ctypes.c_void_p), ("slot_capacity", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p), ("page_size", ctypes.c_int32),
                 ("pages_per_req", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
-                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("k_block_scale", ctypes.c_void_p), ("v_block_scale", ctypes.c_void_p)]
+
+
+class AttnRopeAxes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("section", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
 ATTN_KV_BF16 = 0
 ATTN_KV_E4M3 = 1
+ATTN_KV_E2M1 = 2
 
 
 class AttnError(RuntimeError):
@@ -54,6 +63,7 @@ _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _CFG = ctypes.POINTER(AttnConfig)
 _KV = ctypes.POINTER(AttnKV)
+_ROPE = ctypes.POINTER(AttnRopeAxes)
 
 EXPORTS = {
     "attn_workspace_size": (_SZ, [_CFG, _I32, _I32, _I32]),
@@ -68,6 +78,14 @@ EXPORTS = {
     "attn_decode_splits": (_I32, [_CFG, _I32, _I32]),
     "attn_qkv_proj_prepare": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _P, _P, _I32, _I32, _KV, _P, _P, _SZ, _P]),
     "attn_o_proj": (ctypes.c_int, [_CFG, _P, _I32, _P, _I32, _P, _P, _SZ, _P]),
+    "attn_kv_append_axes": (ctypes.c_int, [_CFG, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _SZ, _P]),
+    "attn_prefill_prepare_axes": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _P, _SZ, _P]),
+    "attn_prefill_axes": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _I32, _I32, _I32, _KV, _ROPE, _P, _P, _SZ, _P]),
+    "attn_decode_axes": (ctypes.c_int, [_CFG, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _P, _SZ, _P]),
+    "attn_decode_attend_axes": (ctypes.c_int, [_CFG, _P, _P, _I32, _I32, _KV, _ROPE, _P, _P, _SZ, _P]),
+    "attn_qkv_proj_prepare_axes": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _P,
+                                                  _SZ, _P]),
+    "attn_kv_gather": (ctypes.c_int, [_CFG, _KV, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
     "attn_get_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "attn_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sample_tokens": (ctypes.c_int, [_P, _I32, _I32, ctypes.c_int64, _P, _P, _P, _P, _P, _P]),
@@ -120,7 +138,7 @@ def config(num_q_heads: int, num_kv_heads: int, head_dim: int, rms_eps: float = 
 class KVCache:
     """Device tensors of one layer's KV cache (see attn_kv_t)."""
 
-    k_cache: torch.Tensor       # bf16, or uint8 E4M3 codes, [num_slots, Hkv, D]
+    k_cache: torch.Tensor       # bf16, or uint8 E4M3 codes, [num_slots, Hkv, D]; E2M1: uint8 [num_slots, Hkv, D/2]
     v_cache: torch.Tensor       # same type and shape as k_cache
     slot_base: torch.Tensor     # int64 [B] (contiguous layout)
     cache_lens: torch.Tensor    # int32 [B]
@@ -129,6 +147,10 @@ class KVCache:
     page_size: int = 0
     k_scale: float = 1.0        # E4M3 caches: entry = code * scale
     v_scale: float = 1.0
+    # E2M1 caches: uint8 [Hkv, num_slots, D/16] E4M3 scales of 16 entries each
+    # (entry = code * block scale * scale); given, the cache is E2M1
+    k_block_scale: torch.Tensor | None = None
+    v_block_scale: torch.Tensor | None = None
 
     # The C struct is built (and the tensors checked) once and rebuilt when a
     # field is assigned; tensors changed in place (resize_, set_) are not seen.
@@ -146,6 +168,15 @@ class KVCache:
 
     def _make_struct(self) -> AttnKV:
         fp8 = self.k_cache.dtype == torch.uint8
+        kbs, vbs = self.k_block_scale, self.v_block_scale
+        fp4 = kbs is not None or vbs is not None
+        if fp4:
+            S, H, half = self.k_cache.shape
+            assert self.v_cache.shape == self.k_cache.shape, "v_cache"
+            for name in ("k_block_scale", "v_block_scale"):
+                t = getattr(self, name)
+                assert t is not None and t.dtype == torch.uint8 and t.is_contiguous() and t.is_cuda, name
+                assert fp8 and tuple(t.shape) == (H, S, half // 8), name
         for name in ("k_cache", "v_cache"):
             t = getattr(self, name)
             assert t.dtype == (torch.uint8 if fp8 else torch.bfloat16), name
@@ -161,7 +192,43 @@ class KVCache:
         return AttnKV(self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.k_cache.shape[0],
                       self.slot_base.data_ptr(), self.cache_lens.data_ptr(),
                       self.slot_capacity.data_ptr(), pt, ps, ppr,
-                      ATTN_KV_E4M3 if fp8 else ATTN_KV_BF16, float(self.k_scale), float(self.v_scale))
+                      ATTN_KV_E2M1 if fp4 else ATTN_KV_E4M3 if fp8 else ATTN_KV_BF16, float(self.k_scale),
+                      float(self.v_scale), kbs.data_ptr() if fp4 else None, vbs.data_ptr() if fp4 else None)
+
+    def rows(self, lo: int, hi: int, cache_lens: torch.Tensor | None = None) -> "KVCache":
+        """The same cache seen by the requests [lo, hi) (with other cached
+        lengths for them, if given)."""
+        pt = self.page_table
+        return dataclasses.replace(self, slot_base=self.slot_base[lo:hi],
+                                   cache_lens=self.cache_lens[lo:hi] if cache_lens is None else cache_lens,
+                                   slot_capacity=self.slot_capacity[lo:hi],
+                                   page_table=None if pt is None else pt[lo:hi].contiguous())
+
+
+@dataclasses.dataclass
+class RopeAxes:
+    """Rotary positions with several axes (see attn_rope_axes_t): positions
+    int32 [A, N] on the device (rows may be strided), sections the rotation
+    pairs of each axis (they sum to D/2), interleaved the order of the axes
+    over the pairs."""
+
+    positions: torch.Tensor
+    sections: tuple
+    interleaved: bool = False
+
+    def struct(self, n: int) -> AttnRopeAxes:
+        t, A = self.positions, len(self.sections)
+        assert t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and A <= 4, "positions"
+        assert t.shape[0] == A and t.shape[1] >= n and (t.shape[1] <= 1 or t.stride(1) == 1), "positions"
+        ld = t.stride(0) if A > 1 else t.shape[1]
+        assert ld >= n, "positions"
+        return AttnRopeAxes(A, (ctypes.c_int32 * 4)(*[int(x) for x in self.sections]), int(bool(self.interleaved)),
+                            t.data_ptr(), ld)
+
+
+def _rope(rope, n):
+    """The C struct of ``rope`` (None: no axes) for a call over n tokens."""
+    return None if rope is None else ctypes.byref(rope.struct(n))
 
 
 def decode_splits(cfg: AttnConfig, B: int, max_cache_len: int) -> int:
@@ -194,44 +261,47 @@ def _bf16(t, name):
     return _ptr(t)
 
 
-def kv_append(cfg: AttnConfig, qkv, k_norm_w, cu_seqlens, kv: KVCache, workspace, stream=None):
+def kv_append(cfg: AttnConfig, qkv, k_norm_w, cu_seqlens, kv: KVCache, workspace, stream=None, rope=None):
+    """K and V of the new tokens into the cache.  ``rope`` (here and below): a
+    RopeAxes with the tokens' positions on several axes."""
     B = cu_seqlens.numel() - 1
     s = kv.struct()
-    _check(load().attn_kv_append(ctypes.byref(cfg), _bf16(qkv, "qkv"), None, _bf16(k_norm_w, "k_norm_w"),
-                                 _ptr(cu_seqlens), B, qkv.shape[0], ctypes.byref(s), _ptr(workspace),
-                                 workspace.numel(), _stream(stream)))
+    _check(load().attn_kv_append_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(k_norm_w, "k_norm_w"),
+                                      _ptr(cu_seqlens), B, qkv.shape[0], ctypes.byref(s), _rope(rope, qkv.shape[0]),
+                                      _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def prefill(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, cu_seqlens, max_seqlen: int, kv: KVCache,
-            out, workspace, stream=None):
+            out, workspace, stream=None, rope=None):
     assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda
     B = cu_seqlens.numel() - 1
     s = kv.struct()
-    _check(load().attn_prefill(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
-                               _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
-                               int(max_seqlen), ctypes.byref(s), _bf16(out, "out"), _ptr(workspace),
-                               workspace.numel(), _stream(stream)))
+    _check(load().attn_prefill_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
+                                    _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
+                                    int(max_seqlen), ctypes.byref(s), _rope(rope, qkv.shape[0]), _bf16(out, "out"),
+                                    _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def decode(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, max_cache_len: int, kv: KVCache, out,
-           workspace, stream=None):
+           workspace, stream=None, rope=None):
     B = qkv.shape[0]
     s = kv.struct()
-    _check(load().attn_decode(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
-                              _bf16(k_norm_w, "k_norm_w"), B, int(max_cache_len), ctypes.byref(s),
-                              _bf16(out, "out"), _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check(load().attn_decode_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
+                                   _bf16(k_norm_w, "k_norm_w"), B, int(max_cache_len), ctypes.byref(s),
+                                   _rope(rope, B), _bf16(out, "out"), _ptr(workspace), workspace.numel(),
+                                   _stream(stream)))
 
 
 def prefill_prepare(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, cu_seqlens, kv: KVCache, q_out,
-                    workspace, stream=None):
+                    workspace, stream=None, rope=None):
     """First half of ``prefill``: K/V appended to the cache, prepared Q
     (normed, rotated, bf16 [N, Hq, D]) written to ``q_out``."""
     B = cu_seqlens.numel() - 1
     s = kv.struct()
-    _check(load().attn_prefill_prepare(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
-                                       _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
-                                       ctypes.byref(s), _bf16(q_out, "q_out"), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)))
+    _check(load().attn_prefill_prepare_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
+                                            _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
+                                            ctypes.byref(s), _rope(rope, qkv.shape[0]), _bf16(q_out, "q_out"),
+                                            _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def prefill_attend(cfg: AttnConfig, q, cu_seqlens, max_seqlen: int, kv: KVCache, out, workspace,
@@ -246,12 +316,13 @@ def prefill_attend(cfg: AttnConfig, q, cu_seqlens, max_seqlen: int, kv: KVCache,
 
 
 def decode_attend(cfg: AttnConfig, qkv, q_norm_w, max_cache_len: int, kv: KVCache, out, workspace,
-                  stream=None):
+                  stream=None, rope=None):
     """Attention half of ``decode`` (the cache already holds the new K/V)."""
     s = kv.struct()
-    _check(load().attn_decode_attend(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
-                                     qkv.shape[0], int(max_cache_len), ctypes.byref(s), _bf16(out, "out"),
-                                     _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check(load().attn_decode_attend_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
+                                          qkv.shape[0], int(max_cache_len), ctypes.byref(s),
+                                          _rope(rope, qkv.shape[0]), _bf16(out, "out"), _ptr(workspace),
+                                          workspace.numel(), _stream(stream)))
 
 
 def decode_static_scratch(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, max_cache_len: int, kv: KVCache,
@@ -266,18 +337,18 @@ def decode_static_scratch(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, max_cache_le
 
 
 def qkv_proj_prepare(cfg: AttnConfig, hidden, w_qkv, q_norm_w, k_norm_w, cu_seqlens, kv: KVCache, q_out,
-                     workspace, stream=None):
+                     workspace, stream=None, rope=None):
     """The merged Q/K/V projection fused with ``prefill_prepare``: qkv =
     hidden [N, C] . w_qkv^T in fp32, then Q/K norm + RoPE, K/V appended,
     prepared Q written to ``q_out`` [N, Hq, D]."""
     assert hidden.dim() == 2 and w_qkv.dim() == 2 and w_qkv.shape[1] == hidden.shape[1]
     B = cu_seqlens.numel() - 1
     s = kv.struct()
-    _check(load().attn_qkv_proj_prepare(ctypes.byref(cfg), _bf16(hidden, "hidden"), hidden.shape[1],
-                                        _bf16(w_qkv, "w_qkv"), _bf16(q_norm_w, "q_norm_w"),
-                                        _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, hidden.shape[0],
-                                        ctypes.byref(s), _ptr(q_out), _ptr(workspace), workspace.numel(),
-                                        _stream(stream)))
+    _check(load().attn_qkv_proj_prepare_axes(ctypes.byref(cfg), _bf16(hidden, "hidden"), hidden.shape[1],
+                                             _bf16(w_qkv, "w_qkv"), _bf16(q_norm_w, "q_norm_w"),
+                                             _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, hidden.shape[0],
+                                             ctypes.byref(s), _rope(rope, hidden.shape[0]), _ptr(q_out),
+                                             _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def o_proj(cfg: AttnConfig, attn_out, w_o, out, workspace, stream=None):
@@ -286,6 +357,20 @@ def o_proj(cfg: AttnConfig, attn_out, w_o, out, workspace, stream=None):
     _check(load().attn_o_proj(ctypes.byref(cfg), _bf16(attn_out, "attn_out"), attn_out.shape[0],
                               _bf16(w_o, "w_o"), w_o.shape[0], _bf16(out, "out"), _ptr(workspace),
                               workspace.numel(), _stream(stream)))
+
+
+def kv_gather(cfg: AttnConfig, kv: KVCache, cu_seqlens, start, k_out, v_out, workspace, stream=None):
+    """Cached entries read back: the entries at positions start[b] + j of
+    request b into rows cu_seqlens[b] + j of ``k_out`` and ``v_out`` (bf16
+    [N, Hkv, D]; codes as the bf16 nearest to the value they stand for)."""
+    assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and cu_seqlens.is_contiguous(), "cu_seqlens"
+    B = cu_seqlens.numel() - 1
+    assert start.dtype == torch.int32 and start.is_cuda and start.is_contiguous() and start.numel() >= B, "start"
+    assert k_out.shape == v_out.shape and tuple(k_out.shape[1:]) == (cfg.num_kv_heads, cfg.head_dim), "k_out"
+    s = kv.struct()
+    _check(load().attn_kv_gather(ctypes.byref(cfg), ctypes.byref(s), _ptr(cu_seqlens), _ptr(start), B,
+                                 k_out.shape[0], _bf16(k_out, "k_out"), _bf16(v_out, "v_out"), _ptr(workspace),
+                                 workspace.numel(), _stream(stream)))
 
 
 def get_status(workspace, stream=None) -> int:

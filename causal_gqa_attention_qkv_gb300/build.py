@@ -33,7 +33,7 @@ def _needs_rebuild(srcs, headers) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        [os.path.join(os.path.dirname(HERE), "include", "attn.h")]
+        sorted(glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")))
     if not force and not _needs_rebuild(srcs, headers):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)

@@ -29,20 +29,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // bf16 cache: boxes of 64 (d) x 1 (head) x box_rows, 128-byte swizzled.
-// E4M3 cache (one byte per entry): boxes of D x 1 x box_rows, 128-byte
-// swizzled for D = 128, unswizzled 64-byte rows for D = 64.
-int encode_cache_map(void* base, int64_t num_slots, int Hkv, int D, int box_rows, bool f8,
+// Caches of codes: boxes of a head's whole row x 1 x box_rows.  E4M3 (D bytes
+// a row): 128-byte swizzled for D = 128, unswizzled 64-byte rows for D = 64.
+// E2M1 (D / 2 bytes a row): 64-byte swizzled for D = 128, unswizzled 32-byte
+// rows for D = 64.
+int encode_cache_map(void* base, int64_t num_slots, int Hkv, int D, int box_rows, int kv_dtype,
                      CUtensorMap* m) {
   auto enc = encoder();
   if (!enc) return -1;
-  const cuuint64_t es = f8 ? 1 : 2;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)num_slots};
-  cuuint64_t strides[2] = {(cuuint64_t)D * es, (cuuint64_t)Hkv * D * es};
-  cuuint32_t box[3] = {f8 ? (cuuint32_t)D : 64u, 1, (cuuint32_t)box_rows};
+  const bool codes = kv_dtype != ATTN_KV_BF16, f4 = kv_dtype == ATTN_KV_E2M1;
+  const cuuint64_t es = codes ? 1 : 2;
+  const cuuint64_t row = f4 ? D / 2 : D;  // elements of a head's row
+  cuuint64_t dims[3] = {row, (cuuint64_t)Hkv, (cuuint64_t)num_slots};
+  cuuint64_t strides[2] = {row * es, (cuuint64_t)Hkv * row * es};
+  cuuint32_t box[3] = {codes ? (cuuint32_t)row : 64u, 1, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapSwizzle sw =
-      (!f8 || D == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = enc(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base,
+  const CUtensorMapSwizzle sw = codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : f4             ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
+  CUresult r = enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base,
                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : -1;
@@ -71,16 +76,37 @@ int check_kv(const attn_kv_t* kv) {
     return ATTN_EINVAL;
   }
   if (kv->num_slots <= 0 || kv->num_slots >= (int64_t(1) << 31)) return ATTN_EINVAL;
-  if (kv->kv_dtype == ATTN_KV_E4M3) {
+  if (kv->kv_dtype == ATTN_KV_E4M3 || kv->kv_dtype == ATTN_KV_E2M1) {
     if (!(kv->k_scale > 0.f) || !(kv->v_scale > 0.f) || std::isinf(kv->k_scale) ||
         std::isinf(kv->v_scale))
       return ATTN_EINVAL;
+    if (kv->kv_dtype == ATTN_KV_E2M1) {
+      if (!kv->k_block_scale || !kv->v_block_scale) return ATTN_EINVAL;
+      if ((reinterpret_cast<uintptr_t>(kv->k_block_scale) | reinterpret_cast<uintptr_t>(kv->v_block_scale)) & 15)
+        return ATTN_EINVAL;
+    }
   } else if (kv->kv_dtype != ATTN_KV_BF16) {
     return ATTN_EINVAL;
   }
   if ((reinterpret_cast<uintptr_t>(kv->k_cache) | reinterpret_cast<uintptr_t>(kv->v_cache)) & 15)
     return ATTN_EINVAL;
   return ATTN_OK;
+}
+
+// Rotary axes of a call over n tokens (rope == NULL: none).
+int check_rope(const attn_rope_axes_t* rope, const attn_config_t* cfg, int32_t n) {
+  if (!rope) return ATTN_OK;
+  const int A = rope->num_axes, half = cfg->head_dim / 2;
+  if (A < 1 || A > 4 || !rope->positions || rope->ld < n || rope->ld < 0) return ATTN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(rope->positions) & 3) return ATTN_EINVAL;
+  int sum = 0;
+  for (int a = 0; a < A; ++a) {
+    if (rope->section[a] < 0 || rope->section[a] > half) return ATTN_EINVAL;
+    if (rope->interleaved && a > 0 && rope->section[a] > 0 && (rope->section[a] - 1) * A + a >= half)
+      return ATTN_EINVAL;
+    sum += rope->section[a];
+  }
+  return sum == half ? ATTN_OK : ATTN_EINVAL;
 }
 
 int check_device() {
@@ -153,9 +179,8 @@ int make_matrix_map(const void* base, int64_t rows, int64_t cols, int box_rows, 
 }
 
 int make_cache_maps(const attn_kv_t& kv, int Hkv, int D, int box_rows, CacheMaps* maps) {
-  const bool f8 = kv.kv_dtype == ATTN_KV_E4M3;
-  if (encode_cache_map(kv.k_cache, kv.num_slots, Hkv, D, box_rows, f8, &maps->k) != 0) return -1;
-  if (encode_cache_map(kv.v_cache, kv.num_slots, Hkv, D, box_rows, f8, &maps->v) != 0) return -1;
+  if (encode_cache_map(kv.k_cache, kv.num_slots, Hkv, D, box_rows, kv.kv_dtype, &maps->k) != 0) return -1;
+  if (encode_cache_map(kv.v_cache, kv.num_slots, Hkv, D, box_rows, kv.kv_dtype, &maps->v) != 0) return -1;
   return 0;
 }
 
@@ -178,8 +203,8 @@ bool ws_ok(const void* ws, size_t bytes, size_t need) {
 
 // Prologue kernel: K (and, with q_out, Q) norm + RoPE, K/V cache append.
 int append(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, const void* k_norm_w,
-           const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv, void* q_out,
-           void* workspace, cudaStream_t s) {
+           const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
+           const attn_rope_axes_t* rope, void* q_out, void* workspace, cudaStream_t s) {
   PrologueArgs a;
   a.cfg = *cfg;
   a.qkv = qkv;
@@ -189,8 +214,9 @@ int append(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, cons
   a.cu_seqlens = cu_seqlens;
   a.B = B;
   a.N = N;
-  a.kv = *kv;
+  a.kv = load_kv(kv);
   a.status = status_of(workspace);
+  a.axes = rope_axes(rope, cfg->head_dim);
   make_rope_freqs(cfg->rope_theta, cfg->head_dim, &a.freqs);
   return launch_prologue(a, s) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
@@ -204,7 +230,7 @@ int prefill_attend(const attn_config_t* cfg, const void* q, const int32_t* cu_se
   pa.N = N;
   pa.max_seqlen = max_seqlen;
   pa.cu_seqlens = cu_seqlens;
-  pa.kv = *kv;
+  pa.kv = load_kv(kv);
   pa.q = q;
   pa.out = out;
   pa.status = status_of(workspace);
@@ -225,8 +251,8 @@ size_t decode_ws_need(const attn_config_t* cfg, int32_t B, int32_t max_cache_len
 // Split-KV decode (and merge); with k_norm_w, the new tokens' K/V are
 // appended inside the split kernel first.
 int decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, const void* k_norm_w,
-                  int32_t B, int32_t max_cache_len, const attn_kv_t* kv, void* out, void* workspace,
-                  cudaStream_t s) {
+                  int32_t B, int32_t max_cache_len, const attn_kv_t* kv, const attn_rope_axes_t* rope,
+                  void* out, void* workspace, cudaStream_t s) {
   int split_len = 0, max_splits = 1;
   decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -234,10 +260,11 @@ int decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_
   DecodeArgs d;
   d.cfg = *cfg;
   d.B = B;
-  d.kv = *kv;
+  d.kv = load_kv(kv);
   d.qkv = qkv;
   d.q_norm_w = q_norm_w;
   d.k_norm_w = k_norm_w;
+  d.axes = rope_axes(rope, cfg->head_dim);
   make_rope_freqs(cfg->rope_theta, cfg->head_dim, &d.freqs);
   d.out = out;
   d.part_o = reinterpret_cast<float*>(ws + kWsHeader);
@@ -282,13 +309,20 @@ int attn_kv_append(const attn_config_t* cfg, const void* qkv, const void* q_norm
                    const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
                    const attn_kv_t* kv, void* workspace, size_t ws_bytes, void* stream) {
   (void)q_norm_w;
+  return attn_kv_append_axes(cfg, qkv, k_norm_w, cu_seqlens, B, N, kv, nullptr, workspace, ws_bytes, stream);
+}
+
+int attn_kv_append_axes(const attn_config_t* cfg, const void* qkv, const void* k_norm_w,
+                        const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
+                        const attn_rope_axes_t* rope, void* workspace, size_t ws_bytes, void* stream) {
   int rc = check_common(cfg, kv, qkv, k_norm_w, k_norm_w);
   if (rc) return rc;
   if (!cu_seqlens || B < 0 || N < 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, N))) return rc;
   if (!ws_ok(workspace, ws_bytes, kWsHeader)) return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (N == 0 || B == 0) return ATTN_OK;
-  return append(cfg, qkv, nullptr, k_norm_w, cu_seqlens, B, N, kv, nullptr, workspace,
+  return append(cfg, qkv, nullptr, k_norm_w, cu_seqlens, B, N, kv, rope, nullptr, workspace,
                 static_cast<cudaStream_t>(stream));
 }
 
@@ -296,14 +330,23 @@ int attn_prefill_prepare(const attn_config_t* cfg, const void* qkv, const void* 
                          const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
                          const attn_kv_t* kv, void* q_out, void* workspace, size_t ws_bytes,
                          void* stream) {
+  return attn_prefill_prepare_axes(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv, nullptr, q_out, workspace,
+                                   ws_bytes, stream);
+}
+
+int attn_prefill_prepare_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                              const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
+                              const attn_kv_t* kv, const attn_rope_axes_t* rope, void* q_out,
+                              void* workspace, size_t ws_bytes, void* stream) {
   int rc = check_common(cfg, kv, qkv, q_norm_w, q_out);
   if (rc) return rc;
   if (!k_norm_w || !aligned16(k_norm_w)) return ATTN_EINVAL;
   if (!cu_seqlens || B < 0 || N < 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, N))) return rc;
   if (!ws_ok(workspace, ws_bytes, kWsHeader)) return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (N == 0 || B == 0) return ATTN_OK;
-  return append(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv, q_out, workspace,
+  return append(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv, rope, q_out, workspace,
                 static_cast<cudaStream_t>(stream));
 }
 
@@ -324,16 +367,25 @@ int attn_prefill(const attn_config_t* cfg, const void* qkv, const void* q_norm_w
                  const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
                  int32_t max_seqlen, const attn_kv_t* kv, void* out, void* workspace,
                  size_t ws_bytes, void* stream) {
+  return attn_prefill_axes(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, max_seqlen, kv, nullptr, out, workspace,
+                           ws_bytes, stream);
+}
+
+int attn_prefill_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                      const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
+                      int32_t max_seqlen, const attn_kv_t* kv, const attn_rope_axes_t* rope, void* out,
+                      void* workspace, size_t ws_bytes, void* stream) {
   int rc = check_common(cfg, kv, qkv, q_norm_w, out);
   if (rc) return rc;
   if (!k_norm_w || !aligned16(k_norm_w)) return ATTN_EINVAL;
   if (!cu_seqlens || B < 0 || N < 0 || max_seqlen < 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, N))) return rc;
   if (!ws_ok(workspace, ws_bytes, kWsHeader + q_stage_bytes(cfg, N))) return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (N == 0 || B == 0) return ATTN_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* q_stage = static_cast<uint8_t*>(workspace) + kWsHeader;
-  if ((rc = append(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv, q_stage, workspace, s)))
+  if ((rc = append(cfg, qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv, rope, q_stage, workspace, s)))
     return rc;
   return prefill_attend(cfg, q_stage, cu_seqlens, B, N, max_seqlen, kv, out, workspace, s);
 }
@@ -341,42 +393,92 @@ int attn_prefill(const attn_config_t* cfg, const void* qkv, const void* q_norm_w
 int attn_decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, int32_t B,
                        int32_t max_cache_len, const attn_kv_t* kv, void* out, void* workspace,
                        size_t ws_bytes, void* stream) {
+  return attn_decode_attend_axes(cfg, qkv, q_norm_w, B, max_cache_len, kv, nullptr, out, workspace, ws_bytes,
+                                 stream);
+}
+
+int attn_decode_attend_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, int32_t B,
+                            int32_t max_cache_len, const attn_kv_t* kv, const attn_rope_axes_t* rope,
+                            void* out, void* workspace, size_t ws_bytes, void* stream) {
   int rc = check_common(cfg, kv, qkv, q_norm_w, out);
   if (rc) return rc;
   if (B < 0 || max_cache_len < 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, B))) return rc;
   int split_len = 0, max_splits = 1;
   if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits)))
     return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (B == 0) return ATTN_OK;
-  return decode_attend(cfg, qkv, q_norm_w, nullptr, B, max_cache_len, kv, out, workspace,
+  return decode_attend(cfg, qkv, q_norm_w, nullptr, B, max_cache_len, kv, rope, out, workspace,
                        static_cast<cudaStream_t>(stream));
 }
 
 int attn_decode(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
                 const void* k_norm_w, int32_t B, int32_t max_cache_len, const attn_kv_t* kv,
                 void* out, void* workspace, size_t ws_bytes, void* stream) {
+  return attn_decode_axes(cfg, qkv, q_norm_w, k_norm_w, B, max_cache_len, kv, nullptr, out, workspace, ws_bytes,
+                          stream);
+}
+
+int attn_decode_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                     const void* k_norm_w, int32_t B, int32_t max_cache_len, const attn_kv_t* kv,
+                     const attn_rope_axes_t* rope, void* out, void* workspace, size_t ws_bytes,
+                     void* stream) {
   int rc = check_common(cfg, kv, qkv, q_norm_w, out);
   if (rc) return rc;
   if (!k_norm_w || !aligned16(k_norm_w)) return ATTN_EINVAL;
   if (B < 0 || max_cache_len < 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, B))) return rc;
   int split_len = 0, max_splits = 1;
   if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits)))
     return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (B == 0) return ATTN_OK;
-  return decode_attend(cfg, qkv, q_norm_w, k_norm_w, B, max_cache_len, kv, out, workspace,
+  return decode_attend(cfg, qkv, q_norm_w, k_norm_w, B, max_cache_len, kv, rope, out, workspace,
                        static_cast<cudaStream_t>(stream));
+}
+
+int attn_kv_gather(const attn_config_t* cfg, const attn_kv_t* kv, const int32_t* cu_seqlens,
+                   const int32_t* start, int32_t B, int32_t N, void* k_out, void* v_out,
+                   void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_common(cfg, kv, k_out, v_out, v_out);
+  if (rc) return rc;
+  if (!cu_seqlens || !start || B < 0 || N < 0) return ATTN_EINVAL;
+  if (!ws_ok(workspace, ws_bytes, kWsHeader)) return ATTN_EWORKSPACE;
+  if ((rc = check_device())) return rc;
+  if (N == 0 || B == 0) return ATTN_OK;
+  GatherArgs a;
+  a.Hkv = cfg->num_kv_heads;
+  a.D = cfg->head_dim;
+  a.cu_seqlens = cu_seqlens;
+  a.B = B;
+  a.N = N;
+  a.kv = load_kv(kv);
+  a.kv.cache_lens = start;  // the kernel's "entries before the range"
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.status = status_of(workspace);
+  return launch_gather(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 int attn_qkv_proj_prepare(const attn_config_t* cfg, const void* hidden, int32_t hidden_size, const void* w_qkv,
                           const void* q_norm_w, const void* k_norm_w, const int32_t* cu_seqlens, int32_t B,
                           int32_t N, const attn_kv_t* kv, void* q_out, void* workspace, size_t ws_bytes,
                           void* stream) {
+  return attn_qkv_proj_prepare_axes(cfg, hidden, hidden_size, w_qkv, q_norm_w, k_norm_w, cu_seqlens, B, N, kv,
+                                    nullptr, q_out, workspace, ws_bytes, stream);
+}
+
+int attn_qkv_proj_prepare_axes(const attn_config_t* cfg, const void* hidden, int32_t hidden_size,
+                               const void* w_qkv, const void* q_norm_w, const void* k_norm_w,
+                               const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
+                               const attn_rope_axes_t* rope, void* q_out, void* workspace, size_t ws_bytes,
+                               void* stream) {
   int rc = check_common(cfg, kv, hidden, q_norm_w, q_out);
   if (rc) return rc;
   if (!w_qkv || !aligned16(w_qkv) || !k_norm_w || !aligned16(k_norm_w)) return ATTN_EINVAL;
   if (!cu_seqlens || B < 0 || N < 0 || hidden_size <= 0 || hidden_size % 8 != 0) return ATTN_EINVAL;
+  if ((rc = check_rope(rope, cfg, N))) return rc;
   if (!ws_ok(workspace, ws_bytes, kWsHeader)) return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (N == 0 || B == 0) return ATTN_OK;
@@ -390,9 +492,10 @@ int attn_qkv_proj_prepare(const attn_config_t* cfg, const void* hidden, int32_t 
   a.cu_seqlens = cu_seqlens;
   a.B = B;
   a.N = N;
-  a.kv = *kv;
+  a.kv = load_kv(kv);
   a.q_out = q_out;
   a.status = status_of(workspace);
+  a.axes = rope_axes(rope, cfg->head_dim);
   make_rope_freqs(cfg->rope_theta, cfg->head_dim, &a.freqs);
   return launch_qkv_proj(a, static_cast<cudaStream_t>(stream));
 }

@@ -31,6 +31,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// What rounding (lo, hi) to the bf16 pair h left of them, as a bf16 pair.
+__device__ __forceinline__ uint32_t bf16_rest(float lo, float hi, uint32_t h) {
+  return pack_bf16(lo - bf16_lo(h), hi - bf16_hi(h));
+}
+
 // ---------------------------------------------------------------- f16 and E4M3
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
@@ -53,6 +58,76 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// ---------------------------------------------------------------- E2M1 with block scales
+// Eight E2M1 codes (nibble i = element i) -> four f16 pairs (elements 2i and
+// 2i + 1).  Exact: every E2M1 value is an f16 value.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& h0, uint32_t& h1, uint32_t& h2, uint32_t& h3) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+      : "r"(w));
+}
+
+// E2M1 codes of eight fp32 values, nibble i = element i: round to nearest
+// even, magnitudes beyond 6 clamped to 6.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+  return r;
+}
+
+// Two E4M3 codes (bits 0-7 and 8-15) -> an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+  return h;
+}
+__device__ __forceinline__ float f16_lo(uint32_t h) { return __half2float(__ushort_as_half((uint16_t)h)); }
+
+// Product of two f16 pairs.  An E2M1 value (2 significant bits) times an E4M3
+// scale (4) needs 6 and lies in [2^-10, 2688]: the product of an entry and its
+// block scale is exact in f16.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Largest magnitude of eight values (NaN if one is NaN).
+__device__ __forceinline__ float amax8(const float (&y)[8]) {
+  float m = fabsf(y[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
+  return m;
+}
+
+// The E4M3 scale (its code) of a block with largest magnitude amax.  The
+// divisions here and in e2m1_codes8 are IEEE divisions: 16-bit inputs meet the
+// rounding boundaries exactly, and a product with a rounded reciprocal would
+// decide those ties by the reciprocal's error.
+__device__ __forceinline__ uint32_t e2m1_block_scale(float amax) { return e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu; }
+
+// Codes of eight values of a block with scale s (the value of its code).
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&y)[8], float s) {
+  if (s == 0.f) return 0u;
+  float z[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = __fdiv_rn(y[e], s);
+  return e2m1x8(z);
 }
 
 // Byte permute: result byte i = byte sel_i of the pair (a = bytes 0-3, b = 4-7).
@@ -246,6 +321,22 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -305,11 +396,38 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], float r) {
   return v;
 }
 
+// Position of every rotation pair of a token: the same one ...
+struct OnePos {
+  float pos;
+  __device__ __forceinline__ float operator()(int) const { return pos; }
+};
+// ... or that of the pair's axis (attn_rope_axes_t): two bits per pair.
+struct RopeAxes {
+  const int32_t* positions;  // [A, ld]; nullptr: no axes
+  int64_t ld;
+  uint32_t axis[4];          // axis of pair i: bits 2 (i % 16), 2 (i % 16) + 1 of word i / 16
+  int32_t num_axes;
+};
+struct AxisPos {
+  const RopeAxes& ax;
+  int64_t token;
+  __device__ __forceinline__ float operator()(int pair) const {
+    const uint32_t a = (ax.axis[pair >> 4] >> (2 * (pair & 15))) & 3u;
+    return (float)__ldg(ax.positions + (int64_t)a * ax.ld + token);
+  }
+};
+// Every position of the token lies in [0, 2^24] (exact in fp32).
+__device__ __forceinline__ bool axes_in_range(const RopeAxes& ax, int64_t token) {
+  bool ok = true;
+  for (int a = 0; a < ax.num_axes; ++a) ok = ok && (uint32_t)__ldg(ax.positions + a * ax.ld + token) <= (1u << 24);
+  return ok;
+}
+
 // cos/sin of the rotation pairs 8 li .. 8 li + 7 (li = lane % (D/16)) at
-// position pos: each lane computes D/64 of the D/2 angles, the lanes that
+// position(s) pos: each lane computes D/64 of the D/2 angles, the lanes that
 // need them read them by shuffle.  All 32 lanes must call this.
-template <int D>
-__device__ __forceinline__ void pair_angles(float pos, const RopeFreqs& fr, int lane, float (&cs)[8],
+template <int D, class Pos>
+__device__ __forceinline__ void pair_angles(const Pos& pos, const RopeFreqs& fr, int lane, float (&cs)[8],
                                             float (&sn)[8]) {
   constexpr int PPL = D / 64;
   const int li = lane % (D / 16);
@@ -317,13 +435,43 @@ __device__ __forceinline__ void pair_angles(float pos, const RopeFreqs& fr, int 
 #pragma unroll
   for (int e = 0; e < PPL; ++e) {
     const int pr = lane * PPL + e;
-    rope_angle(pos, fr.hi[pr], fr.lo[pr], fr, &c_own[e], &s_own[e]);
+    rope_angle(pos(pr), fr.hi[pr], fr.lo[pr], fr, &c_own[e], &s_own[e]);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int pr = li * 8 + e;
     cs[e] = __shfl_sync(0xffffffffu, c_own[e % PPL], pr / PPL);
     sn[e] = __shfl_sync(0xffffffffu, s_own[e % PPL], pr / PPL);
+  }
+}
+
+// E2M1 entries of one head vector in the pair layout, at cache row e (slot *
+// Hkv + head) of the codes and block row sb of the block scales: this lane's
+// 8 values at 8 li (ya) and at D/2 + 8 li (yb) as they are before the division
+// by the tensor's scale (r = its fp32 reciprocal).  A block of 16 sits in two
+// neighbouring lanes; the even one stores its scale.  All 32 lanes must call
+// this; lanes with live == false store nothing.
+template <int D>
+__device__ __forceinline__ void store_e2m1_pair(const float (&xa)[8], const float (&xb)[8], float r, bool live,
+                                                int li, uint8_t* codes, uint8_t* scales) {
+  float ya[8], yb[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    ya[e] = __fmul_rn(xa[e], r);
+    yb[e] = __fmul_rn(xb[e], r);
+  }
+  float ma = amax8(ya), mb = amax8(yb);
+  ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+  mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+  const uint32_t sa = e2m1_block_scale(ma), sb = e2m1_block_scale(mb);
+  const uint32_t ca = e2m1_codes8(ya, f16_lo(e4m3x2_to_f16(sa)));
+  const uint32_t cb = e2m1_codes8(yb, f16_lo(e4m3x2_to_f16(sb)));
+  if (!live) return;
+  *reinterpret_cast<uint32_t*>(codes + 4 * li) = ca;
+  *reinterpret_cast<uint32_t*>(codes + D / 4 + 4 * li) = cb;
+  if ((li & 1) == 0) {
+    scales[li >> 1] = (uint8_t)sa;
+    scales[D / 32 + (li >> 1)] = (uint8_t)sb;
   }
 }
 
@@ -372,11 +520,11 @@ __device__ __forceinline__ void norm_rope_pair(const uint4& raw_a, const uint4& 
 // frag[ks][1].  The four threads of a quad hold the whole row, so the RMSNorm
 // sum is a quad reduction, and RoPE's partner column c + D/2 sits in the same
 // thread at ks + D/32.  All 32 lanes must call this (it shuffles); rows with
-// valid == false yield zeros.
-template <int D>
+// valid == false yield zeros.  Rest: rest holds what the rounding to bf16 left.
+template <int D, bool Rest, class Pos>
 __device__ __forceinline__ void q_row_frags(const uint16_t* row, bool valid, const uint16_t* w,
-                                            float eps, float pos, const RopeFreqs& fr,
-                                            uint32_t (&frag)[D / 16][2]) {
+                                            float eps, const Pos& pos, const RopeFreqs& fr,
+                                            uint32_t (&frag)[D / 16][2], uint32_t (&rest)[D / 16][2]) {
   const int q = threadIdx.x & 3;
   float x[D / 16][4];
   float ss = 0.f;
@@ -409,7 +557,7 @@ __device__ __forceinline__ void q_row_frags(const uint16_t* row, bool valid, con
     for (int j = 0; j < 4; ++j) {
       const int i = 16 * ks + (j >> 1) * 8 + 2 * q + (j & 1);  // rotation pair index < D/2
       float c, s;
-      rope_angle(pos, fr.hi[i], fr.lo[i], fr, &c, &s);
+      rope_angle(pos(i), fr.hi[i], fr.lo[i], fr, &c, &s);
       const float x1 = x[ks][j], x2 = x[ks + D / 32][j];
       x[ks][j] = x1 * c - x2 * s;
       x[ks + D / 32][j] = x2 * c + x1 * s;
@@ -419,6 +567,10 @@ __device__ __forceinline__ void q_row_frags(const uint16_t* row, bool valid, con
   for (int ks = 0; ks < D / 16; ++ks) {
     frag[ks][0] = pack_bf16(x[ks][0], x[ks][1]);
     frag[ks][1] = pack_bf16(x[ks][2], x[ks][3]);
+    if constexpr (Rest) {
+      rest[ks][0] = bf16_rest(x[ks][0], x[ks][1], frag[ks][0]);
+      rest[ks][1] = bf16_rest(x[ks][2], x[ks][3], frag[ks][1]);
+    }
   }
 }
 
@@ -430,9 +582,9 @@ __device__ __forceinline__ void q_row_frags(const uint16_t* row, bool valid, con
 // RMSNorm sum is a quad reduction; the RoPE partner column (D/2 away) sits
 // in quad member c ^ 2.  All 32 lanes must call this; rows with
 // valid == false yield zeros.
-template <int D>
+template <int D, class Pos>
 __device__ __forceinline__ void q_row_frags_quarters(const uint16_t* row, bool valid,
-                                                     const uint16_t* w, float eps, float pos,
+                                                     const uint16_t* w, float eps, const Pos& pos,
                                                      const RopeFreqs& fr,
                                                      uint32_t (&frag)[D / 16][2]) {
   constexpr int Q = D / 4;  // columns per quad member
@@ -469,7 +621,7 @@ __device__ __forceinline__ void q_row_frags_quarters(const uint16_t* row, bool v
   for (int e = 0; e < Q; ++e) {
     const int i = (c & 1) * Q + e;  // rotation pair index < D/2
     float cs, sn;
-    rope_angle(pos, fr.hi[i], fr.lo[i], fr, &cs, &sn);
+    rope_angle(pos(i), fr.hi[i], fr.lo[i], fr, &cs, &sn);
     const float other = __shfl_xor_sync(0xffffffffu, x[e], 2);
     // first half: x_i c - x_{i+D/2} s; second half: x_{i+D/2} c + x_i s
     x[e] = first_half ? x[e] * cs - other * sn : x[e] * cs + other * sn;

@@ -81,10 +81,11 @@ extern "C" int attn_decode_static_scratch(const attn_config_t* cfg, const void* 
   DecodeArgs d;
   d.cfg = *cfg;
   d.B = B;
-  d.kv = *kv;
+  d.kv = load_kv(kv);
   d.qkv = qkv;
   d.q_norm_w = q_norm_w;
   d.k_norm_w = k_norm_w;  // the new K/V are appended inside the split kernel
+  d.axes = RopeAxes{};
   make_rope_freqs(cfg->rope_theta, cfg->head_dim, &d.freqs);
   d.out = out;
   d.part_o = static_cast<float*>(scratch);

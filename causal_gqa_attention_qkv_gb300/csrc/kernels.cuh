@@ -1,6 +1,9 @@
 // Launch interfaces between the C ABI (attn_abi.cu) and the kernels.
 #pragma once
 
+#include <stddef.h>
+#include <string.h>
+
 #include "common.cuh"
 
 namespace gb300 {
@@ -19,6 +22,39 @@ inline KvIndex kv_index(const attn_kv_t& kv) {
   if (kv.page_table)
     while ((1 << x.log2_page) < kv.page_size) ++x.log2_page;
   x.pages_per_req = kv.pages_per_req;
+  return x;
+}
+
+// A caller's attn_kv_t: the fields after v_scale are read for E2M1 caches only.
+inline attn_kv_t load_kv(const attn_kv_t* kv) {
+  attn_kv_t c = {};
+  memcpy(&c, kv, kv->kv_dtype == ATTN_KV_E2M1 ? sizeof(c) : offsetof(attn_kv_t, k_block_scale));
+  return c;
+}
+
+// fp32 reciprocals of the scales of a cache that stores codes (1 for bf16).
+inline float inv_scale(const attn_kv_t& kv, float scale) { return kv.kv_dtype == ATTN_KV_BF16 ? 1.0f : 1.0f / scale; }
+
+// The kernels' form of (checked) rotary axes; rope == NULL: no axes.
+inline RopeAxes rope_axes(const attn_rope_axes_t* rope, int head_dim) {
+  RopeAxes x = {};
+  if (!rope) return x;
+  x.positions = rope->positions;
+  x.ld = rope->ld;
+  x.num_axes = rope->num_axes;
+  int run = 0, left = rope->section[0];
+  for (int i = 0; i < head_dim / 2; ++i) {
+    int a;
+    if (rope->interleaved) {
+      a = i % rope->num_axes;
+      if (i / rope->num_axes >= rope->section[a]) a = 0;
+    } else {
+      while (left == 0) left = rope->section[++run];
+      a = run;
+      --left;
+    }
+    x.axis[i >> 4] |= (uint32_t)a << (2 * (i & 15));
+  }
   return x;
 }
 
@@ -59,11 +95,24 @@ struct PrologueArgs {
   attn_kv_t kv;
   int32_t* status;
   RopeFreqs freqs;
+  RopeAxes axes;  // positions == NULL: c_b + j
 };
 cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream);
 
-// Tensor maps over the K and V cache pools, [num_slots, Hkv, D] bf16, 128-byte
-// swizzled boxes of 64 (d) x 1 (head) x box_rows (slots).
+// Cached entries read back as bf16 (include/attn.h, attn_kv_gather).
+struct GatherArgs {
+  int32_t Hkv, D;
+  const int32_t* cu_seqlens;
+  int32_t B, N;
+  attn_kv_t kv;  // cache_lens: the first position of each request
+  void* k_out;
+  void* v_out;
+  int32_t* status;
+};
+cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream);
+
+// Tensor maps over the K and V cache pools, [num_slots, Hkv, D]: boxes of
+// 1 head x box_rows slots x 64 bf16 or a whole row of codes (see make_cache_maps).
 struct CacheMaps {
   CUtensorMap k;
   CUtensorMap v;
@@ -85,6 +134,7 @@ struct DecodeArgs {
   const void* q_norm_w;  // [D] bf16
   const void* k_norm_w;  // [D] bf16: append the new K/V inside the kernel; NULL: already in the cache
   RopeFreqs freqs;
+  RopeAxes axes;  // positions == NULL: c_b + j
   void* out;      // [B, Hq*D] bf16
   float* part_o;  // [B, Hq, max_splits, D] fp32
   float* part_ml; // [B, Hq, max_splits, 2] fp32 (running max in log2 units, sum)
@@ -132,6 +182,7 @@ struct QkvProjArgs {
   void* q_out;
   int32_t* status;
   RopeFreqs freqs;
+  RopeAxes axes;  // positions == NULL: c_b + j
 };
 int launch_qkv_proj(const QkvProjArgs& a, cudaStream_t stream);
 

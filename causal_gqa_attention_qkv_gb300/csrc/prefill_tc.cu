@@ -45,8 +45,14 @@
 // f16 value); Q arrives in f16, P is packed to f16, the products run as
 // kind::f16 with f16 operands, and the cache scales multiply the scores
 // (k_scale) and the output (v_scale).
+//
+// E2M1 caches take the same path with tiles of 128 x D / 2 bytes of codes: the
+// converting lanes fetch the block scales of their key rows into registers and
+// store code * block scale as f16 (exact).
 #include "kernels.cuh"
 #include "tcgen05.cuh"
+
+#include <type_traits>
 
 namespace gb300 {
 
@@ -78,11 +84,21 @@ struct TcPar {
   int32_t* status;
   int32_t* work;  // [0]: next item to claim, [1]: CTAs finished
   uint16_t* out;
-  float scale_log2;  // log2(e) / sqrt(D), times k_scale for an E4M3 cache
-  float v_scale;     // 1, or v_scale for an E4M3 cache
+  float scale_log2;  // log2(e) / sqrt(D), times k_scale for a cache of codes
+  float v_scale;     // 1, or v_scale for a cache of codes
   int32_t Hq, Hkv, log2G, log2BT, N, B, max_seqlen;
   int32_t num_vitems;  // rounds x B x Hkv, rounds = ceil(max_seqlen / (2 x 128/G))
 };
+
+// What the kernel over an E2M1 cache takes besides.  The others do not: 16 more
+// bytes of parameters cost the bf16 kernel 5 % (189 against 181 us for the
+// Qwen3-4B prefill) by another register allocation.
+struct TcParE2m1 : TcPar {
+  const uint8_t* k_block_scale;  // [Hkv, num_slots, D / 16]
+  const uint8_t* v_block_scale;
+};
+template <int KV>
+using TcParOf = std::conditional_t<KV == ATTN_KV_E2M1, TcParE2m1, TcPar>;
 
 template <int D>
 struct TcLayout {
@@ -323,14 +339,15 @@ __device__ void produce_kv(const TcPar& p, const SeqInfo* seq_tab, const int* ri
 // The same ring for an E4M3 cache, run by the whole warp: lane 0 copies each
 // tile of codes (128 keys x D bytes) into the last 128 x D bytes of its stage;
 // then every lane converts key rows to the f16 tile layout and lane 0
-// releases the stage to the tensor cores.
-template <int D>
-__device__ void produce_kv_f8(const TcPar& p, const SeqInfo* seq_tab, const int* ring,
-                              const CUtensorMap* map, uint8_t* smem, uint64_t* bars, int base,
-                              int full0, int empty0, int land0, int stages, bool& ok) {
+// releases the stage to the tensor cores.  F4: an E2M1 cache (128 keys x D / 2
+// bytes a tile) whose block scales are at bscale.
+template <int D, bool F4>
+__device__ void produce_kv_codes(const TcPar& p, const SeqInfo* seq_tab, const int* ring,
+                                 const CUtensorMap* map, const uint8_t* bscale, uint8_t* smem, uint64_t* bars,
+                                 int base, int full0, int empty0, int land0, int stages, bool& ok) {
   using Lay = TcLayout<D>;
   const int lane = threadIdx.x & 31;
-  constexpr int kCodeBytes = kKeys * D;
+  constexpr int kCodeBytes = kKeys * (F4 ? D / 2 : D);
   if (lane == 0) prefetch_tmap(map);
   ItemWalk w;
   w.start(p, seq_tab, ring, bars, true, ok);
@@ -345,7 +362,31 @@ __device__ void produce_kv_f8(const TcPar& p, const SeqInfo* seq_tab, const int*
       uint8_t* dst = smem + base + st * Lay::kTile;
       uint8_t* land = dst + Lay::kTile - kCodeBytes;  // 1024-aligned
       uint64_t* bar = &bars[land0 + st];
-      if (lane == 0) {
+      uint32_t bs[4][D / 64];  // E2M1: block scales of this lane's four key rows
+      if constexpr (F4) {
+        const int row0 = kv_row(p, w.it, j * kKeys);
+        const int row1 = p.half_boxes ? kv_row(p, w.it, min(j * kKeys + 64, ((w.it.kv_total - 1) >> 6) << 6)) : row0 + 64;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, kCodeBytes);
+          tma_load_3d(land, map, bar, 0, w.it.kh, row0);
+          if (p.half_boxes) tma_load_3d(land + kCodeBytes / 2, map, bar, 0, w.it.kh, row1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t slot = (int64_t)(i < 2 ? row0 : row1) + lane + 32 * (i & 1);
+          const uint8_t* src = bscale + ((int64_t)w.it.kh * p.kv.num_slots + slot) * (D / 16);
+          if (slot >= p.kv.num_slots) {  // past the cache, as TMA fills it
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) bs[i][e] = 0u;
+          } else if constexpr (D == 128) {
+            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(src));
+            bs[i][0] = v.x;
+            bs[i][1] = v.y;
+          } else {
+            bs[i][0] = __ldcg(reinterpret_cast<const uint32_t*>(src));
+          }
+        }
+      } else if (lane == 0) {
         mbar_arrive_expect_tx(bar, kCodeBytes);
         if (!p.half_boxes) {
           tma_load_3d(land, map, bar, 0, w.it.kh, kv_row(p, w.it, j * kKeys));
@@ -362,6 +403,36 @@ __device__ void produce_kv_f8(const TcPar& p, const SeqInfo* seq_tab, const int*
       // 64-column region.  Each row is read whole before any lane writes:
       // for D = 64 later f16 rows cover other lanes' code rows.
       const uint32_t tile = smem_u32(dst), codes = smem_u32(land);
+      if constexpr (F4) {
+        // rows of D / 2 bytes (64-byte swizzled when D = 128); 16 bytes are two blocks
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i) {
+          const uint32_t r = (uint32_t)(lane + 32 * i);
+          uint4 c[D / 32];
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch)
+            c[ch] = lds128(codes + r * (D / 2) + (D == 128 ? (ch ^ ((r >> 1) & 3u)) << 4 : ch << 4));
+          __syncwarp();
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            const uint32_t s2 = e4m3x2_to_f16(bs[i][ch >> 1] >> (16 * (ch & 1)));
+            const uint32_t words[4] = {c[ch].x, c[ch].y, c[ch].z, c[ch].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t sc = prmt(s2, s2, q < 2 ? 0x1010u : 0x3232u);
+              uint4 h;
+              e2m1x8_to_f16(words[q], h.x, h.y, h.z, h.w);
+              h.x = mul_f16x2(h.x, sc);
+              h.y = mul_f16x2(h.y, sc);
+              h.z = mul_f16x2(h.z, sc);
+              h.w = mul_f16x2(h.w, sc);
+              const uint32_t ck = 4 * ch + q;  // 16-byte chunk (8 columns) of the f16 row
+              sts128(tile + (ck >> 3) * kRegionBytes + sw128(r, ck & 7), h);
+            }
+          }
+          __syncwarp();
+        }
+      } else
 #pragma unroll 1
       for (int i = 0; i < kKeys / 32; ++i) {
         const uint32_t r = (uint32_t)(lane + 32 * i);
@@ -759,13 +830,14 @@ __device__ void softmax_tile(const TcPar& p, const SeqInfo* seq_tab, const int* 
   if ((threadIdx.x & 31) == 0) bulk_wait_all();  // every output store has completed
 }
 
-template <int D, bool F8>
+template <int D, int KV>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ CUtensorMap omap, const TcPar p) {
+                      const __grid_constant__ CUtensorMap omap, const TcParOf<KV> p) {
   using Lay = TcLayout<D>;
+  constexpr bool F8 = KV != ATTN_KV_BF16;  // a cache of codes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
@@ -822,10 +894,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 8) {
     softmax_tile<D, F8>(p, seq_tab, ring, sbase, tmem, bars, &omap, warp >> 2, ok);
-  } else if (F8 && warp == kKWarp) {  // the whole warp converts the tiles
-    produce_kv_f8<D>(p, seq_tab, ring, &kmap, smem, bars, Lay::kK, kKFull0, kKEmpty0, kKLand0, kKStages, ok);
-  } else if (F8 && warp == kVWarp) {
-    produce_kv_f8<D>(p, seq_tab, ring, &vmap, smem, bars, Lay::kV, kVFull0, kVEmpty0, kVLand0, kVStages, ok);
+  } else if (F8 && (warp == kKWarp || warp == kVWarp)) {  // the whole warp converts the tiles
+    constexpr bool F4 = KV == ATTN_KV_E2M1;
+    const uint8_t *kbs = nullptr, *vbs = nullptr;
+    if constexpr (F4) {
+      kbs = p.k_block_scale;
+      vbs = p.v_block_scale;
+    }
+    if (warp == kKWarp)
+      produce_kv_codes<D, F4>(p, seq_tab, ring, &kmap, kbs, smem, bars, Lay::kK, kKFull0, kKEmpty0, kKLand0, kKStages, ok);
+    else
+      produce_kv_codes<D, F4>(p, seq_tab, ring, &vmap, vbs, smem, bars, Lay::kV, kVFull0, kVEmpty0, kVLand0, kVStages, ok);
   } else {
     if (lane == 0) {
       if (warp == kKWarp)
@@ -855,9 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool F8>
+template <int D, int KV>
 int launch_prefill_tc_t(const PrefillArgs& a, cudaStream_t stream) {
   using Lay = TcLayout<D>;
+  constexpr bool F8 = KV != ATTN_KV_BF16;
   const int Hq = a.cfg.num_q_heads, Hkv = a.cfg.num_kv_heads;
   const int G = Hq / Hkv;
   const int log2G = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
@@ -870,13 +950,17 @@ int launch_prefill_tc_t(const PrefillArgs& a, cudaStream_t stream) {
   if (make_qkv_map(a.q, a.N, Hq, D, G, BT, &qmap) != 0) return ATTN_ELAUNCH;
   CUtensorMap omap;  // out viewed as [N, Hq, D]; one softmax warp's 32 rows per box
   if (make_qkv_map(a.out, a.N, Hq, D, G, 32 / G, &omap) != 0) return ATTN_ELAUNCH;
-  TcPar p;
+  TcParOf<KV> p;
   p.cu_seqlens = a.cu_seqlens;
   p.kv = kvi;
   p.half_boxes = half_boxes ? 1 : 0;
   p.status = a.status;
   p.work = a.work;
   p.out = static_cast<uint16_t*>(a.out);
+  if constexpr (KV == ATTN_KV_E2M1) {
+    p.k_block_scale = static_cast<const uint8_t*>(a.kv.k_block_scale);
+    p.v_block_scale = static_cast<const uint8_t*>(a.kv.v_block_scale);
+  }
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)D) * (F8 ? a.kv.k_scale : 1.0f);
   p.v_scale = F8 ? a.kv.v_scale : 1.0f;
   p.Hq = Hq;
@@ -894,11 +978,11 @@ int launch_prefill_tc_t(const PrefillArgs& a, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ATTN_ELAUNCH;
-  if (cudaFuncSetAttribute(prefill_tc_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(prefill_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Lay::kSmemBytes) != cudaSuccess)
     return ATTN_ELAUNCH;
   const int grid = (int)std::min<int64_t>(sms, nv);
-  return launch_dependent(prefill_tc_kernel<D, F8>, dim3(grid), dim3(kThreads), Lay::kSmemBytes, stream, qmap,
+  return launch_dependent(prefill_tc_kernel<D, KV>, dim3(grid), dim3(kThreads), Lay::kSmemBytes, stream, qmap,
                           maps.k, maps.v, omap, p) == cudaSuccess
              ? ATTN_OK
              : ATTN_ELAUNCH;
@@ -908,10 +992,15 @@ int launch_prefill_tc_t(const PrefillArgs& a, cudaStream_t stream) {
 
 int launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   if (a.B <= 0 || a.N <= 0 || a.max_seqlen <= 0) return ATTN_OK;
-  const bool f8 = a.kv.kv_dtype == ATTN_KV_E4M3;
-  if (a.cfg.head_dim == 128)
-    return f8 ? launch_prefill_tc_t<128, true>(a, stream) : launch_prefill_tc_t<128, false>(a, stream);
-  return f8 ? launch_prefill_tc_t<64, true>(a, stream) : launch_prefill_tc_t<64, false>(a, stream);
+  const bool wide = a.cfg.head_dim == 128;
+  switch (a.kv.kv_dtype) {
+    case ATTN_KV_E4M3:
+      return wide ? launch_prefill_tc_t<128, ATTN_KV_E4M3>(a, stream) : launch_prefill_tc_t<64, ATTN_KV_E4M3>(a, stream);
+    case ATTN_KV_E2M1:
+      return wide ? launch_prefill_tc_t<128, ATTN_KV_E2M1>(a, stream) : launch_prefill_tc_t<64, ATTN_KV_E2M1>(a, stream);
+    default:
+      return wide ? launch_prefill_tc_t<128, ATTN_KV_BF16>(a, stream) : launch_prefill_tc_t<64, ATTN_KV_BF16>(a, stream);
+  }
 }
 
 }  // namespace gb300

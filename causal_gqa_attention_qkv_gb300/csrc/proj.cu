@@ -59,15 +59,18 @@ struct ProjPar {
   // qkv epilogue
   const uint16_t* q_norm_w;     // [D] bf16
   const uint16_t* k_norm_w;
-  uint16_t* q_out;              // [M, Hq, D] bf16 (f16 next to an E4M3 cache)
+  uint16_t* q_out;              // [M, Hq, D] bf16 (f16 next to a cache of codes)
   void* k_cache;
   void* v_cache;
-  float inv_k, inv_v;           // E4M3: fp32(1 / scale)
+  uint8_t* k_block_scale;       // E2M1: [Hkv, num_slots, D / 16]
+  uint8_t* v_block_scale;
+  float inv_k, inv_v;           // E4M3, E2M1: fp32(1 / scale)
   KvIndex kv;
   const int32_t* cu_seqlens;    // [B + 1]
   int32_t B, Hq, Hkv;
   float eps;
   RopeFreqs freqs;
+  RopeAxes axes;
 };
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
@@ -245,13 +248,36 @@ __device__ __forceinline__ void store_e4m3x32(uint8_t* dst, const float (&y)[32]
   }
 }
 
+// E2M1 entries of 32 consecutive values of a head vector (two blocks), as they
+// are before the product with r, and their block scales.
+__device__ __forceinline__ void store_e2m1x32(uint8_t* codes, uint8_t* scales, const float (&x)[32], float r) {
+  uint32_t w[4], s2 = 0;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    float y0[8], y1[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y0[e] = __fmul_rn(x[16 * b + e], r);
+      y1[e] = __fmul_rn(x[16 * b + 8 + e], r);
+    }
+    const uint32_t sc = e2m1_block_scale(max_nan(amax8(y0), amax8(y1)));
+    const float s = f16_lo(e4m3x2_to_f16(sc));
+    w[2 * b] = e2m1_codes8(y0, s);
+    w[2 * b + 1] = e2m1_codes8(y1, s);
+    s2 |= sc << (8 * b);
+  }
+  *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint16_t*>(scales) = (uint16_t)s2;
+}
+
 // The step's prologue on this thread's row of the accumulator: for each head
 // (D columns) of the tile, Q and K heads are RMS-normalised with their weight
 // and rotated at the token's position (pairs (i, i + D/2)); Q goes to q_out,
 // K and V to the cache slot of the token.  The accumulators are used as they
 // are (fp32, never rounded to bf16 before the norm).
-template <int D, bool F8>
+template <int D, int KV, bool Axes>
 __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const float* qw, const float* kw) {
+  constexpr bool F8 = KV == ATTN_KV_E4M3, F4 = KV == ATTN_KV_E2M1;
   // token facts: 0 = no row, 1 = Q only (cache region too small), 2 = Q and cache
   int ok = 0;
   int64_t slot = 0;
@@ -272,6 +298,10 @@ __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const
       slot = r.valid ? cache_slot(p.kv, r, r.cached + j) : -1;
       if (slot >= 0) ok = 2;
       else if (n0 == 0) set_status(p.status, ATTN_STATUS_CAPACITY);
+      if (p.axes.positions && !axes_in_range(p.axes, row)) {
+        ok = 0;
+        if (n0 == 0) set_status(p.status, ATTN_STATUS_POSITION);
+      }
     } else if (n0 == 0) {
       set_status(p.status, ATTN_STATUS_SEQLENS);
     }
@@ -294,6 +324,10 @@ __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const
 #pragma unroll
         for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
         if (F8) store_e4m3x32(static_cast<uint8_t*>(p.v_cache) + e0, y, p.inv_v);
+        else if (F4)
+          store_e2m1x32(static_cast<uint8_t*>(p.v_cache) + e0 / 2,
+                        p.v_block_scale + ((int64_t)(hd - p.Hq - p.Hkv) * p.kv.num_slots + slot) * (D / 16) + 2 * c, y,
+                        p.inv_v);
         else store_half32<false>(static_cast<uint16_t*>(p.v_cache) + e0, y);
       }
       continue;
@@ -325,27 +359,36 @@ __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const
       tc::ld_32x32b_x32(hcol + D / 2 + 32 * c, r2);
       tc::wait_ld();
       float y1[32], y2[32];
+      auto rotate = [&](const auto& at) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int pi = 32 * c + i;  // pair index < D/2
-        float cs, sn;
-        rope_angle(pos, p.freqs.hi[pi], p.freqs.lo[pi], p.freqs, &cs, &sn);
-        const float a = w[pi] * (__uint_as_float(r1[i]) * inv);
-        const float b = w[pi + D / 2] * (__uint_as_float(r2[i]) * inv);
-        y1[i] = fmaf(-b, sn, a * cs);
-        y2[i] = fmaf(a, sn, b * cs);
-      }
+        for (int i = 0; i < 32; ++i) {
+          const int pi = 32 * c + i;  // pair index < D/2
+          float cs, sn;
+          rope_angle(at(pi), p.freqs.hi[pi], p.freqs.lo[pi], p.freqs, &cs, &sn);
+          const float a = w[pi] * (__uint_as_float(r1[i]) * inv);
+          const float b = w[pi + D / 2] * (__uint_as_float(r2[i]) * inv);
+          y1[i] = fmaf(-b, sn, a * cs);
+          y2[i] = fmaf(a, sn, b * cs);
+        }
+      };
+      if (Axes) rotate(AxisPos{p.axes, ok != 0 ? row : 0});
+      else rotate(OnePos{pos});
       if (is_q) {
         if (ok == 0) continue;
         uint16_t* dst = p.q_out + ((int64_t)row * p.Hq + hd) * D + 32 * c;
-        store_half32<F8>(dst, y1);
-        store_half32<F8>(dst + D / 2, y2);
+        store_half32<F8 || F4>(dst, y1);
+        store_half32<F8 || F4>(dst + D / 2, y2);
       } else {
         if (ok != 2) continue;
         const int64_t e0 = (slot * p.Hkv + (hd - p.Hq)) * D + 32 * c;
         if (F8) {
           store_e4m3x32(static_cast<uint8_t*>(p.k_cache) + e0, y1, p.inv_k);
           store_e4m3x32(static_cast<uint8_t*>(p.k_cache) + e0 + D / 2, y2, p.inv_k);
+        } else if (F4) {
+          uint8_t* codes = static_cast<uint8_t*>(p.k_cache) + e0 / 2;
+          uint8_t* scales = p.k_block_scale + ((int64_t)(hd - p.Hq) * p.kv.num_slots + slot) * (D / 16) + 2 * c;
+          store_e2m1x32(codes, scales, y1, p.inv_k);
+          store_e2m1x32(codes + D / 4, scales + D / 32, y2, p.inv_k);
         } else {
           store_half32<false>(static_cast<uint16_t*>(p.k_cache) + e0, y1);
           store_half32<false>(static_cast<uint16_t*>(p.k_cache) + e0 + D / 2, y2);
@@ -355,7 +398,7 @@ __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const
   }
 }
 
-template <int Epi, int D, bool F8>
+template <int Epi, int D, int KV, bool Axes>
 __device__ void proj_epilogue(const ProjPar& p, uint32_t tmem, uint64_t* bars, const float* qw, const float* kw,
                               bool& ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -372,14 +415,14 @@ __device__ void proj_epilogue(const ProjPar& p, uint32_t tmem, uint64_t* bars, c
     const int row = m0 + 32 * lane_grp + lane;
     const uint32_t taddr = tmem + ((uint32_t)(32 * lane_grp) << 16) + (uint32_t)buf * kBN;
     if (Epi == kEpiPlain) epi_plain(p, row, n0, taddr);
-    else epi_qkv<D, F8>(p, row, n0, taddr, qw, kw);
+    else epi_qkv<D, KV, Axes>(p, row, n0, taddr, qw, kw);
     tc::fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kAccEmpty + buf]);
   }
 }
 
-template <int Epi, int D, bool F8>
+template <int Epi, int D, int KV, bool Axes>
 __global__ void __cluster_dims__(kPair, 1, 1) __launch_bounds__(kThreads, 1)
     proj_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                      const ProjPar p) {
@@ -425,7 +468,7 @@ __global__ void __cluster_dims__(kPair, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) proj_mma(p, smem_u32(smem), tmem, bars, ok);
   } else {
-    proj_epilogue<Epi, D, F8>(p, tmem, bars, qw, kw, ok);
+    proj_epilogue<Epi, D, KV, Axes>(p, tmem, bars, qw, kw, ok);
   }
   if (!ok) set_status(p.status, ATTN_STATUS_TIMEOUT);
   tc::fence_before();
@@ -437,7 +480,7 @@ __global__ void __cluster_dims__(kPair, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::dealloc(tmem, kTmemCols);
 }
 
-template <int Epi, int D, bool F8>
+template <int Epi, int D, int KV, bool Axes>
 int launch_proj_t(const ProjPar& p0, const void* a, const void* b, cudaStream_t stream) {
   ProjPar p = p0;
   CUtensorMap amap, bmap;
@@ -452,7 +495,7 @@ int launch_proj_t(const ProjPar& p0, const void* a, const void* b, cudaStream_t 
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ATTN_ELAUNCH;
-  if (cudaFuncSetAttribute(proj_gemm_kernel<Epi, D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(proj_gemm_kernel<Epi, D, KV, Axes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemBytes) != cudaSuccess)
     return ATTN_ELAUNCH;
   // as many clusters as can be resident at once (pairs must share a GPC,
@@ -465,13 +508,22 @@ int launch_proj_t(const ProjPar& p0, const void* a, const void* b, cudaStream_t 
     qc.blockDim = dim3(kThreads);
     qc.dynamicSmemBytes = kSmemBytes;
     int active = 0;
-    if (cudaOccupancyMaxActiveClusters(&active, proj_gemm_kernel<Epi, D, F8>, &qc) != cudaSuccess || active <= 0)
+    if (cudaOccupancyMaxActiveClusters(&active, proj_gemm_kernel<Epi, D, KV, Axes>, &qc) != cudaSuccess || active <= 0)
       return ATTN_ELAUNCH;
     clusters = std::min(clusters, active);
   }
   const int grid = (int)std::min<int64_t>(clusters, tiles) * kPair;
-  proj_gemm_kernel<Epi, D, F8><<<grid, kThreads, kSmemBytes, stream>>>(amap, bmap, p);
+  proj_gemm_kernel<Epi, D, KV, Axes><<<grid, kThreads, kSmemBytes, stream>>>(amap, bmap, p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
+}
+
+template <int D, bool Axes>
+int launch_qkv_t(const ProjPar& p, const QkvProjArgs& a, cudaStream_t stream) {
+  switch (a.kv.kv_dtype) {
+    case ATTN_KV_E4M3: return launch_proj_t<kEpiQkv, D, ATTN_KV_E4M3, Axes>(p, a.hidden, a.w_qkv, stream);
+    case ATTN_KV_E2M1: return launch_proj_t<kEpiQkv, D, ATTN_KV_E2M1, Axes>(p, a.hidden, a.w_qkv, stream);
+    default: return launch_proj_t<kEpiQkv, D, ATTN_KV_BF16, Axes>(p, a.hidden, a.w_qkv, stream);
+  }
 }
 
 }  // namespace
@@ -485,7 +537,7 @@ int launch_linear(const void* x, const void* w, void* y, int32_t M, int32_t N, i
   p.K = K;
   p.out = static_cast<uint16_t*>(y);
   p.status = status;
-  return launch_proj_t<kEpiPlain, 128, false>(p, x, w, stream);
+  return launch_proj_t<kEpiPlain, 128, ATTN_KV_BF16, false>(p, x, w, stream);
 }
 
 int launch_qkv_proj(const QkvProjArgs& a, cudaStream_t stream) {
@@ -501,9 +553,10 @@ int launch_qkv_proj(const QkvProjArgs& a, cudaStream_t stream) {
   p.q_out = static_cast<uint16_t*>(a.q_out);
   p.k_cache = a.kv.k_cache;
   p.v_cache = a.kv.v_cache;
-  const bool f8 = a.kv.kv_dtype == ATTN_KV_E4M3;
-  p.inv_k = f8 ? 1.0f / a.kv.k_scale : 1.0f;
-  p.inv_v = f8 ? 1.0f / a.kv.v_scale : 1.0f;
+  p.k_block_scale = static_cast<uint8_t*>(a.kv.k_block_scale);
+  p.v_block_scale = static_cast<uint8_t*>(a.kv.v_block_scale);
+  p.inv_k = inv_scale(a.kv, a.kv.k_scale);
+  p.inv_v = inv_scale(a.kv, a.kv.v_scale);
   p.kv = kv_index(a.kv);
   p.cu_seqlens = a.cu_seqlens;
   p.B = a.B;
@@ -511,11 +564,10 @@ int launch_qkv_proj(const QkvProjArgs& a, cudaStream_t stream) {
   p.Hkv = a.cfg.num_kv_heads;
   p.eps = a.cfg.rms_eps;
   p.freqs = a.freqs;
-  if (D == 128)
-    return f8 ? launch_proj_t<kEpiQkv, 128, true>(p, a.hidden, a.w_qkv, stream)
-              : launch_proj_t<kEpiQkv, 128, false>(p, a.hidden, a.w_qkv, stream);
-  return f8 ? launch_proj_t<kEpiQkv, 64, true>(p, a.hidden, a.w_qkv, stream)
-            : launch_proj_t<kEpiQkv, 64, false>(p, a.hidden, a.w_qkv, stream);
+  p.axes = a.axes;
+  const bool axes = a.axes.positions != nullptr;
+  if (D == 128) return axes ? launch_qkv_t<128, true>(p, a, stream) : launch_qkv_t<128, false>(p, a, stream);
+  return axes ? launch_qkv_t<64, true>(p, a, stream) : launch_qkv_t<64, false>(p, a, stream);
 }
 
 }  // namespace gb300

@@ -37,15 +37,18 @@ struct ProloguePar {
   const uint16_t* __restrict__ k_norm_w;   // [D] bf16
   uint16_t* __restrict__ q_out;            // [N, Hq, D] bf16 or NULL
   const int32_t* cu_seqlens;  // [B+1] or NULL: token b is request b (decode)
-  void* __restrict__ k_cache;  // bf16, or E4M3 codes (one byte per entry)
+  void* __restrict__ k_cache;  // bf16, or codes (E4M3: one byte per entry, E2M1: half a byte)
   void* __restrict__ v_cache;
-  float inv_k, inv_v;          // E4M3: fp32(1 / scale), rounded on the host
+  uint8_t* __restrict__ k_block_scale;  // E2M1: [Hkv, num_slots, D/16]
+  uint8_t* __restrict__ v_block_scale;
+  float inv_k, inv_v;          // E4M3, E2M1: fp32(1 / scale), rounded on the host
   KvIndex kv;
   int32_t* status;
   int32_t B, N, Hq, Hkv;
   int64_t steps_per_warp;  // each warp takes this many consecutive (token, step) units
   float eps;
   RopeFreqs freqs;
+  RopeAxes axes;
 };
 
 // One warp per token.  A head vector (D bf16) is held by L = D/16 lanes, lane
@@ -55,14 +58,15 @@ struct ProloguePar {
 // HPI = 32 / L head vectors are taken per step; each load instruction reads
 // HPI runs of 128 contiguous bytes and each store writes whole runs.  cos/sin
 // of the token's D/2 rotation angles are computed once (D/64 per lane) and
-// handed to the lanes that need them with shuffles.  F8: the cache holds E4M3
-// codes.
-template <int D, bool F8>
+// handed to the lanes that need them with shuffles.  KV: the cache's element
+// type (ATTN_KV_*).
+template <int D, int KV>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const ProloguePar p) {
   constexpr int L = D / 16;     // lanes per head vector
   constexpr int HPI = 32 / L;   // head vectors per warp-wide step
   constexpr int H2 = D / 2;     // offset of the second member of a rotation pair
-  constexpr int kBatch = F8 ? kBatchF8 : kBatchBf16;
+  constexpr bool F8 = KV == ATTN_KV_E4M3, F4 = KV == ATTN_KV_E2M1;
+  constexpr int kBatch = KV != ATTN_KV_BF16 ? kBatchF8 : kBatchBf16;
   const int lane = threadIdx.x & 31;
   launch_dependents();  // the attention kernel after this one may be scheduled as CTAs finish
 
@@ -138,11 +142,17 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           set_status(p.status, ATTN_STATUS_CAPACITY);
       }
     }
+    const bool with_axes = p.axes.positions != nullptr;  // kernel-uniform
+    if (with_axes && ok != 0 && !axes_in_range(p.axes, t)) {
+      ok = 0;
+      if (lane == 0) set_status(p.status, ATTN_STATUS_POSITION);
+    }
     if (ok != 0) {  // warp-uniform
 
       // cos/sin of the 8 rotation pairs 8*li .. 8*li + 7 this lane's values belong to
       float cs[8], sn[8];
-      pair_angles<D>(pos, p.freqs, lane, cs, sn);
+      if (with_axes) pair_angles<D>(AxisPos{p.axes, t}, p.freqs, lane, cs, sn);
+      else pair_angles<D>(OnePos{pos}, p.freqs, lane, cs, sn);
       uint16_t* q_row = with_q ? p.q_out + (int64_t)t * p.Hq * D + li * 8 : nullptr;
       const int64_t cache_row = slot * p.Hkv * D + li * 8;
 
@@ -166,6 +176,16 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           const bool is_v = hd >= p.Hq + p.Hkv;
           // steps made only of V heads: bit copies into the cache
           const bool step_all_v = hd0 + (base + k) * HPI >= p.Hq + p.Hkv;
+          if (F4 && step_all_v) {
+            const int kvh = live ? hd - p.Hq - p.Hkv : 0;
+            float xa[8], xb[8];
+            unpack_bf16x8(raw_a[k], xa);
+            unpack_bf16x8(raw_b[k], xb);
+            store_e2m1_pair<D>(xa, xb, p.inv_v, live && ok == 2, li,
+                               static_cast<uint8_t*>(p.v_cache) + (slot * p.Hkv + kvh) * (D / 2),
+                               p.v_block_scale + (kvh * p.kv.num_slots + slot) * (D / 16));
+            continue;
+          }
           if (step_all_v) {
             if (live && ok == 2) {
               const int64_t e0 = cache_row + (int64_t)(hd - p.Hq - p.Hkv) * D;
@@ -186,6 +206,28 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           }
           float ra[8], rb[8];
           norm_rope_pair<D>(raw_a[k], raw_b[k], is_q ? qw[0] : kw[0], is_q ? qw[1] : kw[1], cs, sn, p.eps, ra, rb);
+          if constexpr (F4) {  // K heads, and V heads in a step that they share (all lanes: it shuffles)
+            const int first = hd0 + (base + k) * HPI;  // step-uniform
+            if (first + HPI > p.Hq) {
+              const int kvh = live ? hd - (is_v ? p.Hq + p.Hkv : p.Hq) : 0;
+              const int64_t at = kvh > 0 ? kvh : 0;
+              float xa[8], xb[8];
+              if (is_v) {
+                unpack_bf16x8(raw_a[k], xa);
+                unpack_bf16x8(raw_b[k], xb);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  xa[e] = ra[e];
+                  xb[e] = rb[e];
+                }
+              }
+              store_e2m1_pair<D>(xa, xb, is_v ? p.inv_v : p.inv_k, live && !is_q && ok == 2, li,
+                                 static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + (slot * p.Hkv + at) * (D / 2),
+                                 (is_v ? p.v_block_scale : p.k_block_scale) + (at * p.kv.num_slots + slot) * (D / 16));
+            }
+            if (!is_q) continue;
+          }
           if (!live) continue;
           const int64_t e0 = cache_row + (int64_t)(hd - (is_v ? p.Hq + p.Hkv : p.Hq)) * D;
           if (F8 && !is_q) {
@@ -202,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
             }
             continue;
           }
-          // the prepared Q is f16 next to an E4M3 cache (the prefill kernel's operand type), else bf16
+          // the prepared Q is f16 next to a cache of codes (the prefill kernel's operand type), else bf16
           uint4 va, vb;
           if (is_v) {
             va = raw_a[k];
             vb = raw_b[k];
-          } else if (F8) {
+          } else if (F8 || F4) {
             va = make_uint4(pack_f16(ra[0], ra[1]), pack_f16(ra[2], ra[3]), pack_f16(ra[4], ra[5]), pack_f16(ra[6], ra[7]));
             vb = make_uint4(pack_f16(rb[0], rb[1]), pack_f16(rb[2], rb[3]), pack_f16(rb[4], rb[5]), pack_f16(rb[6], rb[7]));
           } else {
@@ -244,9 +286,10 @@ cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream) {
   p.cu_seqlens = a.cu_seqlens;
   p.k_cache = a.kv.k_cache;
   p.v_cache = a.kv.v_cache;
-  const bool f8 = a.kv.kv_dtype == ATTN_KV_E4M3;
-  p.inv_k = f8 ? 1.0f / a.kv.k_scale : 1.0f;
-  p.inv_v = f8 ? 1.0f / a.kv.v_scale : 1.0f;
+  p.k_block_scale = static_cast<uint8_t*>(a.kv.k_block_scale);
+  p.v_block_scale = static_cast<uint8_t*>(a.kv.v_block_scale);
+  p.inv_k = inv_scale(a.kv, a.kv.k_scale);
+  p.inv_v = inv_scale(a.kv, a.kv.v_scale);
   p.kv = kv_index(a.kv);
   p.status = a.status;
   p.B = a.B;
@@ -255,6 +298,7 @@ cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream) {
   p.Hkv = a.cfg.num_kv_heads;
   p.eps = a.cfg.rms_eps;
   p.freqs = a.freqs;
+  p.axes = a.axes;
   // (token, step) units: a step covers 32 / (D/16) head vectors of a token.
   // Warps take equal runs of consecutive units, cut across token boundaries:
   // with more units than the resident warps (kMinBlocks blocks per SM) every
@@ -271,12 +315,13 @@ cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream) {
   p.steps_per_warp = (units + resident - 1) / resident;
   const int64_t warps = (units + p.steps_per_warp - 1) / p.steps_per_warp;
   const dim3 grid((unsigned)((warps + kWarpsPerBlock - 1) / kWarpsPerBlock));
-  if (a.cfg.head_dim == 128) {
-    if (f8) kv_append_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
-    else kv_append_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (f8) kv_append_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
-    else kv_append_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
+  switch (a.kv.kv_dtype * 2 + (a.cfg.head_dim == 128)) {
+    case ATTN_KV_BF16 * 2: kv_append_kernel<64, ATTN_KV_BF16><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_BF16 * 2 + 1: kv_append_kernel<128, ATTN_KV_BF16><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E4M3 * 2: kv_append_kernel<64, ATTN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E4M3 * 2 + 1: kv_append_kernel<128, ATTN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E2M1 * 2: kv_append_kernel<64, ATTN_KV_E2M1><<<grid, kThreads, 0, stream>>>(p); break;
+    default: kv_append_kernel<128, ATTN_KV_E2M1><<<grid, kThreads, 0, stream>>>(p); break;
   }
   return cudaGetLastError();
 }

@@ -28,6 +28,10 @@ Layouts (all row-major, host tensors on the CPU):
   entries are N(0, 1) values divided by the scale and cast with torch's own
   ``float8_e4m3fn`` conversion; the unused fill is the E4M3 NaN code or a
   finite sentinel code.
+* With ``kv_dtype="e2m1"`` it is uint8 ``[num_slots, Hkv, D/2]`` of E2M1 code
+  pairs (low half first) with block scales ``k_block_scale`` and
+  ``v_block_scale``, uint8 ``[Hkv, num_slots, D/16]``; unused slots hold the
+  NaN scale or the sentinel.
 """
 from __future__ import annotations
 
@@ -48,6 +52,7 @@ E4M3_NAN_BITS = 0x7F
 E4M3_SENTINEL_BITS = 0x5B  # a finite, distinctive code (22.0)
 E4M3_K_SCALE = 0.04
 E4M3_V_SCALE = 0.02
+E2M1_SENTINEL_BITS = 0xA3  # codes 3 (1.5) and 10 (-1.0)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -170,6 +175,21 @@ def _e4m3_codes(x: torch.Tensor, scale: float) -> torch.Tensor:
     return (x / scale).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
 
 
+def _e2m1_codes(x: torch.Tensor, scale: float):
+    """(codes, block scales) of x [..., D]: 16 entries share the E4M3 scale
+    largest magnitude / 6, each takes the nearest E2M1 magnitude (a tie the one
+    with an even code); uint8 [..., D/2] and [..., D/16]."""
+    y = (x / scale).unflatten(-1, (-1, 16))
+    s = (y.abs().amax(-1) / 6).clamp_(max=448.0).to(torch.float8_e4m3fn)
+    z = (y / s.float().clamp_(min=2.0 ** -9)[..., None]).flatten(-2)
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    a = z.abs().contiguous()
+    up, down = torch.searchsorted(mids, a, right=True), torch.searchsorted(mids, a)
+    c = torch.where(up % 2 == 0, up, down) + 8 * torch.signbit(z).long()
+    c = c.to(torch.uint8)
+    return c[..., 0::2] + 16 * c[..., 1::2], s.view(torch.uint8)
+
+
 def make_inputs(w: Workload, extra_capacity: Sequence[int] | None = None,
                 unused_fill: str = "nan", page_size: int = 0, kv_dtype: str = "bf16",
                 k_scale: float = E4M3_K_SCALE, v_scale: float = E4M3_V_SCALE) -> dict:
@@ -184,10 +204,12 @@ def make_inputs(w: Workload, extra_capacity: Sequence[int] | None = None,
     ``page_table`` (int32 [B, max pages]; unused entries -1).  The logical
     contents (qkv, weights, prior cache entries by position) are the same as
     with the contiguous layout for the same workload.
-    ``kv_dtype="e4m3"`` makes a one-byte cache (codes, ``k_scale``, ``v_scale``).
+    ``kv_dtype="e4m3"`` makes a one-byte cache (codes, ``k_scale``, ``v_scale``),
+    ``kv_dtype="e2m1"`` a four-bit one (and ``k_block_scale``, ``v_block_scale``).
     """
-    assert kv_dtype in ("bf16", "e4m3")
+    assert kv_dtype in ("bf16", "e4m3", "e2m1")
     fp8 = kv_dtype == "e4m3"
+    fp4 = kv_dtype == "e2m1"
     g = _gen(1000 + w.seed)
     B, H, Hkv, D = w.batch, w.num_q_heads, w.num_kv_heads, w.head_dim
     N = w.num_tokens
@@ -214,7 +236,13 @@ def make_inputs(w: Workload, extra_capacity: Sequence[int] | None = None,
             k += npg[b]
         num_slots = total * page_size
         base = [0] * B
-    if fp8:
+    kbs = vbs = None
+    if fp4:
+        nan = unused_fill == "nan"
+        k_cache = torch.full((num_slots, Hkv, D // 2), 0xFF if nan else E2M1_SENTINEL_BITS, dtype=torch.uint8)
+        kbs = torch.full((Hkv, num_slots, D // 16), E4M3_NAN_BITS if nan else E4M3_SENTINEL_BITS, dtype=torch.uint8)
+        v_cache, vbs = k_cache.clone(), kbs.clone()
+    elif fp8:
         k_cache = torch.full((num_slots, Hkv, D), E4M3_NAN_BITS if unused_fill == "nan" else E4M3_SENTINEL_BITS,
                              dtype=torch.uint8)
         v_cache = k_cache.clone()
@@ -231,13 +259,17 @@ def make_inputs(w: Workload, extra_capacity: Sequence[int] | None = None,
             if fp8:
                 kp, vp = _e4m3_codes(kp.float(), k_scale), _e4m3_codes(vp.float(), v_scale)
             if page_table is None:
-                k_cache[base[b]:base[b] + c] = kp
-                v_cache[base[b]:base[b] + c] = vp
+                slots = torch.arange(base[b], base[b] + c)
             else:
                 pos = torch.arange(c)
                 slots = page_table[b, pos // page_size].long() * page_size + pos % page_size
-                k_cache[slots] = kp
-                v_cache[slots] = vp
+            if fp4:
+                kp, ks = _e2m1_codes(kp.float(), k_scale)
+                vp, vs = _e2m1_codes(vp.float(), v_scale)
+                kbs[:, slots] = ks.transpose(0, 1)
+                vbs[:, slots] = vs.transpose(0, 1)
+            k_cache[slots] = kp
+            v_cache[slots] = vp
     cu = [0]
     for n in w.new_lens:
         cu.append(cu[-1] + n)
@@ -257,6 +289,8 @@ def make_inputs(w: Workload, extra_capacity: Sequence[int] | None = None,
         "kv_dtype": kv_dtype,
         "k_scale": float(k_scale),
         "v_scale": float(v_scale),
+        "k_block_scale": kbs,
+        "v_block_scale": vbs,
     }
 
 

@@ -93,15 +93,14 @@ def upload(w, host: dict, device="cuda") -> DeviceStep:
     pt = dev(host["page_table"]) if host.get("page_table") is not None else None
     ps = int(host.get("page_size", 0))
     scales = (float(host.get("k_scale", 1.0)), float(host.get("v_scale", 1.0)))
-    part = lambda t, lo, hi: None if t is None else t[lo:hi].contiguous()
+    blocks = [dev(host[n]) if host.get(n) is not None else None for n in ("k_block_scale", "v_block_scale")]
+    kv = attn.KVCache(k_cache, v_cache, slot_base, cache_lens, cap, pt, ps, *scales, *blocks)
     kv_p = kv_d = None
     if df > 0:
-        kv_p = attn.KVCache(k_cache, v_cache, slot_base[:df], cache_lens[:df], cap[:df],
-                            part(pt, 0, df), ps, *scales)
+        kv_p = kv.rows(0, df)
     if df < w.batch:
         assert all(n == 1 for n in w.new_lens[df:]), "decode requests take one token each"
-        kv_d = attn.KVCache(k_cache, v_cache, slot_base[df:], cache_lens[df:], cap[df:],
-                            part(pt, df, w.batch), ps, *scales)
+        kv_d = kv.rows(df, w.batch)
     N = w.num_tokens
     out = torch.zeros((N, w.num_q_heads * w.head_dim), dtype=torch.bfloat16, device=device)
     max_kv = max([c + n for c, n in zip(w.cache_lens, w.new_lens)] + [1])
@@ -248,10 +247,7 @@ class HostPrefill:
             for c, e in zip(plan.chunks, landed):
                 self.s_prep.wait_event(e)
                 cu_d = meta[c.cu[0]:c.cu[1]]
-                ckv = attn.KVCache(kv.k_cache, kv.v_cache, kv.slot_base[c.b0:c.b1], meta[c.cl[0]:c.cl[1]],
-                                   kv.slot_capacity[c.b0:c.b1],
-                                   None if kv.page_table is None else kv.page_table[c.b0:c.b1],
-                                   kv.page_size, kv.k_scale, kv.v_scale)
+                ckv = kv.rows(c.b0, c.b1, meta[c.cl[0]:c.cl[1]])
                 attn.prefill_prepare(self.cfg, self.qkv_dev[c.t0:c.t1], self.q_norm_w, self.k_norm_w, cu_d, ckv,
                                      self.q_stage[c.t0:c.t1], self.ws, self.s_prep)
                 e1 = torch.cuda.Event()

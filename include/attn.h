@@ -15,8 +15,9 @@
  *
  * Conventions used by every entry point:
  *
- * Data types.  qkv, the norm weights, the caches and the output are bf16
- *   (IEEE bfloat16 bits, round-to-nearest-even on every store).  All
+ * Data types.  qkv, the norm weights, the caches (or E4M3, E2M1: kv_dtype
+ *   below) and the output are bf16 (IEEE bfloat16 bits, round-to-nearest-even
+ *   on every store).  All
  *   arithmetic is fp32 (norm, rotation, scores, softmax, accumulation); Q and
  *   the softmax probabilities enter the tensor-core products rounded to bf16.
  * Positions.  Request b has cache_lens[b] = c_b entries already cached and
@@ -111,7 +112,22 @@ typedef struct attn_config {
  *     section 4.3: decode is bound by memory bandwidth; its section 2.6 lists
  *     KV-cache reduction among the modern variants).  Every call takes it;
  *     next to an E4M3 cache the prepared Q of attn_prefill_prepare /
- *     attn_prefill_attend is f16 instead of bf16. */
+ *     attn_prefill_attend is f16 instead of bf16.
+ *   ATTN_KV_E2M1 (2): four bits per entry, OCP FP4 E2M1 (magnitudes 0, 0.5,
+ *     1, 1.5, 2, 3, 4, 6), with one E4M3 scale per block of 16 consecutive
+ *     entries of a head's vector.  k_cache and v_cache: 1-byte
+ *     [num_slots, Hkv, D / 2], byte j of a vector holds entry 2j in its low
+ *     half and entry 2j + 1 in its high half; k_block_scale and
+ *     v_block_scale: 1-byte [Hkv, num_slots, D / 16], 16-byte aligned (a
+ *     head's scales of consecutive slots are contiguous, as the readers of one
+ *     head want them).  A value x is stored with r = fp32(1 / k_scale) (V:
+ *     v_scale) as y = fp32(x * r), block scale s = e4m3(fp32(max |y| / 6)) over
+ *     its block, code = e2m1(fp32(y / s)) (0 where s is 0): both rounded to
+ *     nearest even and clamped to the largest finite value.  Readers take
+ *     code * s * k_scale.  A NaN anywhere in a block makes s, and with it every
+ *     entry of the block, NaN; an infinity is clamped.  A quarter of the bytes
+ *     of a bf16 cache and an eighth of a byte per entry for the scales.  Every
+ *     call takes it; the prepared Q is f16. */
 typedef struct attn_kv {
   void* k_cache;
   void* v_cache;
@@ -123,11 +139,37 @@ typedef struct attn_kv {
   int32_t page_size;            /* slots per page (paged layout) */
   int32_t pages_per_req;        /* row length of page_table (paged layout) */
   int32_t kv_dtype;             /* ATTN_KV_BF16 or ATTN_KV_E4M3 */
-  float k_scale;                /* E4M3: K entry = byte * k_scale */
-  float v_scale;                /* E4M3: V entry = byte * v_scale */
+  float k_scale;                /* E4M3: K entry = byte * k_scale; E2M1: the tensor's scale */
+  float v_scale;                /* E4M3: V entry = byte * v_scale; E2M1: the tensor's scale */
+  /* read only with kv_dtype == ATTN_KV_E2M1 (else callers need not set them) */
+  void* k_block_scale;          /* E2M1: [Hkv, num_slots, D / 16] E4M3 scales */
+  void* v_block_scale;
 } attn_kv_t;
 
-enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1 };
+enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1, ATTN_KV_E2M1 = 2 };
+
+/* Rotary positions with several axes (host struct holding a device pointer).
+ * A token of a multimodal prompt has a position on each of A axes (time,
+ * height and width for images and video; text has the same position on all).
+ * Pair i of D / 2 keeps its frequency theta^(-2i/D) and takes the position of
+ * the axis a(i):
+ *   interleaved == 0: runs of pairs, the first section[0] of axis 0, the next
+ *     section[1] of axis 1, and so on;
+ *   interleaved != 0: a(i) = i % A where i / A < section[i % A], else 0.
+ * section[] sums to D / 2 (interleaved: and every axis > 0 finds its
+ * section[a] pairs below D / 2).  positions: int32 [A, ld] on the device,
+ * positions[a * ld + t] the position of token t (row t of qkv) on axis a, each
+ * in [0, 2^24].  Only the rotation angles come from here: slots, lengths and
+ * the causal limit go by the cache as in the calls without axes.  A token with
+ * a position outside the range sets ATTN_STATUS_POSITION; its K and V are not
+ * appended and its prepared Q (decode: its output row) is left unwritten. */
+typedef struct attn_rope_axes {
+  int32_t num_axes;     /* A: 1 .. 4 */
+  int32_t section[4];   /* rotation pairs per axis */
+  int32_t interleaved;
+  const int32_t* positions;
+  int64_t ld;           /* row length of positions, >= N (decode: >= B) */
+} attn_rope_axes_t;
 
 enum {
   ATTN_OK = 0,
@@ -144,8 +186,10 @@ enum {
   ATTN_STATUS_CAPACITY = 1, /* a request's region cannot hold c_b + n_b entries */
   ATTN_STATUS_SEQLENS = 2,  /* cu_seqlens decreasing or cu_seqlens[B] != N */
   ATTN_STATUS_TIMEOUT = 4,  /* a pipeline wait gave up (internal error) */
-  ATTN_STATUS_BOUNDS = 8    /* max_seqlen / max_cache_len below a request's length:
+  ATTN_STATUS_BOUNDS = 8,   /* max_seqlen / max_cache_len below a request's length:
                                that request's output rows are left unwritten */
+  ATTN_STATUS_POSITION = 16, /* an axis position outside [0, 2^24] (attn_rope_axes_t) */
+  ATTN_STATUS_PAGES = 32    /* a page call refused or skipped something (pages.h) */
 };
 
 /* Workspace bytes needed by any call with at most `max_tokens` new tokens,
@@ -236,6 +280,53 @@ ATTN_API int attn_qkv_proj_prepare(const attn_config_t* cfg, const void* hidden,
                                    const void* w_qkv, const void* q_norm_w, const void* k_norm_w,
                                    const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
                                    void* q_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* The calls above with rotary positions on several axes: the same arguments
+ * and results with the angles of `rope` (host struct; NULL: the position
+ * c_b + j on every pair, i.e. the call without _axes).  attn_prefill_attend
+ * takes the prepared Q of either form.  attn_decode_axes and
+ * attn_decode_attend_axes over a bf16 cache keep Q and the softmax probabilities
+ * to about 16 bits where the calls without axes round them to bf16.  An image's tokens share or repeat
+ * positions, so the positions of a request's next tokens are the caller's to
+ * continue. */
+ATTN_API int attn_kv_append_axes(const attn_config_t* cfg, const void* qkv, const void* k_norm_w,
+                                 const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
+                                 const attn_rope_axes_t* rope, void* workspace, size_t ws_bytes,
+                                 void* stream);
+ATTN_API int attn_prefill_prepare_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                                       const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
+                                       const attn_kv_t* kv, const attn_rope_axes_t* rope, void* q_out,
+                                       void* workspace, size_t ws_bytes, void* stream);
+ATTN_API int attn_prefill_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                               const void* k_norm_w, const int32_t* cu_seqlens, int32_t B, int32_t N,
+                               int32_t max_seqlen, const attn_kv_t* kv, const attn_rope_axes_t* rope,
+                               void* out, void* workspace, size_t ws_bytes, void* stream);
+ATTN_API int attn_decode_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                              const void* k_norm_w, int32_t B, int32_t max_cache_len, const attn_kv_t* kv,
+                              const attn_rope_axes_t* rope, void* out, void* workspace, size_t ws_bytes,
+                              void* stream);
+ATTN_API int attn_decode_attend_axes(const attn_config_t* cfg, const void* qkv, const void* q_norm_w,
+                                     int32_t B, int32_t max_cache_len, const attn_kv_t* kv,
+                                     const attn_rope_axes_t* rope, void* out, void* workspace,
+                                     size_t ws_bytes, void* stream);
+ATTN_API int attn_qkv_proj_prepare_axes(const attn_config_t* cfg, const void* hidden, int32_t hidden_size,
+                                        const void* w_qkv, const void* q_norm_w, const void* k_norm_w,
+                                        const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
+                                        const attn_rope_axes_t* rope, void* q_out, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
+/* Reads cached entries back: row t of k_out and v_out, bf16 [N, Hkv, D]
+ * (16-byte aligned), is the entry at position start[b] + j of request b, where
+ * t = cu_seqlens[b] + j.  start: int32 [B] on the device.  A bf16 entry is
+ * copied; E4M3 and E2M1 entries are given as the bf16 nearest to the fp32
+ * value of byte * scale (E2M1: fp32(code * s) * scale).  The positions must
+ * lie in the request's region (start[b] + n_b <= slot_capacity[b] as for an
+ * append; cache_lens is not used): a request whose range does not is skipped
+ * and an entry whose page lies outside the cache is given as zeros, both with
+ * ATTN_STATUS_CAPACITY.  The workspace needs only its 256-byte header. */
+ATTN_API int attn_kv_gather(const attn_config_t* cfg, const attn_kv_t* kv, const int32_t* cu_seqlens,
+                            const int32_t* start, int32_t B, int32_t N, void* k_out, void* v_out,
+                            void* workspace, size_t ws_bytes, void* stream);
 
 /* The output projection after the attention (code walkthrough section 3.3:
  * o_proj; transformer basics "Attention calculation: part 1"):
