@@ -45,6 +45,11 @@ class AttnRopeAxes(ctypes.Structure):
                 ("positions", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
+class AttnPages(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ref_count", ctypes.c_void_p), ("cache_lens", ctypes.c_void_p),
+                ("num_rows", ctypes.c_int32)]
+
+
 ATTN_KV_BF16 = 0
 ATTN_KV_E4M3 = 1
 ATTN_KV_E2M1 = 2
@@ -64,6 +69,7 @@ _SZ = ctypes.c_size_t
 _CFG = ctypes.POINTER(AttnConfig)
 _KV = ctypes.POINTER(AttnKV)
 _ROPE = ctypes.POINTER(AttnRopeAxes)
+_PAGES = ctypes.POINTER(AttnPages)
 
 EXPORTS = {
     "attn_workspace_size": (_SZ, [_CFG, _I32, _I32, _I32]),
@@ -86,6 +92,12 @@ EXPORTS = {
     "attn_qkv_proj_prepare_axes": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _P,
                                                   _SZ, _P]),
     "attn_kv_gather": (ctypes.c_int, [_CFG, _KV, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
+    "attn_pages_workspace_size": (_SZ, [ctypes.c_int64, _I32]),
+    "attn_pages_reserve": (ctypes.c_int, [_KV, _PAGES, _P, _P, _I32, _P, _SZ, _P]),
+    "attn_pages_fork": (ctypes.c_int, [_CFG, _KV, _PAGES, _P, _P, _I32, _P, _SZ, _P]),
+    "attn_pages_free": (ctypes.c_int, [_KV, _PAGES, _P, _I32, _P, _SZ, _P]),
+    "attn_pages_copy": (ctypes.c_int, [_CFG, _KV, _P, _P, _I32, _P, _SZ, _P]),
+    "attn_pages_compact": (ctypes.c_int, [_CFG, _KV, _PAGES, _P, _SZ, _P]),
     "attn_get_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "attn_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sample_tokens": (ctypes.c_int, [_P, _I32, _I32, ctypes.c_int64, _P, _P, _P, _P, _P, _P]),
@@ -371,6 +383,81 @@ def kv_gather(cfg: AttnConfig, kv: KVCache, cu_seqlens, start, k_out, v_out, wor
     _check(load().attn_kv_gather(ctypes.byref(cfg), ctypes.byref(s), _ptr(cu_seqlens), _ptr(start), B,
                                  k_out.shape[0], _bf16(k_out, "k_out"), _bf16(v_out, "v_out"), _ptr(workspace),
                                  workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- pages (include/pages.h)
+def new_pages_workspace(kv: KVCache, max_rows: int | None = None) -> torch.Tensor:
+    """Allocate and initialise a workspace for the page calls on ``kv``'s pool
+    (``max_rows``: most page-table rows, by default the table's)."""
+    assert kv.page_table is not None and kv.page_size > 0, "the cache is not paged"
+    rows = int(kv.page_table.shape[0]) if max_rows is None else int(max_rows)
+    n = load().attn_pages_workspace_size(kv.k_cache.shape[0] // kv.page_size, rows)
+    if n == 0:
+        raise AttnError(-1, "invalid workspace query")
+    ws = torch.empty(n, dtype=torch.uint8, device=kv.k_cache.device)
+    _check(load().attn_workspace_init(_ptr(ws), n, _stream()))
+    return ws
+
+
+def _i32(t, name):
+    assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), name
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _pages(kv: KVCache, ref_count) -> AttnPages:
+    """The pool's bookkeeping: ``kv``'s page table and cached lengths (written
+    by the page calls) and the pages' reference counts."""
+    assert kv.page_table is not None and kv.page_size > 0, "the cache is not paged"
+    rows = int(kv.page_table.shape[0])
+    assert ref_count.numel() >= kv.k_cache.shape[0] // kv.page_size, "ref_count"
+    assert kv.cache_lens.numel() >= rows, "cache_lens"
+    return AttnPages(_i32(kv.page_table, "page_table"), _i32(ref_count, "ref_count"),
+                     _i32(kv.cache_lens, "cache_lens"), rows)
+
+
+def pages_reserve(kv: KVCache, ref_count, rows, new_tokens, workspace, stream=None):
+    """Room for new_tokens[i] more entries in request rows[i] (int32 device
+    tensors): the lowest free pages into the open entries of kv.page_table."""
+    assert rows.numel() == new_tokens.numel(), "new_tokens"
+    s, p = kv.struct(), _pages(kv, ref_count)
+    _check(load().attn_pages_reserve(ctypes.byref(s), ctypes.byref(p), _i32(rows, "rows"),
+                                     _i32(new_tokens, "new_tokens"), rows.numel(), _ptr(workspace), workspace.numel(),
+                                     _stream(stream)))
+
+
+def pages_fork(cfg: AttnConfig, kv: KVCache, ref_count, src_rows, dst_rows, workspace, stream=None):
+    """Row dst_rows[i] becomes a copy of the request in row src_rows[i]: full
+    pages shared, the open one copied."""
+    assert src_rows.numel() == dst_rows.numel(), "dst_rows"
+    s, p = kv.struct(), _pages(kv, ref_count)
+    _check(load().attn_pages_fork(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _i32(src_rows, "src_rows"),
+                                  _i32(dst_rows, "dst_rows"), src_rows.numel(), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)))
+
+
+def pages_free(kv: KVCache, ref_count, rows, workspace, stream=None):
+    """The requests in ``rows`` end: their pages lose a reference, the rows are
+    emptied."""
+    s, p = kv.struct(), _pages(kv, ref_count)
+    _check(load().attn_pages_free(ctypes.byref(s), ctypes.byref(p), _i32(rows, "rows"), rows.numel(),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def pages_copy(cfg: AttnConfig, kv: KVCache, src_pages, dst_pages, workspace, stream=None):
+    """Page dst_pages[i] becomes a copy of page src_pages[i]."""
+    assert src_pages.numel() == dst_pages.numel(), "dst_pages"
+    s = kv.struct()
+    _check(load().attn_pages_copy(ctypes.byref(cfg), ctypes.byref(s), _i32(src_pages, "src_pages"),
+                                  _i32(dst_pages, "dst_pages"), src_pages.numel(), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)))
+
+
+def pages_compact(cfg: AttnConfig, kv: KVCache, ref_count, workspace, stream=None):
+    """Moves the pages in use to the front of the pool; kv.page_table and
+    ``ref_count`` follow."""
+    s, p = kv.struct(), _pages(kv, ref_count)
+    _check(load().attn_pages_compact(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _ptr(workspace),
+                                     workspace.numel(), _stream(stream)))
 
 
 def get_status(workspace, stream=None) -> int:

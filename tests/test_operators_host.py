@@ -172,3 +172,60 @@ def test_gather_arguments_checked(lib):
         assert call(**bad) == -1, bad
     assert call(ws=None) == -3 and call(n=128) == -3
 
+
+# ------------------------------------------------------------------ page calls
+def paged(attn, **kw):
+    return kv4(attn, **{**dict(num_slots=1000, slot_base=None, page_table=FAKE, page_size=64, pages_per_req=4), **kw})
+
+
+def test_pages_workspace_size(lib):
+    assert lib.attn_pages_workspace_size(1, 1) >= 256 + 6 * 4
+    assert lib.attn_pages_workspace_size(1 << 24, 1 << 24) >= 6 * 4 << 24
+    for pages, rows in ((0, 1), (1, 0), (-1, 5), ((1 << 24) + 1, 1), (1, (1 << 24) + 1)):
+        assert lib.attn_pages_workspace_size(pages, rows) == 0
+
+
+def test_page_calls_check_their_arguments(lib):
+    from causal_gqa_attention_qkv_gb300 import attn
+    f, cfg = ctypes.c_void_p(FAKE), attn.config(8, 2, 64)
+    need = lib.attn_pages_workspace_size(15, 6)
+
+    def calls(kv={}, pages={}, a=f, b=f, n=3, ws=f, nws=need, cfg=cfg, no_kv=False, no_pages=False):
+        k = None if no_kv else ctypes.byref(paged(attn, **kv))
+        p = None if no_pages else ctypes.byref(attn.AttnPages(*{**dict(page_table=FAKE, ref_count=FAKE, cache_lens=FAKE,
+                                                                       num_rows=6), **pages}.values()))
+        c = ctypes.byref(cfg)
+        return dict(reserve=lib.attn_pages_reserve(k, p, a, b, n, ws, nws, None),
+                    fork=lib.attn_pages_fork(c, k, p, a, b, n, ws, nws, None),
+                    free=lib.attn_pages_free(k, p, a, n, ws, nws, None),
+                    copy=lib.attn_pages_copy(c, k, a, b, n, ws, nws, None),
+                    compact=lib.attn_pages_compact(c, k, p, ws, nws, None))
+
+    every = {"reserve", "fork", "free", "copy", "compact"}
+
+    def refused(names, code=-1, **kw):
+        for name, rc in calls(**kw).items():
+            if name in names:
+                assert rc == code, (name, kw, rc)
+            else:
+                assert rc in PAST_CHECKS, (name, kw, rc)
+
+    refused(set())
+    refused(every, no_kv=True)
+    refused(every - {"copy"}, no_pages=True)
+    refused(every, kv={"page_table": None, "slot_base": FAKE})
+    refused(every, kv={"page_size": 48})
+    refused(every, kv={"num_slots": 63})                      # not one page
+    refused(every, kv={"num_slots": (1 << 30) + 64}, nws=1 << 40)  # more than 2^24 pages
+    refused(every, kv={"k_block_scale": None})
+    for name in ("page_table", "ref_count", "cache_lens"):
+        refused(every - {"copy"}, pages={name: None})
+    refused(every - {"copy"}, pages={"num_rows": 0})
+    refused({"reserve", "fork", "free", "copy"}, a=None)
+    refused({"reserve", "fork", "copy"}, b=None)
+    refused({"reserve", "fork", "free", "copy"}, n=-1)
+    refused({"reserve", "fork"}, n=7)                         # more than the rows
+    refused(every, code=-3, ws=None)
+    refused(every, code=-3, ws=ctypes.c_void_p(FAKE + 64))
+    refused({"reserve", "fork", "compact"}, code=-3, nws=need - 256)
+    refused({"fork", "copy", "compact"}, code=-2, cfg=attn.config(8, 3, 64))
