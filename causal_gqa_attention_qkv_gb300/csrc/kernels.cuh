@@ -143,6 +143,7 @@ struct DecodeArgs {
 };
 int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits);
 int launch_decode(const DecodeArgs& a, cudaStream_t stream);
+int launch_decode_e2m1(const DecodeArgs& a, cudaStream_t stream);  // the split kernel over an E2M1 cache
 
 struct PrefillArgs {
   attn_config_t cfg;
