@@ -101,6 +101,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The same with the low (high) half of s for both.
+__device__ __forceinline__ uint32_t mul_f16x2_lo(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __low2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_f16x2_hi(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __high2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -115,18 +125,32 @@ __device__ __forceinline__ float amax8(const float (&y)[8]) {
   return m;
 }
 
-// The E4M3 scale (its code) of a block with largest magnitude amax.  The
-// divisions here and in e2m1_codes8 are IEEE divisions: 16-bit inputs meet the
-// rounding boundaries exactly, and a product with a rounded reciprocal would
-// decide those ties by the reciprocal's error.
+// The E4M3 scale (its code) of a block with largest magnitude amax, by an IEEE
+// division: 16-bit inputs meet the rounding boundaries exactly, and a product with
+// a rounded reciprocal would decide those ties by the reciprocal's error.
 __device__ __forceinline__ uint32_t e2m1_block_scale(float amax) { return e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu; }
 
-// Codes of eight values of a block with scale s (the value of its code).
+// Codes of eight values of a block with scale s (the value of its code): those of
+// the quotients y / s rounded to fp32, for less than eight divisions.  Every
+// boundary between codes is a multiple m of 1/4.  With m the multiple nearest to an
+// approximate quotient, y - m s rounds to zero only if it is zero (m s is exact: 4
+// and 5 bits) and m + (y - m s) / s, rounded once, lies on the side of m that y / s
+// does: a nonzero y - m s is at least an ulp of y, and (ulp of y) / s exceeds half
+// an ulp of m since s is below twice the power of two in it.
 __device__ __forceinline__ uint32_t e2m1_codes8(const float (&y)[8], float s) {
-  if (s == 0.f) return 0u;
+  if (!(s > 0.f)) {  // an empty block, or a NaN one (whose codes do not matter)
+    return 0u;
+  }
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // s is in [2^-9, 448]
+  constexpr float kQuarters = 3145728.f;  // 1.5 * 2^21: its ulp is 1/4
   float z[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = __fdiv_rn(y[e], s);
+  for (int e = 0; e < 8; ++e) {
+    const float q = fminf(fmaxf(__fmul_rn(y[e], inv), -8.f), 8.f);  // an infinity stays on its side
+    const float m = __fsub_rn(__fadd_rn(q, kQuarters), kQuarters);
+    z[e] = fmaf(fmaf(-m, s, y[e]), inv, m);
+  }
   return e2m1x8(z);
 }
 
@@ -472,6 +496,122 @@ __device__ __forceinline__ void store_e2m1_pair(const float (&xa)[8], const floa
   if ((li & 1) == 0) {
     scales[li >> 1] = (uint8_t)sa;
     scales[D / 32 + (li >> 1)] = (uint8_t)sb;
+  }
+}
+
+// ---------------------------------------------------------------- K to the last bit of fp32
+// A four-bit code moves by up to a third of its value when its input crosses a
+// rounding boundary, so K is brought to the fp32 value nearest to the exact one
+// before it is coded (the plain fp32 steps are off by some 1e-7 and crossed a
+// boundary about ten times as often).  Values are pairs hi + lo of floats: the
+// error-free sum and product are Knuth's and Dekker's (by fma).
+struct F2 {
+  float hi, lo;
+};
+__device__ __forceinline__ F2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ F2 two_prod(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, fmaf(a, b, -p)};
+}
+
+// cos and sin of pos * f as pairs, absolute error about 1e-8: the angle reduced by
+// multiples of pi / 2 to a pair |r| <= pi / 4, then the Taylor series with the leading
+// terms (r, and 1 - r^2 / 2) kept exactly.
+__device__ __forceinline__ void rope_angle_fine(float pos, float f_hi, float f_lo, const RopeFreqs& fr, F2* c, F2* s) {
+  const F2 a = two_prod(pos, f_hi);
+  const float k = rintf(a.hi * (4.f * fr.inv_two_pi));
+  const float h_hi = 0.25f * fr.two_pi_hi, h_lo = 0.25f * fr.two_pi_lo;  // pi / 2
+  const F2 q = two_prod(-k, h_lo);
+  const F2 t = two_sum(fmaf(-k, h_hi, a.hi), q.hi);
+  const F2 r = two_sum(t.hi, t.lo + q.lo + fmaf(pos, f_lo, a.lo));
+  const F2 r2 = two_prod(r.hi, r.hi);
+  const float x = r2.hi;
+  const float ps = fmaf(fmaf(fmaf(fmaf(-1.f / 39916800, x, 1.f / 362880), x, -1.f / 5040), x, 1.f / 120), x, -1.f / 6);
+  const float pc = fmaf(fmaf(fmaf(fmaf(1.f / 479001600, x, -1.f / 3628800), x, 1.f / 40320), x, -1.f / 720), x, 1.f / 24);
+  F2 sn = two_sum(r.hi, r.hi * x * ps);
+  sn = two_sum(sn.hi, fmaf(r.lo, fmaf(-0.5f, x, 1.f), sn.lo));
+  F2 cs = two_sum(1.f, -0.5f * x);
+  cs = two_sum(cs.hi, cs.lo + (fmaf(x * x, pc, -0.5f * r2.lo) - r.hi * r.lo));  // hi alone is the nearest float
+  const int quarter = (int)k & 3;
+  const bool swap = quarter & 1, neg_c = quarter == 1 || quarter == 2, neg_s = quarter >= 2;
+  *c = swap ? sn : cs;
+  *s = swap ? cs : sn;
+  if (neg_c) *c = {-c->hi, -c->lo};
+  if (neg_s) *s = {-s->hi, -s->lo};
+}
+
+// pair_angles() with pairs hi + lo.
+template <int D, class Pos>
+__device__ __forceinline__ void pair_angles_fine(const Pos& pos, const RopeFreqs& fr, int lane, F2 (&cs)[8], F2 (&sn)[8]) {
+  constexpr int PPL = D / 64;
+  const int li = lane % (D / 16);
+  F2 c_own[PPL], s_own[PPL];
+#pragma unroll
+  for (int e = 0; e < PPL; ++e) {
+    const int pr = lane * PPL + e;
+    rope_angle_fine(pos(pr), fr.hi[pr], fr.lo[pr], fr, &c_own[e], &s_own[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int from = (li * 8 + e) / PPL;
+    cs[e].hi = __shfl_sync(0xffffffffu, c_own[e % PPL].hi, from);
+    cs[e].lo = __shfl_sync(0xffffffffu, c_own[e % PPL].lo, from);
+    sn[e].hi = __shfl_sync(0xffffffffu, s_own[e % PPL].hi, from);
+    sn[e].lo = __shfl_sync(0xffffffffu, s_own[e % PPL].lo, from);
+  }
+}
+
+// y c - z s rounded once (s negated by the caller for the sum).
+__device__ __forceinline__ float rotate_fine(const F2& y, const F2& c, const F2& z, const F2& s) {
+  const F2 m = two_prod(y.hi, c.hi), n = two_prod(-z.hi, s.hi);
+  const F2 d = two_sum(m.hi, n.hi);
+  const float e = fmaf(y.hi, c.lo, fmaf(y.lo, c.hi, m.lo)) - fmaf(z.hi, s.lo, fmaf(z.lo, s.hi, -n.lo));
+  return d.hi + (d.lo + e);
+}
+
+// norm_rope_pair() with one rounding to fp32 at the end.  x and w are bf16: x^2
+// and w x are exact in fp32.
+template <int D>
+__device__ __forceinline__ void norm_rope_pair_fine(const uint4& raw_a, const uint4& raw_b, const uint4& w_a,
+                                                    const uint4& w_b, const F2 (&cs)[8], const F2 (&sn)[8], float eps,
+                                                    float (&ra)[8], float (&rb)[8]) {
+  constexpr int L = D / 16;
+  float xa[8], xb[8];
+  unpack_bf16x8(raw_a, xa);
+  unpack_bf16x8(raw_b, xb);
+  F2 ss = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const F2 t = two_sum(xa[e] * xa[e], xb[e] * xb[e]);
+    const F2 u = two_sum(ss.hi, t.hi);
+    ss = {u.hi, ss.lo + (u.lo + t.lo)};
+  }
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) {
+    const F2 u = two_sum(ss.hi, __shfl_xor_sync(0xffffffffu, ss.hi, off));
+    ss = {u.hi, ss.lo + __shfl_xor_sync(0xffffffffu, ss.lo, off) + u.lo};
+  }
+  F2 v = two_sum(ss.hi * (1.0f / D), eps);
+  v.lo += ss.lo * (1.0f / D);
+  // 1 / sqrt(v): one Newton step on rsqrtf's value g, its correction kept apart
+  const float g = rsqrtf(v.hi);
+  const F2 g2 = two_prod(g, g);
+  const float res = fmaf(-v.hi, g2.hi, 1.f) - fmaf(v.hi, g2.lo, v.lo * g2.hi);
+  const float g_lo = 0.5f * g * res;
+  float wa[8], wb[8];
+  unpack_bf16x8(w_a, wa);
+  unpack_bf16x8(w_b, wb);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float pa = wa[e] * xa[e], pb = wb[e] * xb[e];
+    F2 ya = two_prod(pa, g), yb = two_prod(pb, g);
+    ya.lo = fmaf(pa, g_lo, ya.lo);
+    yb.lo = fmaf(pb, g_lo, yb.lo);
+    ra[e] = rotate_fine(ya, cs[e], yb, sn[e]);
+    rb[e] = rotate_fine(yb, cs[e], ya, F2{-sn[e].hi, -sn[e].lo});
   }
 }
 

@@ -55,13 +55,20 @@ __device__ __forceinline__ void append_new_kv(const DecodePar& p, const ReqInfo&
     xa = __ldg(reinterpret_cast<const uint4*>(src));
     xb = __ldg(reinterpret_cast<const uint4*>(src + H2));
   }
-  float cs[8], sn[8];
-  if constexpr (Axes) pair_angles<D>(AxisPos{p.axes, b}, p.freqs, lane, cs, sn);
-  else pair_angles<D>(OnePos{(float)r.cached}, p.freqs, lane, cs, sn);
   const uint4 wa = __ldg(reinterpret_cast<const uint4*>(p.k_norm_w + li * 8));
   const uint4 wb = __ldg(reinterpret_cast<const uint4*>(p.k_norm_w + li * 8 + H2));
   float ra[8], rb[8];
-  norm_rope_pair<D>(xa, xb, wa, wb, cs, sn, p.eps, ra, rb);
+  if constexpr (KV == ATTN_KV_E2M1) {
+    F2 cs[8], sn[8];
+    if constexpr (Axes) pair_angles_fine<D>(AxisPos{p.axes, b}, p.freqs, lane, cs, sn);
+    else pair_angles_fine<D>(OnePos{(float)r.cached}, p.freqs, lane, cs, sn);
+    norm_rope_pair_fine<D>(xa, xb, wa, wb, cs, sn, p.eps, ra, rb);
+  } else {
+    float cs[8], sn[8];
+    if constexpr (Axes) pair_angles<D>(AxisPos{p.axes, b}, p.freqs, lane, cs, sn);
+    else pair_angles<D>(OnePos{(float)r.cached}, p.freqs, lane, cs, sn);
+    norm_rope_pair<D>(xa, xb, wa, wb, cs, sn, p.eps, ra, rb);
+  }
   if constexpr (KV == ATTN_KV_E2M1) {
     if (which != 0) {
       unpack_bf16x8(xa, ra);

@@ -81,15 +81,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// Products of an f16 pair with the low (high) half of s.
-__device__ __forceinline__ uint32_t mul_lo(uint32_t a, uint32_t s) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __low2half2(*reinterpret_cast<__half2*>(&s)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t mul_hi(uint32_t a, uint32_t s) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), __high2half2(*reinterpret_cast<__half2*>(&s)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -167,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   grid_dependency_wait();  // the append kernel's cache entries, earlier kernels' reads of the outputs
 
   if (warp == kConsumerWarps) {  // ---------------- producer warp
-    if (p.k_norm_w && split == n_splits - 1) append_new_kv<D, ATTN_KV_E2M1, Axes>(p, r, b, kh, lane);
+    const bool append = p.k_norm_w && split == n_splits - 1;  // the new token's key is in the last stage
     if (lane == 0) {
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
@@ -193,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       int64_t slot[2] = {__shfl_sync(0xffffffffu, slot_now, 2 * i - w0), __shfl_sync(0xffffffffu, slot_now, 2 * i + 1 - w0)};
       if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
       if (!ok) break;
+      if (append && i == npass - 1) append_new_kv<D, ATTN_KV_E2M1, Axes>(p, r, b, kh, lane);
       const int pos = k0 + i * 2 * kKeysPerTile;
       const int halves = pos + kKeysPerTile < k1 ? 2 : 1;
       const uint32_t stage = smem_u32(smem) + st * Lay::kStageBytes;
@@ -326,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
         for (int h = 0; h < 2; ++h) {
           uint32_t a[4];
           if (w < 2) {
-            a[0] = mul_lo(x[2 * h], sc[0]);
-            a[1] = mul_lo(y[2 * h], sc[1]);
-            a[2] = mul_lo(x[2 * h + 1], sc[0]);
-            a[3] = mul_lo(y[2 * h + 1], sc[1]);
+            a[0] = mul_f16x2_lo(x[2 * h], sc[0]);
+            a[1] = mul_f16x2_lo(y[2 * h], sc[1]);
+            a[2] = mul_f16x2_lo(x[2 * h + 1], sc[0]);
+            a[3] = mul_f16x2_lo(y[2 * h + 1], sc[1]);
           } else {
-            a[0] = mul_hi(x[2 * h], sc[0]);
-            a[1] = mul_hi(y[2 * h], sc[1]);
-            a[2] = mul_hi(x[2 * h + 1], sc[0]);
-            a[3] = mul_hi(y[2 * h + 1], sc[1]);
+            a[0] = mul_f16x2_hi(x[2 * h], sc[0]);
+            a[1] = mul_f16x2_hi(y[2 * h], sc[1]);
+            a[2] = mul_f16x2_hi(x[2 * h + 1], sc[0]);
+            a[3] = mul_f16x2_hi(y[2 * h + 1], sc[1]);
           }
           mma_f16_16816(s[t], a, qb[2 * w + h][0], qb[2 * w + h][1]);
         }
@@ -452,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
           for (int k = 0; k < 4; ++k) {
             e2m1x8_to_f16(vw[k][w], x[k][0], x[k][1], x[k][2], x[k][3]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[k][c] = mul_lo(x[k][c], sc[k]);
+            for (int c = 0; c < 4; ++c) x[k][c] = mul_f16x2_lo(x[k][c], sc[k]);
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c)

@@ -46,9 +46,12 @@
 // kind::f16 with f16 operands, and the cache scales multiply the scores
 // (k_scale) and the output (v_scale).
 //
-// E2M1 caches take the same path with tiles of 128 x D / 2 bytes of codes: the
-// converting lanes fetch the block scales of their key rows into registers and
-// store code * block scale as f16 (exact).
+// E2M1 caches: the warps fetch codes into two landing buffers each (8 KB for
+// D = 128; the space that the other kernels stage output rows in), a tile or two
+// ahead, and convert them with their block scales (read into registers) to
+// code * block scale in f16 (exact).  Landing a tile of codes in its own stage, as
+// the E4M3 path does, left every load's latency between a free stage and its
+// conversion: 3.6 us a tile.
 #include "kernels.cuh"
 #include "tcgen05.cuh"
 
@@ -339,15 +342,14 @@ __device__ void produce_kv(const TcPar& p, const SeqInfo* seq_tab, const int* ri
 // The same ring for an E4M3 cache, run by the whole warp: lane 0 copies each
 // tile of codes (128 keys x D bytes) into the last 128 x D bytes of its stage;
 // then every lane converts key rows to the f16 tile layout and lane 0
-// releases the stage to the tensor cores.  F4: an E2M1 cache (128 keys x D / 2
-// bytes a tile) whose block scales are at bscale.
-template <int D, bool F4>
-__device__ void produce_kv_codes(const TcPar& p, const SeqInfo* seq_tab, const int* ring,
-                                 const CUtensorMap* map, const uint8_t* bscale, uint8_t* smem, uint64_t* bars,
-                                 int base, int full0, int empty0, int land0, int stages, bool& ok) {
+// releases the stage to the tensor cores.
+template <int D>
+__device__ void produce_kv_f8(const TcPar& p, const SeqInfo* seq_tab, const int* ring,
+                              const CUtensorMap* map, uint8_t* smem, uint64_t* bars, int base,
+                              int full0, int empty0, int land0, int stages, bool& ok) {
   using Lay = TcLayout<D>;
   const int lane = threadIdx.x & 31;
-  constexpr int kCodeBytes = kKeys * (F4 ? D / 2 : D);
+  constexpr int kCodeBytes = kKeys * D;
   if (lane == 0) prefetch_tmap(map);
   ItemWalk w;
   w.start(p, seq_tab, ring, bars, true, ok);
@@ -362,31 +364,7 @@ __device__ void produce_kv_codes(const TcPar& p, const SeqInfo* seq_tab, const i
       uint8_t* dst = smem + base + st * Lay::kTile;
       uint8_t* land = dst + Lay::kTile - kCodeBytes;  // 1024-aligned
       uint64_t* bar = &bars[land0 + st];
-      uint32_t bs[4][D / 64];  // E2M1: block scales of this lane's four key rows
-      if constexpr (F4) {
-        const int row0 = kv_row(p, w.it, j * kKeys);
-        const int row1 = p.half_boxes ? kv_row(p, w.it, min(j * kKeys + 64, ((w.it.kv_total - 1) >> 6) << 6)) : row0 + 64;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, kCodeBytes);
-          tma_load_3d(land, map, bar, 0, w.it.kh, row0);
-          if (p.half_boxes) tma_load_3d(land + kCodeBytes / 2, map, bar, 0, w.it.kh, row1);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t slot = (int64_t)(i < 2 ? row0 : row1) + lane + 32 * (i & 1);
-          const uint8_t* src = bscale + ((int64_t)w.it.kh * p.kv.num_slots + slot) * (D / 16);
-          if (slot >= p.kv.num_slots) {  // past the cache, as TMA fills it
-#pragma unroll
-            for (int e = 0; e < D / 64; ++e) bs[i][e] = 0u;
-          } else if constexpr (D == 128) {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(src));
-            bs[i][0] = v.x;
-            bs[i][1] = v.y;
-          } else {
-            bs[i][0] = __ldcg(reinterpret_cast<const uint32_t*>(src));
-          }
-        }
-      } else if (lane == 0) {
+      if (lane == 0) {
         mbar_arrive_expect_tx(bar, kCodeBytes);
         if (!p.half_boxes) {
           tma_load_3d(land, map, bar, 0, w.it.kh, kv_row(p, w.it, j * kKeys));
@@ -403,36 +381,6 @@ __device__ void produce_kv_codes(const TcPar& p, const SeqInfo* seq_tab, const i
       // 64-column region.  Each row is read whole before any lane writes:
       // for D = 64 later f16 rows cover other lanes' code rows.
       const uint32_t tile = smem_u32(dst), codes = smem_u32(land);
-      if constexpr (F4) {
-        // rows of D / 2 bytes (64-byte swizzled when D = 128); 16 bytes are two blocks
-#pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i) {
-          const uint32_t r = (uint32_t)(lane + 32 * i);
-          uint4 c[D / 32];
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch)
-            c[ch] = lds128(codes + r * (D / 2) + (D == 128 ? (ch ^ ((r >> 1) & 3u)) << 4 : ch << 4));
-          __syncwarp();
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
-            const uint32_t s2 = e4m3x2_to_f16(bs[i][ch >> 1] >> (16 * (ch & 1)));
-            const uint32_t words[4] = {c[ch].x, c[ch].y, c[ch].z, c[ch].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t sc = prmt(s2, s2, q < 2 ? 0x1010u : 0x3232u);
-              uint4 h;
-              e2m1x8_to_f16(words[q], h.x, h.y, h.z, h.w);
-              h.x = mul_f16x2(h.x, sc);
-              h.y = mul_f16x2(h.y, sc);
-              h.z = mul_f16x2(h.z, sc);
-              h.w = mul_f16x2(h.w, sc);
-              const uint32_t ck = 4 * ch + q;  // 16-byte chunk (8 columns) of the f16 row
-              sts128(tile + (ck >> 3) * kRegionBytes + sw128(r, ck & 7), h);
-            }
-          }
-          __syncwarp();
-        }
-      } else
 #pragma unroll 1
       for (int i = 0; i < kKeys / 32; ++i) {
         const uint32_t r = (uint32_t)(lane + 32 * i);
@@ -465,6 +413,133 @@ __device__ void produce_kv_codes(const TcPar& p, const SeqInfo* seq_tab, const i
   if (lane == 0)
     for (int t = max(0, issued - stages); t < issued; ++t)
       (void)mbar_wait(&bars[land0 + t % stages], (t / stages) & 1);
+}
+
+// The ring over an E2M1 cache, run by the whole warp: tiles of codes (128 keys x
+// D / 2 bytes) land in two buffers of their own at `land`, up to two ahead of the
+// tile being converted, their block scales in registers.
+template <int D>
+__device__ void produce_kv_e2m1(const TcPar& p, const SeqInfo* seq_tab, const int* ring, const CUtensorMap* map,
+                                const uint8_t* bscale, uint8_t* smem, uint64_t* bars, int base, int land, int full0,
+                                int empty0, int land0, int stages, bool& ok) {
+  using Lay = TcLayout<D>;
+  constexpr int kCodeBytes = kKeys * (D / 2);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) prefetch_tmap(map);
+  ItemWalk w;
+  w.start(p, seq_tab, ring, bars, true, ok);
+  int j = 0;        // next tile of the walk's item to fetch; nk: the next item is not read yet
+  int issued = 0;   // tiles fetched so far
+  int g = 0;        // tiles converted so far
+  uint32_t bs0[4][D / 64], bs1[4][D / 64];  // block scales of this lane's four key rows of the landing tiles
+  // Block scales of the tile of KV head kh whose keys 0 and 64 are rows r0 and r1.
+  auto scales = [&](uint32_t(&bs)[4][D / 64], int kh, int r0, int r1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t slot = (int64_t)(i < 2 ? r0 : r1) + lane + 32 * (i & 1);
+      const uint8_t* src = bscale + ((int64_t)kh * p.kv.num_slots + slot) * (D / 16);
+      if (slot >= p.kv.num_slots) {  // past the cache, as TMA fills it
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) bs[i][e] = 0u;
+      } else if constexpr (D == 128) {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(src));
+        bs[i][0] = v.x;
+        bs[i][1] = v.y;
+      } else {
+        bs[i][0] = __ldcg(reinterpret_cast<const uint32_t*>(src));
+      }
+    }
+  };
+  // Fetches the next tile into landing buffer issued % 2; false when there is none
+  // yet.  The next item's number is waited for only when every fetched tile is
+  // converted: it is published once the item before this one is computed, which
+  // may still need those tiles.
+  auto fetch = [&]() -> bool {
+    if (!ok || !w.valid) return false;
+    if (j == w.it.nk) {
+      if (g < issued &&
+          !__all_sync(0xffffffffu, mbar_test_wait(&bars[kItemFull0 + w.k % kRing], (w.k / kRing) & 1)))
+        return false;
+      w.next(p, ok);
+      j = 0;
+      if (!ok || !w.valid) return false;
+    }
+    const int b = issued & 1;
+    const int r0 = kv_row(p, w.it, j * kKeys);
+    const int r1 = p.half_boxes ? kv_row(p, w.it, min(j * kKeys + 64, ((w.it.kv_total - 1) >> 6) << 6)) : r0 + 64;
+    if (b) scales(bs1, w.it.kh, r0, r1);
+    else scales(bs0, w.it.kh, r0, r1);
+    if (lane == 0) {
+      uint64_t* bar = &bars[land0 + b];
+      uint8_t* dst = smem + land + b * kCodeBytes;
+      mbar_arrive_expect_tx(bar, kCodeBytes);
+      tma_load_3d(dst, map, bar, 0, w.it.kh, r0);
+      if (p.half_boxes) tma_load_3d(dst + kCodeBytes / 2, map, bar, 0, w.it.kh, r1);
+    }
+    ++issued;
+    ++j;
+    return true;
+  };
+  auto convert = [&]() {  // tile g
+    const int st = g % stages, b = g & 1;
+    if (!__all_sync(0xffffffffu, g < stages || mbar_wait(&bars[empty0 + st], (g / stages - 1) & 1)) ||
+        !__all_sync(0xffffffffu, mbar_wait(&bars[land0 + b], (g >> 1) & 1))) {
+      ok = false;
+      return;
+    }
+    // Lane l converts key rows l, l + 32, l + 64, l + 96: D / 2 bytes (64-byte
+    // swizzled when D = 128; 16 bytes are two blocks) -> f16 row r of each
+    // 64-column region.
+    const uint32_t tile = smem_u32(smem + base + st * Lay::kTile), codes = smem_u32(smem + land + b * kCodeBytes);
+    uint32_t bs[4][D / 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) bs[i][e] = b ? bs1[i][e] : bs0[i][e];
+    // not unrolled: with its copy for the other operand the unrolled loop overflows
+    // the instruction cache, and the CTAs slow each other down by half
+#pragma unroll 1
+    for (int i = 0; i < kKeys / 32; ++i) {
+      const uint32_t r = (uint32_t)(lane + 32 * i);
+      uint4 c[D / 32];
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch)
+        c[ch] = lds128(codes + r * (D / 2) + (D == 128 ? (ch ^ ((r >> 1) & 3u)) << 4 : ch << 4));
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        const uint32_t s2 = e4m3x2_to_f16(bs[0][ch >> 1] >> (16 * (ch & 1)));
+        const uint32_t words[4] = {c[ch].x, c[ch].y, c[ch].z, c[ch].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[4];
+          e2m1x8_to_f16(words[q], h[0], h[1], h[2], h[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = q < 2 ? mul_f16x2_lo(h[e], s2) : mul_f16x2_hi(h[e], s2);
+          const uint32_t ck = 4 * ch + q;  // 16-byte chunk (8 columns) of the f16 row
+          sts128(tile + (ck >> 3) * kRegionBytes + sw128(r, ck & 7), make_uint4(h[0], h[1], h[2], h[3]));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        bs[0][e] = bs[1][e];
+        bs[1][e] = bs[2][e];
+        bs[2][e] = bs[3][e];
+      }
+    }
+    tc::fence_proxy_async();  // the f16 tile is visible to the tensor cores
+    __syncwarp();             // and every lane is done with the codes
+    if (lane == 0) mbar_arrive(&bars[full0 + st]);
+    ++g;
+  };
+  while (ok) {
+    while (issued - g < 2 && fetch()) {
+    }
+    if (!ok || issued == g) break;
+    convert();
+  }
+  // Every copy issued has landed before the CTA may exit.
+  if (lane == 0)
+    for (int t = max(0, issued - 2); t < issued; ++t) (void)mbar_wait(&bars[land0 + (t & 1)], (t >> 1) & 1);
 }
 
 // Claims items from the counter in the workspace, publishes each to the
@@ -613,7 +688,9 @@ __device__ void issue_mma(const TcPar& p, const SeqInfo* seq_tab, const int* rin
 }
 
 // Softmax and epilogue of Q tile x (0: A, 1: B) of every item.
-template <int D, bool F8>
+// Staged: whole rows leave through the staging slots by TMA (an E2M1 kernel has
+// landing buffers there).
+template <int D, bool F8, bool Staged>
 __device__ void softmax_tile(const TcPar& p, const SeqInfo* seq_tab, const int* ring, uint32_t sbase,
                              uint32_t tmem, uint64_t* bars, const CUtensorMap* omap, int x, bool& ok) {
   using Lay = TcLayout<D>;
@@ -780,7 +857,7 @@ __device__ void softmax_tile(const TcPar& p, const SeqInfo* seq_tab, const int* 
       // sequence only).
       const int tpw = 32 >> p.log2G;
       const int wtok0 = it.t0 + x * BT + (warp & 3) * tpw;
-      const bool full = wtok0 + tpw <= it.n_b;  // warp-uniform
+      const bool full = Staged && wtok0 + tpw <= it.n_b;  // warp-uniform
       const uint32_t slot = sbase + Lay::kStg + warp * 4096;
       const int lane = threadIdx.x & 31;
       const bool store = tok < it.n_b;
@@ -893,18 +970,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   if (warp < 8) {
-    softmax_tile<D, F8>(p, seq_tab, ring, sbase, tmem, bars, &omap, warp >> 2, ok);
+    softmax_tile<D, F8, KV != ATTN_KV_E2M1>(p, seq_tab, ring, sbase, tmem, bars, &omap, warp >> 2, ok);
   } else if (F8 && (warp == kKWarp || warp == kVWarp)) {  // the whole warp converts the tiles
-    constexpr bool F4 = KV == ATTN_KV_E2M1;
-    const uint8_t *kbs = nullptr, *vbs = nullptr;
-    if constexpr (F4) {
-      kbs = p.k_block_scale;
-      vbs = p.v_block_scale;
+    if constexpr (KV == ATTN_KV_E2M1) {
+      constexpr int kLand = 2 * kKeys * (D / 2);  // two landing buffers
+      static_assert(2 * kLand <= 8 * 4096, "landing buffers in the staging slots");
+      if (warp == kKWarp)
+        produce_kv_e2m1<D>(p, seq_tab, ring, &kmap, p.k_block_scale, smem, bars, Lay::kK, Lay::kStg, kKFull0, kKEmpty0,
+                           kKLand0, kKStages, ok);
+      else
+        produce_kv_e2m1<D>(p, seq_tab, ring, &vmap, p.v_block_scale, smem, bars, Lay::kV, Lay::kStg + kLand, kVFull0,
+                           kVEmpty0, kVLand0, kVStages, ok);
+    } else if (warp == kKWarp) {
+      produce_kv_f8<D>(p, seq_tab, ring, &kmap, smem, bars, Lay::kK, kKFull0, kKEmpty0, kKLand0, kKStages, ok);
+    } else {
+      produce_kv_f8<D>(p, seq_tab, ring, &vmap, smem, bars, Lay::kV, kVFull0, kVEmpty0, kVLand0, kVStages, ok);
     }
-    if (warp == kKWarp)
-      produce_kv_codes<D, F4>(p, seq_tab, ring, &kmap, kbs, smem, bars, Lay::kK, kKFull0, kKEmpty0, kKLand0, kKStages, ok);
-    else
-      produce_kv_codes<D, F4>(p, seq_tab, ring, &vmap, vbs, smem, bars, Lay::kV, kVFull0, kVEmpty0, kVLand0, kVStages, ok);
   } else {
     if (lane == 0) {
       if (warp == kKWarp)

@@ -22,6 +22,9 @@ constexpr int kThreads = kWarpsPerBlock * 32;
 #ifndef PROLOGUE_BATCH_F8
 #define PROLOGUE_BATCH_F8 4
 #endif
+#ifndef PROLOGUE_BATCH_F4
+#define PROLOGUE_BATCH_F4 2
+#endif
 #ifndef PROLOGUE_MIN_BLOCKS
 #define PROLOGUE_MIN_BLOCKS 2
 #endif
@@ -29,6 +32,7 @@ constexpr int kThreads = kWarpsPerBlock * 32;
 // as many as fit in the registers two blocks per SM allow
 constexpr int kBatchBf16 = PROLOGUE_BATCH;
 constexpr int kBatchF8 = PROLOGUE_BATCH_F8;
+constexpr int kBatchF4 = PROLOGUE_BATCH_F4;
 constexpr int kMinBlocks = PROLOGUE_MIN_BLOCKS;  // resident blocks per SM the registers allow
 
 struct ProloguePar {
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
   constexpr int HPI = 32 / L;   // head vectors per warp-wide step
   constexpr int H2 = D / 2;     // offset of the second member of a rotation pair
   constexpr bool F8 = KV == ATTN_KV_E4M3, F4 = KV == ATTN_KV_E2M1;
-  constexpr int kBatch = KV != ATTN_KV_BF16 ? kBatchF8 : kBatchBf16;
+  constexpr int kBatch = F4 ? kBatchF4 : F8 ? kBatchF8 : kBatchBf16;
   const int lane = threadIdx.x & 31;
   launch_dependents();  // the attention kernel after this one may be scheduled as CTAs finish
 
@@ -151,8 +155,21 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
 
       // cos/sin of the 8 rotation pairs 8*li .. 8*li + 7 this lane's values belong to
       float cs[8], sn[8];
-      if (with_axes) pair_angles<D>(AxisPos{p.axes, t}, p.freqs, lane, cs, sn);
-      else pair_angles<D>(OnePos{pos}, p.freqs, lane, cs, sn);
+      F2 cs2[F4 ? 8 : 1], sn2[F4 ? 8 : 1];  // E2M1: K is rotated to the last bit of fp32
+      auto angles = [&](const auto& at) {
+        if constexpr (F4) {
+          pair_angles_fine<D>(at, p.freqs, lane, cs2, sn2);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            cs[e] = cs2[e].hi;
+            sn[e] = sn2[e].hi;
+          }
+        } else {
+          pair_angles<D>(at, p.freqs, lane, cs, sn);
+        }
+      };
+      if (with_axes) angles(AxisPos{p.axes, t});
+      else angles(OnePos{pos});
       uint16_t* q_row = with_q ? p.q_out + (int64_t)t * p.Hq * D + li * 8 : nullptr;
       const int64_t cache_row = slot * p.Hkv * D + li * 8;
 
@@ -167,9 +184,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
             raw_b[k] = in ? __ldg(reinterpret_cast<const uint4*>(src + H2)) : make_uint4(0, 0, 0, 0);
           }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          if (base + k >= s_end) break;  // warp-uniform
+        // step base + k, whose values are xa and xb
+        auto step = [&](int k, const uint4& xa, const uint4& xb) {
           const int hd = hd0 + (base + k) * HPI + sub;  // head index in the qkv row
           const bool live = hd < p.Hq + 2 * p.Hkv;
           const bool is_q = hd < p.Hq;
@@ -178,13 +194,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           const bool step_all_v = hd0 + (base + k) * HPI >= p.Hq + p.Hkv;
           if (F4 && step_all_v) {
             const int kvh = live ? hd - p.Hq - p.Hkv : 0;
-            float xa[8], xb[8];
-            unpack_bf16x8(raw_a[k], xa);
-            unpack_bf16x8(raw_b[k], xb);
-            store_e2m1_pair<D>(xa, xb, p.inv_v, live && ok == 2, li,
+            float fa[8], fb[8];
+            unpack_bf16x8(xa, fa);
+            unpack_bf16x8(xb, fb);
+            store_e2m1_pair<D>(fa, fb, p.inv_v, live && ok == 2, li,
                                static_cast<uint8_t*>(p.v_cache) + (slot * p.Hkv + kvh) * (D / 2),
                                p.v_block_scale + (kvh * p.kv.num_slots + slot) * (D / 16));
-            continue;
+            return;
           }
           if (step_all_v) {
             if (live && ok == 2) {
@@ -192,43 +208,50 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
               if constexpr (F8) {
                 float y[8];
                 uint8_t* dst = static_cast<uint8_t*>(p.v_cache) + e0;
-                unpack_bf16x8(raw_a[k], y);
+                unpack_bf16x8(xa, y);
                 *reinterpret_cast<uint2*>(dst) = e4m3x8(y, p.inv_v);
-                unpack_bf16x8(raw_b[k], y);
+                unpack_bf16x8(xb, y);
                 *reinterpret_cast<uint2*>(dst + H2) = e4m3x8(y, p.inv_v);
               } else {
                 uint16_t* dst = static_cast<uint16_t*>(p.v_cache) + e0;
-                *reinterpret_cast<uint4*>(dst) = raw_a[k];
-                *reinterpret_cast<uint4*>(dst + H2) = raw_b[k];
+                *reinterpret_cast<uint4*>(dst) = xa;
+                *reinterpret_cast<uint4*>(dst + H2) = xb;
               }
             }
-            continue;
+            return;
           }
           float ra[8], rb[8];
-          norm_rope_pair<D>(raw_a[k], raw_b[k], is_q ? qw[0] : kw[0], is_q ? qw[1] : kw[1], cs, sn, p.eps, ra, rb);
+          const bool with_k = hd0 + (base + k) * HPI + HPI > p.Hq;  // step-uniform
+          if constexpr (F4) {
+            if (with_k)
+              norm_rope_pair_fine<D>(xa, xb, is_q ? qw[0] : kw[0], is_q ? qw[1] : kw[1], cs2, sn2, p.eps, ra, rb);
+            else
+              norm_rope_pair<D>(xa, xb, qw[0], qw[1], cs, sn, p.eps, ra, rb);
+          } else {
+            norm_rope_pair<D>(xa, xb, is_q ? qw[0] : kw[0], is_q ? qw[1] : kw[1], cs, sn, p.eps, ra, rb);
+          }
           if constexpr (F4) {  // K heads, and V heads in a step that they share (all lanes: it shuffles)
-            const int first = hd0 + (base + k) * HPI;  // step-uniform
-            if (first + HPI > p.Hq) {
+            if (with_k) {
               const int kvh = live ? hd - (is_v ? p.Hq + p.Hkv : p.Hq) : 0;
               const int64_t at = kvh > 0 ? kvh : 0;
-              float xa[8], xb[8];
+              float fa[8], fb[8];
               if (is_v) {
-                unpack_bf16x8(raw_a[k], xa);
-                unpack_bf16x8(raw_b[k], xb);
+                unpack_bf16x8(xa, fa);
+                unpack_bf16x8(xb, fb);
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  xa[e] = ra[e];
-                  xb[e] = rb[e];
+                  fa[e] = ra[e];
+                  fb[e] = rb[e];
                 }
               }
-              store_e2m1_pair<D>(xa, xb, is_v ? p.inv_v : p.inv_k, live && !is_q && ok == 2, li,
+              store_e2m1_pair<D>(fa, fb, is_v ? p.inv_v : p.inv_k, live && !is_q && ok == 2, li,
                                  static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + (slot * p.Hkv + at) * (D / 2),
                                  (is_v ? p.v_block_scale : p.k_block_scale) + (at * p.kv.num_slots + slot) * (D / 16));
             }
-            if (!is_q) continue;
+            if (!is_q) return;
           }
-          if (!live) continue;
+          if (!live) return;
           const int64_t e0 = cache_row + (int64_t)(hd - (is_v ? p.Hq + p.Hkv : p.Hq)) * D;
           if (F8 && !is_q) {
             if (ok == 2) {
@@ -236,19 +259,19 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
               const float r = is_v ? p.inv_v : p.inv_k;
               float ya[8], yb[8];
               if (is_v) {
-                unpack_bf16x8(raw_a[k], ya);
-                unpack_bf16x8(raw_b[k], yb);
+                unpack_bf16x8(xa, ya);
+                unpack_bf16x8(xb, yb);
               }
               *reinterpret_cast<uint2*>(dst) = e4m3x8(is_v ? ya : ra, r);
               *reinterpret_cast<uint2*>(dst + H2) = e4m3x8(is_v ? yb : rb, r);
             }
-            continue;
+            return;
           }
           // the prepared Q is f16 next to a cache of codes (the prefill kernel's operand type), else bf16
           uint4 va, vb;
           if (is_v) {
-            va = raw_a[k];
-            vb = raw_b[k];
+            va = xa;
+            vb = xb;
           } else if (F8 || F4) {
             va = make_uint4(pack_f16(ra[0], ra[1]), pack_f16(ra[2], ra[3]), pack_f16(ra[4], ra[5]), pack_f16(ra[6], ra[7]));
             vb = make_uint4(pack_f16(rb[0], rb[1]), pack_f16(rb[2], rb[3]), pack_f16(rb[4], rb[5]), pack_f16(rb[6], rb[7]));
@@ -263,6 +286,26 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           if (is_q || ok == 2) {
             *reinterpret_cast<uint4*>(dst) = va;
             *reinterpret_cast<uint4*>(dst + H2) = vb;
+          }
+        };
+        if constexpr (F4) {
+          // One copy of the (long) body, the batch shifted through its first place:
+          // unrolled it overflows the instruction cache (prepare of the Qwen3-4B
+          // prefill: 83 us with two copies, 115 us with four, 70 us so).
+#pragma unroll 1
+          for (int k = 0; k < kBatch && base + k < s_end; ++k) {
+            step(k, raw_a[0], raw_b[0]);
+#pragma unroll
+            for (int e = 0; e + 1 < kBatch; ++e) {
+              raw_a[e] = raw_a[e + 1];
+              raw_b[e] = raw_b[e + 1];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            if (base + k >= s_end) break;  // warp-uniform
+            step(k, raw_a[k], raw_b[k]);
           }
         }
       }

@@ -125,6 +125,19 @@ def test_prefill_and_mixed(hq, hkv, d, lens, cache, ps, df):
     check_out(w, host, cache_of(ds), ds.out)
 
 
+@pytest.mark.parametrize("hq,hkv,d,ps", [(16, 8, 128, 0), (8, 8, 64, 64)])
+def test_prefill_of_many_short_requests(hq, hkv, d, ps):
+    """Several work items per CTA, most of them of one key tile: the warps that
+    fetch tiles ahead must not wait for an item that is only handed out once the
+    fetched tiles are computed."""
+    lens = [1 + (7 * i) % 60 for i in range(160)]
+    cache = [(13 * i) % 90 for i in range(160)]
+    w = gen.custom(f"short4_{d}", hq, hkv, d, lens, cache, seed=d, decode_from=160)
+    host = gen.make_inputs(w, page_size=ps, kv_dtype="e2m1", k_scale=KS, v_scale=VS)
+    ds = run(w, host)
+    check_out(w, host, ds.kv_prefill, ds.out)
+
+
 @pytest.mark.parametrize("hq,hkv,d,cache,ps", [
     (32, 8, 128, [0, 5, 63, 64, 700, 3000, 9000], 0),
     (4, 2, 64, [12, 300], 0),
