@@ -124,21 +124,24 @@ def _check(rc: int) -> None:
         raise AttnError(rc, load().attn_strerror(rc).decode())
 
 
+# Addresses and streams go to ctypes as plain integers (the argument types say
+# what they are): an object less per argument on calls that take microseconds.
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # The current stream's handle without building a torch Stream object per call
 # (a few microseconds on every launch); torch.cuda.current_stream() otherwise.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None):
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     if _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def config(num_q_heads: int, num_kv_heads: int, head_dim: int, rms_eps: float = 1e-6,
@@ -170,6 +173,7 @@ class KVCache:
         object.__setattr__(self, name, value)
         if name != "_built":
             object.__setattr__(self, "_built", None)
+            object.__setattr__(self, "_built_pages", None)
 
     def struct(self) -> AttnKV:
         built = self.__dict__.get("_built")
@@ -206,6 +210,21 @@ class KVCache:
                       self.slot_capacity.data_ptr(), pt, ps, ppr,
                       ATTN_KV_E2M1 if fp4 else ATTN_KV_E4M3 if fp8 else ATTN_KV_BF16, float(self.k_scale),
                       float(self.v_scale), kbs.data_ptr() if fp4 else None, vbs.data_ptr() if fp4 else None)
+
+    def pages_struct(self, ref_count: torch.Tensor) -> AttnPages:
+        """The pool's bookkeeping for the page calls: this cache's page table and
+        cached lengths (which they write) and the pages' reference counts.  Built
+        and checked like struct(), and again for another ref_count."""
+        built = self.__dict__.get("_built_pages")
+        if built is None or built[0] is not ref_count:
+            assert self.page_table is not None and self.page_size > 0, "the cache is not paged"
+            n = int(self.page_table.shape[0])
+            assert ref_count.numel() >= self.k_cache.shape[0] // self.page_size, "ref_count"
+            assert self.cache_lens.numel() >= n, "cache_lens"
+            built = (ref_count, AttnPages(_i32(self.page_table, "page_table"), _i32(ref_count, "ref_count"),
+                                          _i32(self.cache_lens, "cache_lens"), n))
+            object.__setattr__(self, "_built_pages", built)
+        return built[1]
 
     def rows(self, lo: int, hi: int, cache_lens: torch.Tensor | None = None) -> "KVCache":
         """The same cache seen by the requests [lo, hi) (with other cached
@@ -266,6 +285,11 @@ def new_workspace(cfg: AttnConfig, max_tokens: int, max_batch: int, max_kv_len: 
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     _check(load().attn_workspace_init(_ptr(ws), n, _stream()))
     return ws
+
+
+def _i32(t, name):
+    assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), name
+    return t.data_ptr()
 
 
 def _bf16(t, name):
@@ -399,27 +423,11 @@ def new_pages_workspace(kv: KVCache, max_rows: int | None = None) -> torch.Tenso
     return ws
 
 
-def _i32(t, name):
-    assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), name
-    return ctypes.c_void_p(t.data_ptr())
-
-
-def _pages(kv: KVCache, ref_count) -> AttnPages:
-    """The pool's bookkeeping: ``kv``'s page table and cached lengths (written
-    by the page calls) and the pages' reference counts."""
-    assert kv.page_table is not None and kv.page_size > 0, "the cache is not paged"
-    rows = int(kv.page_table.shape[0])
-    assert ref_count.numel() >= kv.k_cache.shape[0] // kv.page_size, "ref_count"
-    assert kv.cache_lens.numel() >= rows, "cache_lens"
-    return AttnPages(_i32(kv.page_table, "page_table"), _i32(ref_count, "ref_count"),
-                     _i32(kv.cache_lens, "cache_lens"), rows)
-
-
 def pages_reserve(kv: KVCache, ref_count, rows, new_tokens, workspace, stream=None):
     """Room for new_tokens[i] more entries in request rows[i] (int32 device
     tensors): the lowest free pages into the open entries of kv.page_table."""
     assert rows.numel() == new_tokens.numel(), "new_tokens"
-    s, p = kv.struct(), _pages(kv, ref_count)
+    s, p = kv.struct(), kv.pages_struct(ref_count)
     _check(load().attn_pages_reserve(ctypes.byref(s), ctypes.byref(p), _i32(rows, "rows"),
                                      _i32(new_tokens, "new_tokens"), rows.numel(), _ptr(workspace), workspace.numel(),
                                      _stream(stream)))
@@ -429,7 +437,7 @@ def pages_fork(cfg: AttnConfig, kv: KVCache, ref_count, src_rows, dst_rows, work
     """Row dst_rows[i] becomes a copy of the request in row src_rows[i]: full
     pages shared, the open one copied."""
     assert src_rows.numel() == dst_rows.numel(), "dst_rows"
-    s, p = kv.struct(), _pages(kv, ref_count)
+    s, p = kv.struct(), kv.pages_struct(ref_count)
     _check(load().attn_pages_fork(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _i32(src_rows, "src_rows"),
                                   _i32(dst_rows, "dst_rows"), src_rows.numel(), _ptr(workspace), workspace.numel(),
                                   _stream(stream)))
@@ -438,7 +446,7 @@ def pages_fork(cfg: AttnConfig, kv: KVCache, ref_count, src_rows, dst_rows, work
 def pages_free(kv: KVCache, ref_count, rows, workspace, stream=None):
     """The requests in ``rows`` end: their pages lose a reference, the rows are
     emptied."""
-    s, p = kv.struct(), _pages(kv, ref_count)
+    s, p = kv.struct(), kv.pages_struct(ref_count)
     _check(load().attn_pages_free(ctypes.byref(s), ctypes.byref(p), _i32(rows, "rows"), rows.numel(),
                                   _ptr(workspace), workspace.numel(), _stream(stream)))
 
@@ -455,7 +463,7 @@ def pages_copy(cfg: AttnConfig, kv: KVCache, src_pages, dst_pages, workspace, st
 def pages_compact(cfg: AttnConfig, kv: KVCache, ref_count, workspace, stream=None):
     """Moves the pages in use to the front of the pool; kv.page_table and
     ``ref_count`` follow."""
-    s, p = kv.struct(), _pages(kv, ref_count)
+    s, p = kv.struct(), kv.pages_struct(ref_count)
     _check(load().attn_pages_compact(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _ptr(workspace),
                                      workspace.numel(), _stream(stream)))
 

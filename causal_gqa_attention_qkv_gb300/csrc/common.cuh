@@ -431,6 +431,7 @@ struct RopeAxes {
   int64_t ld;
   uint32_t axis[4];          // axis of pair i: bits 2 (i % 16), 2 (i % 16) + 1 of word i / 16
   int32_t num_axes;
+  uint32_t used;             // bit a: some pair takes axis a
 };
 struct AxisPos {
   const RopeAxes& ax;
@@ -440,10 +441,18 @@ struct AxisPos {
     return (float)__ldg(ax.positions + (int64_t)a * ax.ld + token);
   }
 };
-// Every position of the token lies in [0, 2^24] (exact in fp32).
+// Positions that a lane of a warp holds for its own pairs N lane .. N lane + N - 1.
+template <int N>
+struct LanePos {
+  float pos[N];
+  __device__ __forceinline__ float operator()(int pair) const { return pos[pair & (N - 1)]; }
+};
+constexpr uint32_t kMaxPosition = 1u << 24;  // exact in fp32
+// Every position of the token, on the axes that have pairs, lies in [0, 2^24].
 __device__ __forceinline__ bool axes_in_range(const RopeAxes& ax, int64_t token) {
   bool ok = true;
-  for (int a = 0; a < ax.num_axes; ++a) ok = ok && (uint32_t)__ldg(ax.positions + a * ax.ld + token) <= (1u << 24);
+  for (int a = 0; a < ax.num_axes; ++a)
+    if (ax.used >> a & 1) ok = ok && (uint32_t)__ldg(ax.positions + a * ax.ld + token) <= kMaxPosition;
   return ok;
 }
 

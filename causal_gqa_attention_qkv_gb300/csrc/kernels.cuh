@@ -54,6 +54,7 @@ inline RopeAxes rope_axes(const attn_rope_axes_t* rope, int head_dim) {
       --left;
     }
     x.axis[i >> 4] |= (uint32_t)a << (2 * (i & 15));
+    x.used |= 1u << a;
   }
   return x;
 }

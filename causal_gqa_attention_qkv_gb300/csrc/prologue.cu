@@ -63,8 +63,9 @@ struct ProloguePar {
 // HPI runs of 128 contiguous bytes and each store writes whole runs.  cos/sin
 // of the token's D/2 rotation angles are computed once (D/64 per lane) and
 // handed to the lanes that need them with shuffles.  KV: the cache's element
-// type (ATTN_KV_*).
-template <int D, int KV>
+// type (ATTN_KV_*).  Axes: rotary positions with several axes; a lane holds the
+// positions of its own D/64 pairs, read one token ahead.
+template <int D, int KV, bool Axes>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const ProloguePar p) {
   constexpr int L = D / 16;     // lanes per head vector
   constexpr int HPI = 32 / L;   // head vectors per warp-wide step
@@ -99,6 +100,17 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
   if (u0 >= u_end) return;
   int t = (int)(u0 / nstep);
   int s_begin = (int)(u0 - (int64_t)t * nstep);
+  constexpr int PPL = D / 64;
+  int32_t next_pos[PPL];  // Axes: positions of the coming token
+  auto load_positions = [&](int token) {
+#pragma unroll
+    for (int e = 0; e < PPL; ++e) {
+      const int pair = lane * PPL + e;
+      const uint32_t a = (p.axes.axis[pair >> 4] >> (2 * (pair & 15))) & 3u;
+      next_pos[e] = __ldg(p.axes.positions + (int64_t)a * p.axes.ld + token);
+    }
+  };
+  if constexpr (Axes) load_positions(t);
   for (;;) {
     const int s_end = (int)min((int64_t)nstep, s_begin + (u_end - u0));
     const uint16_t* row = p.qkv + (int64_t)t * W + (int64_t)hd0 * D + li * 8;
@@ -146,10 +158,19 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           set_status(p.status, ATTN_STATUS_CAPACITY);
       }
     }
-    const bool with_axes = p.axes.positions != nullptr;  // kernel-uniform
-    if (with_axes && ok != 0 && !axes_in_range(p.axes, t)) {
-      ok = 0;
-      if (lane == 0) set_status(p.status, ATTN_STATUS_POSITION);
+    LanePos<PPL> own;
+    if constexpr (Axes) {
+      bool in_range = true;
+#pragma unroll
+      for (int e = 0; e < PPL; ++e) {
+        own.pos[e] = (float)next_pos[e];
+        in_range = in_range && (uint32_t)next_pos[e] <= kMaxPosition;
+      }
+      if (u_end - u0 > s_end - s_begin) load_positions(t + 1);
+      if (!__all_sync(0xffffffffu, in_range) && ok != 0) {
+        ok = 0;
+        if (lane == 0) set_status(p.status, ATTN_STATUS_POSITION);
+      }
     }
     if (ok != 0) {  // warp-uniform
 
@@ -168,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
           pair_angles<D>(at, p.freqs, lane, cs, sn);
         }
       };
-      if (with_axes) angles(AxisPos{p.axes, t});
+      if constexpr (Axes) angles(own);
       else angles(OnePos{pos});
       uint16_t* q_row = with_q ? p.q_out + (int64_t)t * p.Hq * D + li * 8 : nullptr;
       const int64_t cache_row = slot * p.Hkv * D + li * 8;
@@ -317,6 +338,18 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const P
   }
 }
 
+template <bool Axes>
+void launch_kv(int kv_dtype, int head_dim, const ProloguePar& p, dim3 grid, cudaStream_t stream) {
+  switch (kv_dtype * 2 + (head_dim == 128)) {
+    case ATTN_KV_BF16 * 2: kv_append_kernel<64, ATTN_KV_BF16, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_BF16 * 2 + 1: kv_append_kernel<128, ATTN_KV_BF16, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E4M3 * 2: kv_append_kernel<64, ATTN_KV_E4M3, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E4M3 * 2 + 1: kv_append_kernel<128, ATTN_KV_E4M3, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+    case ATTN_KV_E2M1 * 2: kv_append_kernel<64, ATTN_KV_E2M1, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+    default: kv_append_kernel<128, ATTN_KV_E2M1, Axes><<<grid, kThreads, 0, stream>>>(p); break;
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream) {
@@ -358,14 +391,8 @@ cudaError_t launch_prologue(const PrologueArgs& a, cudaStream_t stream) {
   p.steps_per_warp = (units + resident - 1) / resident;
   const int64_t warps = (units + p.steps_per_warp - 1) / p.steps_per_warp;
   const dim3 grid((unsigned)((warps + kWarpsPerBlock - 1) / kWarpsPerBlock));
-  switch (a.kv.kv_dtype * 2 + (a.cfg.head_dim == 128)) {
-    case ATTN_KV_BF16 * 2: kv_append_kernel<64, ATTN_KV_BF16><<<grid, kThreads, 0, stream>>>(p); break;
-    case ATTN_KV_BF16 * 2 + 1: kv_append_kernel<128, ATTN_KV_BF16><<<grid, kThreads, 0, stream>>>(p); break;
-    case ATTN_KV_E4M3 * 2: kv_append_kernel<64, ATTN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p); break;
-    case ATTN_KV_E4M3 * 2 + 1: kv_append_kernel<128, ATTN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p); break;
-    case ATTN_KV_E2M1 * 2: kv_append_kernel<64, ATTN_KV_E2M1><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv_append_kernel<128, ATTN_KV_E2M1><<<grid, kThreads, 0, stream>>>(p); break;
-  }
+  if (a.axes.positions) launch_kv<true>(a.kv.kv_dtype, a.cfg.head_dim, p, grid, stream);
+  else launch_kv<false>(a.kv.kv_dtype, a.cfg.head_dim, p, grid, stream);
   return cudaGetLastError();
 }
 

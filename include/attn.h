@@ -159,7 +159,7 @@ enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1, ATTN_KV_E2M1 = 2 };
  * section[] sums to D / 2 (interleaved: and every axis > 0 finds its
  * section[a] pairs below D / 2).  positions: int32 [A, ld] on the device,
  * positions[a * ld + t] the position of token t (row t of qkv) on axis a, each
- * in [0, 2^24].  Only the rotation angles come from here: slots, lengths and
+ * in [0, 2^24] (the positions of an axis without pairs do not matter).  Only the rotation angles come from here: slots, lengths and
  * the causal limit go by the cache as in the calls without axes.  A token with
  * a position outside the range sets ATTN_STATUS_POSITION; its K and V are not
  * appended and its prepared Q (decode: its output row) is left unwritten. */
