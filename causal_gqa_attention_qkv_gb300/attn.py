@@ -213,18 +213,18 @@ class KVCache:
 
     def pages_struct(self, ref_count: torch.Tensor) -> AttnPages:
         """The pool's bookkeeping for the page calls: this cache's page table and
-        cached lengths (which they write) and the pages' reference counts.  Built
-        and checked like struct(), and again for another ref_count."""
+        cached lengths (which they write; checked once, like struct()) and the
+        pages' reference counts."""
         built = self.__dict__.get("_built_pages")
-        if built is None or built[0] is not ref_count:
+        if built is None:
             assert self.page_table is not None and self.page_size > 0, "the cache is not paged"
             n = int(self.page_table.shape[0])
-            assert ref_count.numel() >= self.k_cache.shape[0] // self.page_size, "ref_count"
             assert self.cache_lens.numel() >= n, "cache_lens"
-            built = (ref_count, AttnPages(_i32(self.page_table, "page_table"), _i32(ref_count, "ref_count"),
-                                          _i32(self.cache_lens, "cache_lens"), n))
+            built = (_i32(self.page_table, "page_table"), _i32(self.cache_lens, "cache_lens"), n,
+                     self.k_cache.shape[0] // self.page_size)
             object.__setattr__(self, "_built_pages", built)
-        return built[1]
+        assert ref_count.numel() >= built[3], "ref_count"
+        return AttnPages(built[0], _i32(ref_count, "ref_count"), built[1], built[2])
 
     def rows(self, lo: int, hi: int, cache_lens: torch.Tensor | None = None) -> "KVCache":
         """The same cache seen by the requests [lo, hi) (with other cached

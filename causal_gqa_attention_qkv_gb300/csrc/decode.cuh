@@ -116,7 +116,9 @@ __device__ __forceinline__ void append_new_kv(const DecodePar& p, const ReqInfo&
 template <int D, int KV, bool Axes>
 __device__ __forceinline__ bool decode_begin(const DecodePar& p, int split, int kh, int b, ReqInfo* req, int* k0,
                                              int* k1, int* splits) {
-  const ReqInfo r = load_request(p.kv, b, 1);  // request facts: written by the caller, not by a kernel
+  // Request facts: written by the caller, or by a page call, whose last kernel lets
+  // no dependent start before it has completed.
+  const ReqInfo r = load_request(p.kv, b, 1);
   const bool append = p.k_norm_w != nullptr;
   if (!r.valid) {  // nothing written (with the append kernel before this one: flagged there)
     if (append && split == 0 && kh == 0 && threadIdx.x == 0) set_status(p.status, ATTN_STATUS_CAPACITY);

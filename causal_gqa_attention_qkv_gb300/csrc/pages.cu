@@ -113,7 +113,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   const int gwarp = (int)rank * kPlanWarps + warp, nwarps = kCluster * kPlanWarps;
-  launch_dependents();
+  // The copy kernel of the same call may start early: it waits before it reads.  A
+  // reservation is followed by kernels that read the caller's tables and lengths as
+  // settled (some before their wait), so they start when it has completed.
+  if constexpr (OP != kReserve) launch_dependents();
   grid_dependency_wait();
   // this warp's run of pages
   const int run = ((p.num_pages + nwarps - 1) / nwarps + 31) & ~31;
@@ -338,6 +341,7 @@ struct CopyPar {
   int32_t* status;
 };
 
+// No kernel below lets its dependents start early (see plan_kernel).
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPar p) {
   const int i = blockIdx.x / p.units, u = blockIdx.x % p.units;
   grid_dependency_wait();

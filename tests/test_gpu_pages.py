@@ -438,3 +438,105 @@ def test_serving_loop(kind, axes):
     attn.pages_free(kv, ref, i32([0, 1, 3, 4, 5]), ws)
     assert (ref == 0).all() and (kv.page_table == -1).all()
     assert attn.get_status(ws) == 0 and attn.get_status(aws) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e2m1"])
+def test_a_captured_step_of_reserve_and_decode_crosses_pages(kind):
+    """Reserve, decode over the pool's own rows and the lengths' increment, recorded
+    once: replayed across page boundaries right behind a fork and a free, every
+    output equals the one over contiguous caches bit for bit."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    hq, hkv, d, ps, rows, ppr, steps = 4, 2, 128, 64, 4, 5, 140
+    pool = Pool(kind, 24, ps, hkv, d, [], rows, ppr, seed=6)
+    cfg, kv, ws = attn.config(hq, hkv, d), pool.kv, pool.ws
+    W, S = (hq + 2 * hkv) * d, ppr * ps
+    g = torch.Generator().manual_seed(12)
+    qw, kw = [(1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2)]
+    new = lambda n: torch.randn(n, W, generator=g).bfloat16().cuda()
+    aws = attn.new_workspace(cfg, 256, rows, S)
+    lens = [63, 100, 0, 0]
+    blocks = [None, None]
+    if kind == "e2m1":
+        blocks = [torch.zeros(hkv, rows * S, d // 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    like = lambda t: torch.zeros(rows * S, *t.shape[1:], dtype=torch.uint8, device="cuda").view(t.dtype) \
+        if t.dtype == torch.uint8 else torch.zeros(rows * S, *t.shape[1:], dtype=t.dtype, device="cuda")
+    flat = attn.KVCache(like(kv.k_cache), like(kv.v_cache), torch.arange(0, rows * S, S, device="cuda"),
+                        torch.zeros(rows, dtype=torch.int32, device="cuda"), kv.slot_capacity.clone(), None, 0, 0.03,
+                        0.06, *blocks)
+    prompts = new(163)
+    cu = i32([0, 63, 163])
+    attn.pages_reserve(kv, pool.ref, i32([0, 1]), i32([63, 100]), ws)
+    for c in (kv, flat):
+        out = torch.empty(163, hq * d, dtype=torch.bfloat16, device="cuda")
+        attn.prefill(cfg, prompts, qw, kw, cu, 100, c.rows(0, 2), out, aws)
+        c.cache_lens[:2] += i32([63, 100])
+    for s, t in ((0, 2), (1, 3)):  # what the fork below does, by copies
+        flat.k_cache[t * S:t * S + S] = flat.k_cache[s * S:s * S + S]
+        flat.v_cache[t * S:t * S + S] = flat.v_cache[s * S:s * S + S]
+        for b in blocks:
+            if b is not None:
+                b[:, t * S:t * S + S] = b[:, s * S:s * S + S].clone()
+        flat.cache_lens[t] = flat.cache_lens[s]
+    every, ones = i32(list(range(rows))), i32([1] * rows)
+    qkv, out = new(rows), torch.empty(rows, hq * d, dtype=torch.bfloat16, device="cuda")
+    attn.pages_fork(cfg, kv, pool.ref, i32([0, 1]), i32([2, 3]), ws)
+
+    def step():
+        attn.pages_reserve(kv, pool.ref, every, ones, ws)
+        attn.decode(cfg, qkv, qw, kw, S - 1, kv, out, aws)
+        kv.cache_lens.add_(1)
+
+    step()  # eager, straight behind the fork
+    want = torch.empty_like(out)
+    attn.decode(cfg, qkv, qw, kw, S - 1, flat, want, aws)
+    flat.cache_lens.add_(1)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(steps):
+        qkv.copy_(new(rows))
+        if i == steps // 2:  # two requests end, another is forked into their place
+            attn.pages_free(kv, pool.ref, i32([2, 3]), ws)
+            attn.pages_fork(cfg, kv, pool.ref, i32([1, 0]), i32([2, 3]), ws)
+            for s, t in ((1, 2), (0, 3)):
+                flat.k_cache[t * S:t * S + S] = flat.k_cache[s * S:s * S + S]
+                flat.v_cache[t * S:t * S + S] = flat.v_cache[s * S:s * S + S]
+                for b in blocks:
+                    if b is not None:
+                        b[:, t * S:t * S + S] = b[:, s * S:s * S + S].clone()
+                flat.cache_lens[t] = flat.cache_lens[s]
+        graph.replay()
+        attn.decode(cfg, qkv, qw, kw, S - 1, flat, want, aws)
+        flat.cache_lens.add_(1)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), i
+    assert torch.equal(kv.cache_lens, flat.cache_lens)
+    assert attn.get_status(ws) == 0 and attn.get_status(aws) == 0
+
+
+def test_two_pools_on_two_streams_at_once():
+    """Calls on different pools, each with its own workspace, do not meet."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    make = lambda seed: Pool("e2m1", 300, 64, 2, 128, [500, 77, 640, 3], 12, 12, seed=seed)
+
+    def calls(pool):
+        attn.pages_fork(pool.cfg, pool.kv, pool.ref, lists[0], lists[1], pool.ws)
+        attn.pages_free(pool.kv, pool.ref, lists[2], pool.ws)
+        attn.pages_reserve(pool.kv, pool.ref, lists[3], lists[4], pool.ws)
+        attn.pages_compact(pool.cfg, pool.kv, pool.ref, pool.ws)
+
+    lists = [i32(x) for x in ([0, 1, 1, 3], [4, 5, 6, 7], [0, 6], [4, 8, 1], [70, 129, 1])]
+    want = []
+    for seed in (21, 22):
+        pool = make(seed)
+        calls(pool)
+        want.append(pool.state())
+    pools, streams = [make(21), make(22)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for pool, s in zip(pools, streams):
+        with torch.cuda.stream(s):
+            calls(pool)
+    torch.cuda.synchronize()
+    for pool, w in zip(pools, want):
+        assert pool.status() == 0
+        same(pool.state(), w)
