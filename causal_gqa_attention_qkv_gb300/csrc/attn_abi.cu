@@ -244,7 +244,7 @@ size_t q_stage_bytes(const attn_config_t* cfg, int64_t N) {
 
 size_t decode_ws_need(const attn_config_t* cfg, int32_t B, int32_t max_cache_len, int* split_len,
                       int* max_splits) {
-  *split_len = decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, max_splits);
+  *split_len = decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, max_splits, false);
   return kWsHeader + partial_bytes(*cfg, B, *max_splits);
 }
 
@@ -253,8 +253,9 @@ size_t decode_ws_need(const attn_config_t* cfg, int32_t B, int32_t max_cache_len
 int decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_w, const void* k_norm_w,
                   int32_t B, int32_t max_cache_len, const attn_kv_t* kv, const attn_rope_axes_t* rope,
                   void* out, void* workspace, cudaStream_t s) {
-  int split_len = 0, max_splits = 1;
-  decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits);
+  int max_splits = 1;
+  const int split_len = decode_split_len(B, cfg->num_kv_heads, max_cache_len + 1, &max_splits,
+                                         rope != nullptr || kv->kv_dtype == ATTN_KV_E2M1);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t rows = (size_t)B * cfg->num_q_heads * max_splits;
   DecodeArgs d;
@@ -294,7 +295,7 @@ size_t attn_workspace_size(const attn_config_t* cfg, int32_t max_tokens, int32_t
 int32_t attn_decode_splits(const attn_config_t* cfg, int32_t B, int32_t max_cache_len) {
   if (check_config(cfg) != ATTN_OK || B < 0 || max_cache_len < 0) return ATTN_EINVAL;
   int max_splits = 1;
-  decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits);
+  decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits, false);
   return max_splits;
 }
 

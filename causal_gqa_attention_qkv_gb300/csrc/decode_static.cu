@@ -64,7 +64,7 @@ extern "C" int attn_decode_static_scratch(const attn_config_t* cfg, const void* 
     return ATTN_EINVAL;
   int max_splits = 1;
   const int split_len =
-      decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits);
+      decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits, kv->kv_dtype == ATTN_KV_E2M1);
   // With one split per request the split kernel writes `out` directly and no
   // partial result is stored: such calls need no scratch at all.
   const size_t rows = (size_t)B * cfg->num_q_heads * max_splits;

@@ -142,7 +142,7 @@ struct DecodeArgs {
   int32_t split_len, max_splits;
   int32_t* status;
 };
-int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits);
+int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits, bool longer);
 int launch_decode(const DecodeArgs& a, cudaStream_t stream);
 int launch_decode_e2m1(const DecodeArgs& a, cudaStream_t stream);  // the split kernel over an E2M1 cache
 

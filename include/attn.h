@@ -159,10 +159,11 @@ enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1, ATTN_KV_E2M1 = 2 };
  * section[] sums to D / 2 (interleaved: and every axis > 0 finds its
  * section[a] pairs below D / 2).  positions: int32 [A, ld] on the device,
  * positions[a * ld + t] the position of token t (row t of qkv) on axis a, each
- * in [0, 2^24] (the positions of an axis without pairs do not matter).  Only the rotation angles come from here: slots, lengths and
- * the causal limit go by the cache as in the calls without axes.  A token with
- * a position outside the range sets ATTN_STATUS_POSITION; its K and V are not
- * appended and its prepared Q (decode: its output row) is left unwritten. */
+ * in [0, 2^24] (the positions of an axis without pairs do not matter).  Only
+ * the rotation angles come from here: slots, lengths and the causal limit go
+ * by the cache as in the calls without axes.  A token with a position outside
+ * the range sets ATTN_STATUS_POSITION; its K and V are not appended and its
+ * prepared Q (decode: its output row) is left unwritten. */
 typedef struct attn_rope_axes {
   int32_t num_axes;     /* A: 1 .. 4 */
   int32_t section[4];   /* rotation pairs per axis */
@@ -285,10 +286,10 @@ ATTN_API int attn_qkv_proj_prepare(const attn_config_t* cfg, const void* hidden,
  * and results with the angles of `rope` (host struct; NULL: the position
  * c_b + j on every pair, i.e. the call without _axes).  attn_prefill_attend
  * takes the prepared Q of either form.  attn_decode_axes and
- * attn_decode_attend_axes over a bf16 cache keep Q and the softmax probabilities
- * to about 16 bits where the calls without axes round them to bf16.  An image's tokens share or repeat
- * positions, so the positions of a request's next tokens are the caller's to
- * continue. */
+ * attn_decode_attend_axes over a bf16 cache keep Q and the softmax
+ * probabilities to about 16 bits where the calls without axes round them to
+ * bf16.  An image's tokens share or repeat positions, so the positions of a
+ * request's next tokens are the caller's to continue. */
 ATTN_API int attn_kv_append_axes(const attn_config_t* cfg, const void* qkv, const void* k_norm_w,
                                  const int32_t* cu_seqlens, int32_t B, int32_t N, const attn_kv_t* kv,
                                  const attn_rope_axes_t* rope, void* workspace, size_t ws_bytes,
@@ -344,6 +345,8 @@ ATTN_API int attn_o_proj(const attn_config_t* cfg, const void* attn_out, int32_t
  * about 2048 CTAs run when every request is at its longest, with at least 256
  * keys and at most 16 splits per request.  1 means every output row is
  * written by the split kernel directly (no partials, no merge launch).
+ * Over an E2M1 cache and with rotary axes a split has at least
+ * min(2048, 8 B Hkv) keys besides, so there the number is an upper bound.
  * Returns ATTN_EINVAL (< 0) for invalid arguments.  Host-only. */
 ATTN_API int32_t attn_decode_splits(const attn_config_t* cfg, int32_t B, int32_t max_cache_len);
 
