@@ -184,27 +184,30 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
         slot_now = slot_next;
         slot_next = tile_slot(w0 + 32 + lane);
       }
-      int64_t slot[2] = {__shfl_sync(0xffffffffu, slot_now, 2 * i - w0), __shfl_sync(0xffffffffu, slot_now, 2 * i + 1 - w0)};
       if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
       if (!ok) break;
       if (append && i == npass - 1) append_new_kv<D, ATTN_KV_E2M1, Axes>(p, r, b, kh, lane);
-      const int pos = k0 + i * 2 * kKeysPerTile;
-      const int halves = pos + kKeysPerTile < k1 ? 2 : 1;
+      const int halves = min(2, ntiles - 2 * i);
       const uint32_t stage = smem_u32(smem) + st * Lay::kStageBytes;
-      if (halves == 1) slot[1] = slot[0];
-      if (slot[0] < 0 || slot[1] < 0) {  // a page outside the cache is read from slot 0
+      // Lanes 0 .. 3 issue the copies of K and V (bit 0) of the halves (bit 1): one
+      // lane issuing all eight in turn cost 4 % of the call.
+      const int which = lane & 1, half = (lane >> 1) & 1;
+      const bool issues = lane < 2 * halves;
+      int64_t slot = __shfl_sync(0xffffffffu, slot_now, 2 * i - w0 + half);
+      if (__any_sync(0xffffffffu, issues && slot < 0)) {  // a page outside the cache is read from slot 0
         if (lane == 0) set_status(p.status, ATTN_STATUS_CAPACITY);
-        slot[0] = slot[0] < 0 ? 0 : slot[0];
-        slot[1] = slot[1] < 0 ? 0 : slot[1];
+        if (slot < 0) slot = 0;
       }
-      const uint32_t shift = (uint32_t)((row0 + slot[0]) * SB) & 15u;  // the same for every half of the CTA
+      // the same for every half of the CTA (a half past the end has no slot)
+      const uint32_t shift = (uint32_t)((row0 + __shfl_sync(0xffffffffu, slot, 0)) * SB) & 15u;
       const uint32_t sbytes = kKeysPerTile * SB + (shift ? 16u : 0u);
-      const int64_t at[2] = {(row0 + slot[0]) * SB - shift, (row0 + slot[1]) * SB - shift};
-      const bool bulk = at[0] + sbytes <= end && at[1] + sbytes <= end;  // else past the arrays: key by key
+      const int64_t at = (row0 + slot) * SB - shift;
+      const bool bulk = __all_sync(0xffffffffu, !issues || at + sbytes <= end);  // else past the arrays: key by key
       if (!bulk) {
-        for (int h = 0; h < halves; ++h)
+        for (int h = 0; h < halves; ++h) {
+          const int64_t from = __shfl_sync(0xffffffffu, at, 2 * h) + shift;
           for (int key = lane; key < kKeysPerTile; key += 32) {
-            const int64_t a = at[h] + shift + key * SB;
+            const int64_t a = from + key * SB;
             const bool in = a + SB <= end;
             const uint32_t dst = stage + h * Lay::kScaleBytes + shift + key * SB;
             for (uint32_t w = 0; w < SB; w += 4) {
@@ -214,22 +217,18 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + Lay::kVs + w), "r"(y) : "memory");
             }
           }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later bulk copy to the same place
         __syncwarp();  // before the arrival below
       }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], halves * 2 * (Lay::kTileBytes + (bulk ? sbytes : 0)));
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (h < halves) {
-            uint8_t* kt = smem + st * Lay::kStageBytes + h * Lay::kTileBytes;
-            tma_load_3d(kt, &kmap, &full[st], 0, kh, (int)slot[h]);
-            tma_load_3d(kt + Lay::kV, &vmap, &full[st], 0, kh, (int)slot[h]);
-            if (bulk) {
-              bulk_load(stage + Lay::kKs + h * Lay::kScaleBytes, p.k_block_scale + at[h], sbytes, &full[st]);
-              bulk_load(stage + Lay::kVs + h * Lay::kScaleBytes, p.v_block_scale + at[h], sbytes, &full[st]);
-            }
-          }
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], halves * 2 * (Lay::kTileBytes + (bulk ? sbytes : 0)));
+      __syncwarp();
+      if (issues) {
+        tma_load_3d(smem + st * Lay::kStageBytes + (which ? Lay::kV : 0) + half * Lay::kTileBytes,
+                    which ? &vmap : &kmap, &full[st], 0, kh, (int)slot);
+        if (bulk)
+          bulk_load(stage + (which ? Lay::kVs : Lay::kKs) + half * Lay::kScaleBytes,
+                    (which ? p.v_block_scale : p.k_block_scale) + at, sbytes, &full[st]);
       }
       __syncwarp();
       issued = i + 1;
