@@ -540,3 +540,42 @@ def test_two_pools_on_two_streams_at_once():
     for pool, w in zip(pools, want):
         assert pool.status() == 0
         same(pool.state(), w)
+
+
+def test_lists_longer_than_the_plan_has_warps_or_lanes():
+    """Several list entries per warp (more than 32 of them too), a row that asks
+    for more than 32 pages, runs of pages of more than one look, a refusal that only
+    the last row causes, and a list of every row in reverse."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    ps, P, rows, ppr = 64, 40000, 9000, 45
+    rng = np.random.RandomState(9)
+    lens = [int(x) for x in rng.randint(0, 2 * ps, rows)]
+    pool = Pool("bf16", P, ps, 1, 64, lens, rows, ppr, seed=9)
+    st = pool.state()
+    rows_list = list(range(rows))[::-1]
+    more = [int(x) for x in rng.randint(0, 2 * ps, rows)]
+    for b in (0, 17, 4444, 8999):
+        more[rows_list.index(b)] = 40 * ps
+    free = P - int((st[1] > 0).sum())
+    need = sum(-(-(lens[b] + m) // ps) - -(-lens[b] // ps) for b, m in zip(rows_list, more))
+    assert need < free
+    over = more[:-1] + [ppr * ps - lens[0] + 1]  # the last row's length would not fit its table
+    attn.pages_reserve(pool.kv, pool.ref, i32(rows_list), i32(over), pool.ws)
+    assert pool.status() == attn.ATTN_STATUS_PAGES
+    same(pool.state()[:3], st[:3])
+    assert plain_reserve(st, ps, rows_list, more)
+    attn.pages_reserve(pool.kv, pool.ref, i32(rows_list), i32(more), pool.ws)
+    assert pool.status() == 0
+    same(pool.state()[:3], st[:3])
+    gone = rng.permutation(rows)[:4000].tolist()
+    plain_free(st, gone)
+    attn.pages_free(pool.kv, pool.ref, i32(gone), pool.ws)
+    src = [b for b in range(rows) if b not in set(gone)][:1200]  # five forks per warp
+    assert plain_fork(st, ps, src, gone[:1200], 4)
+    attn.pages_fork(pool.cfg, pool.kv, pool.ref, i32(src), i32(gone[:1200]), pool.ws)
+    assert pool.status() == 0
+    same(pool.state(), st)
+    plain_compact(st)
+    attn.pages_compact(pool.cfg, pool.kv, pool.ref, pool.ws)
+    assert pool.status() == 0
+    same(pool.state(), st)
