@@ -361,3 +361,43 @@ def test_host_buffer_prefill_over_four_bits():
     for m in ("k_cache", "v_cache", "k_block_scale", "v_block_scale"):
         assert torch.equal(getattr(a.kv_prefill, m), getattr(b.kv_prefill, m)), m
     check_out(w, host, b.kv_prefill, out)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 64), (3, 3, 64), (16, 2, 128)])
+def test_a_cache_that_ends_with_its_last_request(hq, hkv, d):
+    """No slot behind the last region, odd slot numbers, tiles that reach past the
+    arrays: decode, prefill and gather give the bits of a cache with room behind it."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    lens, new = [5, 71, 200], [1, 66, 3]
+    g = torch.Generator().manual_seed(d + hq)
+    cap = [c + n + 1 for c, n in zip(lens, new)]
+    base = [0, cap[0], cap[0] + cap[1]]
+    T = sum(cap)  # an odd start for the last two, nothing behind the last
+    rand = lambda *s: torch.randint(0, 256, s, generator=g, dtype=torch.uint8)
+    codes, blocks = rand(2, T, hkv, d // 2), torch.randint(0x28, 0x40, (2, hkv, T, d // 16), generator=g, dtype=torch.uint8)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cfg = attn.config(hq, hkv, d)
+    W = (hq + 2 * hkv) * d
+    qkv, one = [torch.randn(n, W, generator=g).bfloat16().cuda() for n in (sum(new), 3)]
+    w = [(1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2)]
+    got = []
+    for S in (T, T + 300):
+        c = torch.full((2, S, hkv, d // 2), 0xFF, dtype=torch.uint8)
+        b = torch.full((2, hkv, S, d // 16), 0x7F, dtype=torch.uint8)
+        c[:, :T], b[:, :, :T] = codes, blocks
+        c, b = c.cuda(), b.cuda()
+        kv = attn.KVCache(c[0], c[1], torch.tensor(base, device="cuda"), i32(lens), i32(cap), None, 0, 0.04, 0.03, b[0].clone(),
+                          b[1].clone())
+        ws = attn.new_workspace(cfg, sum(new), 3, 512)
+        out = torch.empty(sum(new), hq * d, dtype=torch.bfloat16, device="cuda")
+        attn.prefill(cfg, qkv, w[0], w[1], i32([0, 1, 67, 70]), 66, kv, out, ws)
+        kv.cache_lens += i32(new)
+        dec = torch.empty(3, hq * d, dtype=torch.bfloat16, device="cuda")
+        attn.decode(cfg, one, w[0], w[1], 203, kv, dec, ws)
+        k, v = [torch.empty(T, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        attn.kv_gather(cfg, kv, i32([0, base[1], base[2], T]), i32([0, 0, 0]), k, v, ws)
+        assert attn.get_status(ws) == 0
+        got.append([x.view(torch.int16) for x in (out, dec, k, v)])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert torch.isfinite(out).all() and torch.isfinite(dec).all()

@@ -579,3 +579,52 @@ def test_lists_longer_than_the_plan_has_warps_or_lanes():
     attn.pages_compact(pool.cfg, pool.kv, pool.ref, pool.ws)
     assert pool.status() == 0
     same(pool.state(), st)
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "bf16"])
+def test_offsets_past_32_bits(kind):
+    """The same request in the first and in the last pages of a pool of more than
+    2^32 bytes: the same bits from prefill, decode and gather, after a copy and a
+    fork between the two ends too."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    hq, hkv, d, ps, ppr = 8, 8, 128, 64, 4
+    w = {"bf16": 2 * d, "e2m1": d // 2}[kind]
+    P = (1 << 32) // (ps * hkv * w) + 9
+    S = P * ps
+    k, v = [torch.empty(S, hkv, w, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    blocks = [torch.empty(hkv, S, d // 16, dtype=torch.uint8, device="cuda") for _ in range(2)] if kind == "e2m1" else [None] * 2
+    if kind == "bf16":
+        k, v = k.view(torch.bfloat16), v.view(torch.bfloat16)
+    table = [[2, 0, 1, -1], [P - 1, P - 3, P - 2, -1], [-1] * 4]
+    kv = attn.KVCache(k, v, torch.zeros(3, dtype=torch.int64, device="cuda"), i32([0, 0, 0]), i32([ppr * ps] * 3), i32(table),
+                      ps, 0.03, 0.06, *blocks)
+    ref = torch.zeros(P, dtype=torch.int32, device="cuda")
+    ref[[0, 1, 2, P - 1, P - 2, P - 3]] = 1
+    ref[3:P - 3] = 1  # taken by others, but for the page that the fork below gets
+    ref[P - 5] = 0
+    cfg, ws, n = attn.config(hq, hkv, d), attn.new_pages_workspace(kv), 150
+    aws = attn.new_workspace(cfg, 2 * n, 3, ppr * ps)
+    g = torch.Generator().manual_seed(3)
+    nw = [(1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2)]
+    x = torch.randn(n + 1, (hq + 2 * hkv) * d, generator=g).bfloat16().cuda()
+    new = lambda m: torch.empty(m, hq * d, dtype=torch.bfloat16, device="cuda")
+    same_rows = lambda t: all(torch.equal(t[0].view(torch.int16), r.view(torch.int16)) for r in t[1:])
+    out = new(2 * n)
+    attn.prefill(cfg, torch.cat([x[:n], x[:n]]), *nw, i32([0, n, 2 * n]), n, kv.rows(0, 2), out, aws)
+    assert same_rows(out.view(2, n, -1)) and torch.isfinite(out).all()
+    kv.cache_lens[:2] += n
+    attn.pages_fork(cfg, kv, ref, i32([0]), i32([2]), ws)  # its open page is page 1, the copy page P - 5
+    assert kv.page_table[2].tolist() == [2, 0, P - 5, -1]
+    dec = new(3)
+    attn.decode(cfg, x[n:].expand(3, -1).contiguous(), *nw, ppr * ps - 1, kv, dec, aws)
+    assert same_rows(dec) and torch.isfinite(dec).all()
+    kv.cache_lens += 1
+    ko, vo = [torch.empty(3 * (n + 1), hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    attn.kv_gather(cfg, kv, i32([0, n + 1, 2 * n + 2, 3 * n + 3]), i32([0, 0, 0]), ko, vo, aws)
+    assert same_rows(ko.view(3, n + 1, -1)) and same_rows(vo.view(3, n + 1, -1))
+    attn.pages_copy(cfg, kv, i32([2, 0]), i32([P - 7, P - 6]), ws)
+    kv.page_table[0, :2] = i32([P - 7, P - 6])
+    k2, v2 = torch.empty_like(ko), torch.empty_like(vo)
+    attn.kv_gather(cfg, kv, i32([0, n + 1, 2 * n + 2, 3 * n + 3]), i32([0, 0, 0]), k2, v2, aws)
+    assert torch.equal(ko.view(torch.int16), k2.view(torch.int16)) and torch.equal(vo.view(torch.int16), v2.view(torch.int16))
+    assert attn.get_status(ws) == 0 and attn.get_status(aws) == 0
