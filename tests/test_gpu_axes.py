@@ -191,3 +191,10 @@ def test_positions_out_of_range_skip_the_token():
                 rope=attn.RopeAxes(pos.cuda(), [24, 20, 20], False))
     assert ds.status() == attn.ATTN_STATUS_POSITION
     assert (ds.out[1] == 7).all() and (ds.out[0] != 7).any()
+
+
+@pytest.mark.parametrize("kind,ps", [("bf16", 0), ("e4m3", 64), ("e2m1", 64)])
+def test_decode_of_a_batch_whose_heads_fill_the_card(kind, ps):
+    """Splits of 2048 keys (B Hkv = 320): requests of one split beside some of three."""
+    cache = [int(x) for x in np.linspace(0, 2100, 38)] + [4500, 2047]
+    test_decode((16, 8, 64, [], cache, [12, 10, 10], True, kind, ps))

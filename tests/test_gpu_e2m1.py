@@ -90,6 +90,7 @@ DECODE = [
     (6, 3, 128, [0, 70, 6000], 256),
     (2, 1, 128, [9000], 0),
     (128, 16, 128, [40, 513], 0),
+    (32, 4, 64, [4200, 2047, 2048] + list(range(1, 2200, 30)), 64),  # splits of 2048 keys, groups of 8
 ]
 
 
