@@ -526,16 +526,24 @@ __device__ __forceinline__ F2 two_prod(float a, float b) {
   return {p, fmaf(a, b, -p)};
 }
 
-// cos and sin of pos * f as pairs, absolute error about 1e-8: the angle reduced by
-// multiples of pi / 2 to a pair |r| <= pi / 4, then the Taylor series with the leading
-// terms (r, and 1 - r^2 / 2) kept exactly.
+// cos and sin of pos * f as pairs: the angle reduced by multiples of pi / 2 to a
+// pair |r| <= pi / 4, then the Taylor series with the leading terms (r, and 1 - r^2 /
+// 2) kept exactly.  Far out one rounded quotient is off by up to one multiple (the
+// quotient at 2^24 has steps of 1), so the reduction (Cody and Waite's, on pairs) is
+// done twice; the second quotient is small.  Absolute error about 2e-8 up to
+// positions of 2^22, 8e-8 at 2^24 (the roundings of the low part, which grows with
+// the position).
 __device__ __forceinline__ void rope_angle_fine(float pos, float f_hi, float f_lo, const RopeFreqs& fr, F2* c, F2* s) {
   const F2 a = two_prod(pos, f_hi);
-  const float k = rintf(a.hi * (4.f * fr.inv_two_pi));
   const float h_hi = 0.25f * fr.two_pi_hi, h_lo = 0.25f * fr.two_pi_lo;  // pi / 2
-  const F2 q = two_prod(-k, h_lo);
-  const F2 t = two_sum(fmaf(-k, h_hi, a.hi), q.hi);
-  const F2 r = two_sum(t.hi, t.lo + q.lo + fmaf(pos, f_lo, a.lo));
+  const float k1 = rintf(a.hi * (4.f * fr.inv_two_pi));
+  const F2 p = two_prod(-k1, h_hi), q = two_prod(-k1, h_lo);
+  const F2 u = two_sum(a.hi, p.hi);
+  const F2 t = two_sum(u.hi, q.hi);
+  const F2 v = two_sum(t.hi, fmaf(pos, f_lo, a.lo));
+  const F2 z = two_sum(v.hi, ((t.lo + v.lo) + (p.lo + u.lo)) + q.lo);
+  const float k2 = rintf(z.hi * (4.f * fr.inv_two_pi));
+  const F2 r = two_sum(fmaf(-k2, h_hi, z.hi), fmaf(-k2, h_lo, z.lo));
   const F2 r2 = two_prod(r.hi, r.hi);
   const float x = r2.hi;
   const float ps = fmaf(fmaf(fmaf(fmaf(-1.f / 39916800, x, 1.f / 362880), x, -1.f / 5040), x, 1.f / 120), x, -1.f / 6);
@@ -544,7 +552,7 @@ __device__ __forceinline__ void rope_angle_fine(float pos, float f_hi, float f_l
   sn = two_sum(sn.hi, fmaf(r.lo, fmaf(-0.5f, x, 1.f), sn.lo));
   F2 cs = two_sum(1.f, -0.5f * x);
   cs = two_sum(cs.hi, cs.lo + (fmaf(x * x, pc, -0.5f * r2.lo) - r.hi * r.lo));  // hi alone is the nearest float
-  const int quarter = (int)k & 3;
+  const int quarter = (int)(k1 + k2) & 3;
   const bool swap = quarter & 1, neg_c = quarter == 1 || quarter == 2, neg_s = quarter >= 2;
   *c = swap ? sn : cs;
   *s = swap ? cs : sn;
