@@ -136,7 +136,8 @@ __device__ __forceinline__ uint32_t e2m1_block_scale(float amax) { return e4m3x2
 // approximate quotient, y - m s rounds to zero only if it is zero (m s is exact: 4
 // and 5 bits) and m + (y - m s) / s, rounded once, lies on the side of m that y / s
 // does: a nonzero y - m s is at least an ulp of y, and (ulp of y) / s exceeds half
-// an ulp of m since s is below twice the power of two in it.
+// an ulp of m since s is below twice the power of two in it.  All on |y|; the sign is
+// put back at the end, so that a zero keeps its own.
 __device__ __forceinline__ uint32_t e2m1_codes8(const float (&y)[8], float s) {
   if (!(s > 0.f)) {  // an empty block, or a NaN one (whose codes do not matter)
     return 0u;
@@ -147,9 +148,10 @@ __device__ __forceinline__ uint32_t e2m1_codes8(const float (&y)[8], float s) {
   float z[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float q = fminf(fmaxf(__fmul_rn(y[e], inv), -8.f), 8.f);  // an infinity stays on its side
+    const float a = fabsf(y[e]);
+    const float q = fminf(__fmul_rn(a, inv), 8.f);
     const float m = __fsub_rn(__fadd_rn(q, kQuarters), kQuarters);
-    z[e] = fmaf(fmaf(-m, s, y[e]), inv, m);
+    z[e] = copysignf(fmaf(fmaf(-m, s, a), inv, m), y[e]);
   }
   return e2m1x8(z);
 }

@@ -142,3 +142,39 @@ def test_k_of_many_tokens_near_the_last_position(d):
         near = torch.searchsorted(grid, target).clamp(1, len(grid) - 1)
         best = torch.minimum((target - grid[near]).abs(), (target - grid[near - 1]).abs())
         assert ((target - sv[..., 0]).abs() <= best + 2 * err.amax(-1) / 6).all()
+
+
+def signed_zeros_and_borders(d, scale):
+    """bf16 rows [n, 2, D]: +0 and -0 among other entries, blocks of -0 alone, tiny
+    negative entries beside large ones, ordinary values, values next to borders."""
+    rng = np.random.RandomState(d)
+    x = rng.randn(64, 2, d)
+    x[rng.rand(*x.shape) < 0.2] = -0.0
+    x[rng.rand(*x.shape) < 0.1] = 0.0
+    x[3, 0] = -0.0
+    x[4, 1, :d // 2] *= -1e-30
+    x[5] = -np.abs(x[5]) * 1e-3
+    x[5, :, ::16] = 7
+    x[6:40] = rng.choice([0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6], (34, 2, d)) * rng.choice([-1, 1], (34, 2, d)) * scale
+    return torch.from_numpy(x.astype(np.float32)).bfloat16()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0625, 0.0371, 1.7, 1e-4])
+def test_v_bytes_are_the_formats(d, scale):
+    """V's bytes, signs of zeros among them, for scales that are no powers of two
+    too (the product with the rounded reciprocal is inexact there)."""
+    from causal_gqa_attention_qkv_gb300 import attn, step
+    v = signed_zeros_and_borders(d, scale)
+    n = v.shape[0]
+    for lens, df in (([n], 1), ([1] * n, 0)):
+        w = gen.custom(f"vb_{d}", 4, 2, d, lens, [0] * len(lens), seed=d, decode_from=df)
+        host = gen.make_inputs(w, kv_dtype="e2m1", k_scale=0.03, v_scale=scale)
+        host["qkv"].view(n, 8, d)[:, 6:] = v
+        ds = step.upload(w, host)
+        ds.run()
+        assert ds.status() == 0
+        codes, scales = stored(ds.kv_prefill or ds.kv_decode, "v", written_slots(host))
+        want, blocks = ref64.e2m1_store(v.float().numpy(), scale)
+        assert np.array_equal(scales, blocks)
+        assert np.array_equal(codes, want), f"{(codes != want).mean():.2%}"
