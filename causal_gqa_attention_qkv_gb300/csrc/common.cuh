@@ -619,7 +619,8 @@ __device__ __forceinline__ void norm_rope_pair_fine(const uint4& raw_a, const ui
   const float g = rsqrtf(v.hi);
   const F2 g2 = two_prod(g, g);
   const float res = fmaf(-v.hi, g2.hi, 1.f) - fmaf(v.hi, g2.lo, v.lo * g2.hi);
-  const float g_lo = 0.5f * g * res;
+  // (past the range of fp32 squares g is 0 and its correction no number: then none)
+  const float g_lo = fabsf(res) < 1.f ? 0.5f * g * res : 0.f;
   float wa[8], wb[8];
   unpack_bf16x8(w_a, wa);
   unpack_bf16x8(w_b, wb);

@@ -178,3 +178,27 @@ def test_v_bytes_are_the_formats(d, scale):
         want, blocks = ref64.e2m1_store(v.float().numpy(), scale)
         assert np.array_equal(scales, blocks)
         assert np.array_equal(codes, want), f"{(codes != want).mean():.2%}"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_k_whose_squares_overflow_is_stored_as_over_a_bf16_cache(d):
+    """Arithmetic is fp32: a mean of squares past its range makes the normed head 0,
+    whatever the cache holds, and marks nothing as no number."""
+    from causal_gqa_attention_qkv_gb300 import attn, step
+    for lens, df in (([5], 1), ([1] * 5, 0)):
+        w = gen.custom(f"ov_{d}", 4, 2, d, lens, [0] * len(lens), seed=d, decode_from=df)
+        got = []
+        for kind in ("bf16", "e2m1"):
+            host = gen.make_inputs(w, kv_dtype=kind, k_scale=0.03, v_scale=0.05)
+            host["qkv"].view(5, 8, d)[2, 4, 7] = 1e25
+            ds = step.upload(w, host)
+            cu = torch.tensor([0] + np.cumsum(lens).tolist(), dtype=torch.int32, device="cuda")
+            kv = ds.kv_prefill or ds.kv_decode
+            if df:
+                attn.kv_append(ds.cfg, ds.qkv, ds.k_norm_w, cu, kv, ds.workspace)
+            else:
+                ds.run()
+            assert ds.status() == 0
+            got.append(ref64.entries(kv.k_cache, kind, 0.03 if kind == "e2m1" else 1, kv.k_block_scale)[written_slots(host)])
+        assert (got[0][2, 0] == 0).all() and (got[1][2, 0] == 0).all()
+        assert np.isfinite(got[1]).all() and (got[1][2, 1] != 0).any() and (got[1][1, 0] != 0).any()
