@@ -832,13 +832,14 @@ __device__ __forceinline__ ReqInfo load_request(const KvIndex& kv, int b, int32_
   return r;
 }
 
-// Slot of the entry at position pos of a request, or -1 when its page number
-// is outside the cache (paged layout; pos < pages_per_req * page_size).
-__device__ __forceinline__ int64_t cache_slot(const KvIndex& kv, const ReqInfo& r, int pos) {
+// Slot of the entry at position pos of a request, or `none` (negative) when its
+// page number is outside the cache (paged layout; pos < pages_per_req * page_size).
+// A tile of n keys read from slot -n is all zeros: TMA fills them in.
+__device__ __forceinline__ int64_t cache_slot(const KvIndex& kv, const ReqInfo& r, int pos, int none = -1) {
   if (!r.pages) return r.slot0 + pos;
   const int64_t pg = __ldg(r.pages + (pos >> kv.log2_page));
   const int64_t slot = (pg << kv.log2_page) + (pos & ((1 << kv.log2_page) - 1));
-  return (pg >= 0 && slot < kv.num_slots) ? slot : -1;
+  return (pg >= 0 && slot < kv.num_slots) ? slot : none;
 }
 
 }  // namespace gb300

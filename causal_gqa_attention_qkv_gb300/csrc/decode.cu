@@ -109,11 +109,8 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         uint8_t* kt = smem + st * Lay::kStageBytes;
         uint8_t* vt = kt + Lay::kTileBytes;
         // a 64-key tile lies in one page; a page outside the cache reads as zeros
-        int64_t slot = cache_slot(p.kv, r, k0 + i * kKeysPerTile);
-        if (slot < 0) {
-          set_status(p.status, ATTN_STATUS_CAPACITY);
-          slot = 0;
-        }
+        const int64_t slot = cache_slot(p.kv, r, k0 + i * kKeysPerTile, -kKeysPerTile);
+        if (slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
 #pragma unroll
         for (int rg = 0; rg < Lay::kRegions; ++rg) {  // x: 64 bf16 (128 B) per box, or 0
           tma_load_3d(kt + rg * Lay::kRegionBytes, &kmap, &full[st], rg * 64, kh, (int)slot);

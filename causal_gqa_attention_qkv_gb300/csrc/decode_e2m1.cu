@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     // First slots of the tiles [w0, w0 + 32) (slot_now, one per lane) and of the 32 after
     // them, read ahead: no page-table read stands between a free stage and its refill.
     const int ntiles = (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
-    auto tile_slot = [&](int t) -> int64_t { return t < ntiles ? cache_slot(p.kv, r, k0 + t * kKeysPerTile) : 0; };
+    // A page outside the cache reads as zeros; its scales are not read.
+    auto tile_slot = [&](int t) -> int64_t {
+      return t < ntiles ? cache_slot(p.kv, r, k0 + t * kKeysPerTile, -kKeysPerTile) : 0;
+    };
     int w0 = 0;
     int64_t slot_now = tile_slot(lane), slot_next = tile_slot(32 + lane);
     int issued = 0, st = 0;
@@ -193,22 +196,21 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       // lane issuing all eight in turn cost 4 % of the call.
       const int which = lane & 1, half = (lane >> 1) & 1;
       const bool issues = lane < 2 * halves;
-      int64_t slot = __shfl_sync(0xffffffffu, slot_now, 2 * i - w0 + half);
-      if (__any_sync(0xffffffffu, issues && slot < 0)) {  // a page outside the cache is read from slot 0
-        if (lane == 0) set_status(p.status, ATTN_STATUS_CAPACITY);
-        if (slot < 0) slot = 0;
-      }
+      const int64_t slot = __shfl_sync(0xffffffffu, slot_now, 2 * i - w0 + half);
       // the same for every half of the CTA (a half past the end has no slot)
       const uint32_t shift = (uint32_t)((row0 + __shfl_sync(0xffffffffu, slot, 0)) * SB) & 15u;
       const uint32_t sbytes = kKeysPerTile * SB + (shift ? 16u : 0u);
       const int64_t at = (row0 + slot) * SB - shift;
-      const bool bulk = __all_sync(0xffffffffu, !issues || at + sbytes <= end);  // else past the arrays: key by key
+      // else past the arrays, or a page outside the cache: key by key
+      const bool bulk = __all_sync(0xffffffffu, !issues || (slot >= 0 && at + sbytes <= end));
       if (!bulk) {
+        if (issues && slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
         for (int h = 0; h < halves; ++h) {
           const int64_t from = __shfl_sync(0xffffffffu, at, 2 * h) + shift;
+          const bool none = __shfl_sync(0xffffffffu, slot, 2 * h) < 0;
           for (int key = lane; key < kKeysPerTile; key += 32) {
             const int64_t a = from + key * SB;
-            const bool in = a + SB <= end;
+            const bool in = !none && a + SB <= end;
             const uint32_t dst = stage + h * Lay::kScaleBytes + shift + key * SB;
             for (uint32_t w = 0; w < SB; w += 4) {
               const uint32_t x = in ? __ldcg(reinterpret_cast<const uint32_t*>(p.k_block_scale + a + w)) : 0u;
