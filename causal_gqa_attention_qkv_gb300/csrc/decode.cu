@@ -48,10 +48,16 @@ __device__ __forceinline__ uint32_t f8_off(uint32_t key, uint32_t chunk) {
   return D == 128 ? sw128(key, chunk) : key * (uint32_t)D + (chunk << 4);
 }
 
+// A sum of products with what the rounding of one factor left of them.
+__device__ __forceinline__ float plus_rest(float x, float rest) {
+  return fabsf(x) < -kNegInf ? x + rest : x;
+}
+
 // Axes: rotary positions with several axes.  With a bf16 cache these calls also
 // carry what rounding Q and P to bf16 leaves, in the fragments' rows 8-15, which
 // are padding otherwise: the products cost the same and the result is that of
-// unrounded Q and P to within 2^-16.
+// unrounded Q and P to within 2^-16.  Next to an infinite entry the rests' product is
+// infinite with a sign of its own, or no number: there the sum goes without it.
 // F8: the cache holds E4M3 codes.  The tiles are converted to f16 in
 // registers (exact) and the products run as f16 mma.sync.  Each lane then
 // reads contiguous bytes: for Q.K^T, quad member c takes the columns
@@ -312,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     if constexpr (Rest) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[e][0] += s[e][2];
-        s[e][1] += s[e][3];
+        s[e][0] = plus_rest(s[e][0], s[e][2]);
+        s[e][1] = plus_rest(s[e][1], s[e][3]);
       }
     }
     const int kfirst = k0 + i * kKeysPerTile + warp * 16;  // first key of this warp's slice
@@ -413,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     float* dst = mo + (warp * G + qrow) * D;
 #pragma unroll
     for (int dt = 0; dt < D / 8; ++dt) {
-      dst[dt * 8 + 2 * qc] = Rest ? o[dt][0] + o[dt][2] : o[dt][0];
-      dst[dt * 8 + 2 * qc + 1] = Rest ? o[dt][1] + o[dt][3] : o[dt][1];
+      dst[dt * 8 + 2 * qc] = Rest ? plus_rest(o[dt][0], o[dt][2]) : o[dt][0];
+      dst[dt * 8 + 2 * qc + 1] = Rest ? plus_rest(o[dt][1], o[dt][3]) : o[dt][1];
     }
     if ((lane & 3) == 0) {
       mm[warp * G + qrow] = m;

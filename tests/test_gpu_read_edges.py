@@ -1,8 +1,9 @@
 """GPU tests of what calls read at their edges: pages whose number lies outside the
-cache."""
+cache, infinite entries under rotary axes."""
 import pytest
 import torch
 
+import ref64
 from causal_gqa_attention_qkv_gb300 import inputs as gen
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +51,35 @@ def test_a_page_outside_the_cache_reads_as_zeros(kind, hq, hkv, d, ps, lens, cac
     assert torch.isfinite(outs[0]).all()
     for o in outs[1:]:
         assert torch.equal(bits(o), bits(outs[0]))
+
+
+AXES = ([24, 20, 20], [12, 10, 10])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_entries_under_axes(d):
+    """An infinite V entry gives that infinity (every weight is positive here), an
+    infinite K entry whose score is -inf takes no part: as in the call without axes."""
+    from causal_gqa_attention_qkv_gb300 import attn, step
+    w = gen.custom(f"inf_{d}", 4, 2, d, [1, 1, 1], [40, 300, 9], seed=d, decode_from=0)
+    host = gen.make_inputs(w)
+    slot = lambda b, p: int(host["slot_base"][b]) + p
+    host["v_cache"][slot(0, 5), 0, 3] = float("inf")
+    host["v_cache"][slot(1, 200), 1, 7] = float("-inf")
+    host["k_cache"][slot(2, 4), 0, 0] = float("-inf")
+    pos = torch.stack([torch.tensor([40, 300, 9], dtype=torch.int32)] * 3)  # the plain call's positions
+    q, _, _ = ref64.prepared(w, host)
+    heads = [h for h in (0, 1) if q[2, h, 0] > 0]  # of KV head 0: the score is -inf where q > 0
+    assert heads
+    plain, axes = step.upload(w, host), step.upload(w, host)
+    plain.run()
+    sections = AXES[0] if d == 128 else AXES[1]
+    attn.decode(axes.cfg, axes.qkv, axes.q_norm_w, axes.k_norm_w, axes.max_cache_len, axes.kv_decode, axes.out,
+                axes.workspace, rope=attn.RopeAxes(pos.cuda(), sections, True))
+    assert plain.status() == 0 and axes.status() == 0
+    a, b = plain.out.view(3, 4, d).float(), axes.out.view(3, 4, d).float()
+    assert (a[0, :2, 3] == float("inf")).all() and (a[1, 2:, 7] == float("-inf")).all()
+    assert (b[0, :2, 3] == float("inf")).all() and (b[1, 2:, 7] == float("-inf")).all()
+    for h in heads:
+        assert torch.isfinite(a[2, h]).all() and torch.isfinite(b[2, h]).all()
+    assert torch.equal(torch.isfinite(a), torch.isfinite(b))
