@@ -82,6 +82,7 @@ EXPORTS = {
     "attn_decode_attend": (ctypes.c_int, [_CFG, _P, _P, _I32, _I32, _KV, _P, _P, _SZ, _P]),
     "attn_decode_static_scratch": (ctypes.c_int, [_CFG, _P, _P, _P, _I32, _I32, _KV, _P, _P, _P]),
     "attn_decode_splits": (_I32, [_CFG, _I32, _I32]),
+    "attn_decode_splits_of": (_I32, [_CFG, _I32, _I32, _I32, _I32]),
     "attn_qkv_proj_prepare": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _P, _P, _I32, _I32, _KV, _P, _P, _SZ, _P]),
     "attn_o_proj": (ctypes.c_int, [_CFG, _P, _I32, _P, _I32, _P, _P, _SZ, _P]),
     "attn_kv_append_axes": (ctypes.c_int, [_CFG, _P, _P, _P, _I32, _I32, _KV, _ROPE, _P, _SZ, _P]),
@@ -175,6 +176,13 @@ class KVCache:
             object.__setattr__(self, "_built", None)
             object.__setattr__(self, "_built_pages", None)
 
+    @property
+    def kv_dtype(self) -> int:
+        """Element type, ATTN_KV_*."""
+        if self.k_block_scale is not None or self.v_block_scale is not None:
+            return ATTN_KV_E2M1
+        return ATTN_KV_E4M3 if self.k_cache.dtype == torch.uint8 else ATTN_KV_BF16
+
     def struct(self) -> AttnKV:
         built = self.__dict__.get("_built")
         if built is None:
@@ -185,7 +193,7 @@ class KVCache:
     def _make_struct(self) -> AttnKV:
         fp8 = self.k_cache.dtype == torch.uint8
         kbs, vbs = self.k_block_scale, self.v_block_scale
-        fp4 = kbs is not None or vbs is not None
+        fp4 = self.kv_dtype == ATTN_KV_E2M1
         if fp4:
             S, H, half = self.k_cache.shape
             assert self.v_cache.shape == self.k_cache.shape, "v_cache"
@@ -208,8 +216,8 @@ class KVCache:
         return AttnKV(self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.k_cache.shape[0],
                       self.slot_base.data_ptr(), self.cache_lens.data_ptr(),
                       self.slot_capacity.data_ptr(), pt, ps, ppr,
-                      ATTN_KV_E2M1 if fp4 else ATTN_KV_E4M3 if fp8 else ATTN_KV_BF16, float(self.k_scale),
-                      float(self.v_scale), kbs.data_ptr() if fp4 else None, vbs.data_ptr() if fp4 else None)
+                      self.kv_dtype, float(self.k_scale), float(self.v_scale),
+                      kbs.data_ptr() if fp4 else None, vbs.data_ptr() if fp4 else None)
 
     def pages_struct(self, ref_count: torch.Tensor) -> AttnPages:
         """The pool's bookkeeping for the page calls: this cache's page table and
@@ -262,10 +270,11 @@ def _rope(rope, n):
     return None if rope is None else ctypes.byref(rope.struct(n))
 
 
-def decode_splits(cfg: AttnConfig, B: int, max_cache_len: int) -> int:
-    """Number of KV splits attn_decode uses for its longest request (the
-    library's own policy, attn_decode_splits)."""
-    n = load().attn_decode_splits(ctypes.byref(cfg), int(B), int(max_cache_len))
+def decode_splits(cfg: AttnConfig, B: int, max_cache_len: int, kv_dtype: int = ATTN_KV_BF16, axes: bool = False) -> int:
+    """Number of KV splits a decode call over a cache of type ``kv_dtype`` (with
+    ``axes``: rotary axes) uses for its longest request (the library's own policy,
+    attn_decode_splits_of)."""
+    n = load().attn_decode_splits_of(ctypes.byref(cfg), int(B), int(max_cache_len), int(kv_dtype), int(axes))
     if n < 0:
         raise AttnError(int(n), load().attn_strerror(int(n)).decode())
     return int(n)

@@ -242,10 +242,13 @@ size_t q_stage_bytes(const attn_config_t* cfg, int64_t N) {
   return align_up((size_t)N * cfg->num_q_heads * cfg->head_dim * 2, 256);
 }
 
-size_t decode_ws_need(const attn_config_t* cfg, int32_t B, int32_t max_cache_len, int* split_len,
-                      int* max_splits) {
-  *split_len = decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, max_splits, false);
-  return kWsHeader + partial_bytes(*cfg, B, *max_splits);
+// Calls over an E2M1 cache and with axes take longer splits.
+bool longer_splits(int32_t kv_dtype, bool axes) { return axes || kv_dtype == ATTN_KV_E2M1; }
+
+size_t decode_ws_need(const attn_config_t* cfg, int32_t B, int32_t max_cache_len, bool longer) {
+  int max_splits = 1;
+  decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits, longer);
+  return kWsHeader + partial_bytes(*cfg, B, max_splits);
 }
 
 // Split-KV decode (and merge); with k_norm_w, the new tokens' K/V are
@@ -255,7 +258,7 @@ int decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_
                   void* out, void* workspace, cudaStream_t s) {
   int max_splits = 1;
   const int split_len = decode_split_len(B, cfg->num_kv_heads, max_cache_len + 1, &max_splits,
-                                         rope != nullptr || kv->kv_dtype == ATTN_KV_E2M1);
+                                         longer_splits(kv->kv_dtype, rope != nullptr));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t rows = (size_t)B * cfg->num_q_heads * max_splits;
   DecodeArgs d;
@@ -286,16 +289,21 @@ extern "C" {
 size_t attn_workspace_size(const attn_config_t* cfg, int32_t max_tokens, int32_t max_batch,
                            int32_t max_kv_len) {
   if (check_config(cfg) != ATTN_OK || max_tokens < 0 || max_batch < 0 || max_kv_len < 0) return 0;
-  int split_len = 0, max_splits = 1;
-  const size_t decode = decode_ws_need(cfg, max_batch, std::max(max_kv_len, 1) - 1, &split_len, &max_splits);
+  const size_t decode = decode_ws_need(cfg, max_batch, std::max(max_kv_len, 1) - 1, false);  // covers longer splits
   const size_t prefill = kWsHeader + q_stage_bytes(cfg, max_tokens);
   return std::max(prefill, decode);
 }
 
 int32_t attn_decode_splits(const attn_config_t* cfg, int32_t B, int32_t max_cache_len) {
+  return attn_decode_splits_of(cfg, B, max_cache_len, ATTN_KV_BF16, 0);
+}
+
+int32_t attn_decode_splits_of(const attn_config_t* cfg, int32_t B, int32_t max_cache_len, int32_t kv_dtype,
+                              int32_t axes) {
   if (check_config(cfg) != ATTN_OK || B < 0 || max_cache_len < 0) return ATTN_EINVAL;
+  if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3 && kv_dtype != ATTN_KV_E2M1) return ATTN_EINVAL;
   int max_splits = 1;
-  decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits, false);
+  decode_split_len(std::max(B, 1), cfg->num_kv_heads, max_cache_len + 1, &max_splits, longer_splits(kv_dtype, axes != 0));
   return max_splits;
 }
 
@@ -405,8 +413,7 @@ int attn_decode_attend_axes(const attn_config_t* cfg, const void* qkv, const voi
   if (rc) return rc;
   if (B < 0 || max_cache_len < 0) return ATTN_EINVAL;
   if ((rc = check_rope(rope, cfg, B))) return rc;
-  int split_len = 0, max_splits = 1;
-  if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits)))
+  if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, longer_splits(kv->kv_dtype, rope != nullptr))))
     return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (B == 0) return ATTN_OK;
@@ -430,8 +437,7 @@ int attn_decode_axes(const attn_config_t* cfg, const void* qkv, const void* q_no
   if (!k_norm_w || !aligned16(k_norm_w)) return ATTN_EINVAL;
   if (B < 0 || max_cache_len < 0) return ATTN_EINVAL;
   if ((rc = check_rope(rope, cfg, B))) return rc;
-  int split_len = 0, max_splits = 1;
-  if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, &split_len, &max_splits)))
+  if (!ws_ok(workspace, ws_bytes, decode_ws_need(cfg, B, max_cache_len, longer_splits(kv->kv_dtype, rope != nullptr))))
     return ATTN_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (B == 0) return ATTN_OK;

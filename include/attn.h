@@ -346,9 +346,13 @@ ATTN_API int attn_o_proj(const attn_config_t* cfg, const void* attn_out, int32_t
  * keys and at most 16 splits per request.  1 means every output row is
  * written by the split kernel directly (no partials, no merge launch).
  * Over an E2M1 cache and with rotary axes a split has at least
- * min(2048, 8 B Hkv) keys besides, so there the number is an upper bound.
- * Returns ATTN_EINVAL (< 0) for invalid arguments.  Host-only. */
+ * min(2048, 8 B Hkv) keys besides, so there the number is an upper bound;
+ * attn_decode_splits_of gives the number of a call over a cache of type
+ * kv_dtype, with rotary axes if axes != 0 (attn_decode_splits: bf16, none).
+ * Both return ATTN_EINVAL (< 0) for invalid arguments.  Host-only. */
 ATTN_API int32_t attn_decode_splits(const attn_config_t* cfg, int32_t B, int32_t max_cache_len);
+ATTN_API int32_t attn_decode_splits_of(const attn_config_t* cfg, int32_t B, int32_t max_cache_len,
+                                       int32_t kv_dtype, int32_t axes);
 
 /* Attention half of attn_decode (the cache must already hold the new
  * token's K/V at slot slot_base[b] + c_b).  attn_decode gives bit for bit the
@@ -365,8 +369,8 @@ ATTN_API int attn_decode_attend(const attn_config_t* cfg, const void* qkv, const
  * as attn_decode, except that the split-KV partial results live in a
  * library-owned static device array of 16 MiB per GPU (held by every GPU that
  * loads the library until the process exits) instead of a workspace.
- *   - With splits = attn_decode_splits(cfg, B, max_cache_len) > 1 the
- *     partials take B * Hq * splits * (D + 2) * 4 bytes (each of the two
+ *   - With splits = attn_decode_splits_of(cfg, B, max_cache_len, kv_dtype, 0)
+ *     > 1 the partials take B * Hq * splits * (D + 2) * 4 bytes (each of the two
  *     arrays rounded up to 256 bytes); requests needing more than the array
  *     return ATTN_ESCRATCH and launch nothing.  With splits == 1 every output
  *     row is written directly and the call needs no scratch at any B.
