@@ -175,6 +175,7 @@ class KVCache:
         if name != "_built":
             object.__setattr__(self, "_built", None)
             object.__setattr__(self, "_built_pages", None)
+            object.__setattr__(self, "_fits", None)
 
     @property
     def kv_dtype(self) -> int:
@@ -189,6 +190,23 @@ class KVCache:
             built = self._make_struct()
             object.__setattr__(self, "_built", built)
         return built
+
+    def struct_for(self, cfg: AttnConfig, exact: bool = False) -> AttnKV:
+        """struct() for a call with ``cfg``: refused where the caches hold fewer
+        entries per slot than cfg's heads, where cfg is not that of an E2M1 cache, and
+        with ``exact`` (calls that move or read whole slots) where they hold others."""
+        d = self.__dict__
+        if (cfg.num_kv_heads, cfg.head_dim, exact) != d["_fits"]:  # not as in the last call with this struct
+            H, D, k = cfg.num_kv_heads, cfg.head_dim, self.k_cache
+            if self.k_block_scale is not None:
+                assert tuple(k.shape[1:]) == (H, D // 2), "cfg is not the cache's"
+            else:
+                n = k.shape[0] * H * D
+                assert k.numel() == n if exact else k.numel() >= n, "cfg is not the cache's"
+                assert self.v_cache.numel() >= n, "cfg is not the cache's"
+            self.struct()
+            d["_fits"] = (H, D, exact)
+        return d["_built"]
 
     def _make_struct(self) -> AttnKV:
         fp8 = self.k_cache.dtype == torch.uint8
@@ -310,7 +328,7 @@ def kv_append(cfg: AttnConfig, qkv, k_norm_w, cu_seqlens, kv: KVCache, workspace
     """K and V of the new tokens into the cache.  ``rope`` (here and below): a
     RopeAxes with the tokens' positions on several axes."""
     B = cu_seqlens.numel() - 1
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_kv_append_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(k_norm_w, "k_norm_w"),
                                       _ptr(cu_seqlens), B, qkv.shape[0], ctypes.byref(s), _rope(rope, qkv.shape[0]),
                                       _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -320,7 +338,7 @@ def prefill(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, cu_seqlens, max_seqlen: in
             out, workspace, stream=None, rope=None):
     assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda
     B = cu_seqlens.numel() - 1
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_prefill_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
                                     _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
                                     int(max_seqlen), ctypes.byref(s), _rope(rope, qkv.shape[0]), _bf16(out, "out"),
@@ -330,7 +348,7 @@ def prefill(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, cu_seqlens, max_seqlen: in
 def decode(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, max_cache_len: int, kv: KVCache, out,
            workspace, stream=None, rope=None):
     B = qkv.shape[0]
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_decode_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
                                    _bf16(k_norm_w, "k_norm_w"), B, int(max_cache_len), ctypes.byref(s),
                                    _rope(rope, B), _bf16(out, "out"), _ptr(workspace), workspace.numel(),
@@ -342,7 +360,7 @@ def prefill_prepare(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, cu_seqlens, kv: KV
     """First half of ``prefill``: K/V appended to the cache, prepared Q
     (normed, rotated, bf16 [N, Hq, D]) written to ``q_out``."""
     B = cu_seqlens.numel() - 1
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_prefill_prepare_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
                                             _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, qkv.shape[0],
                                             ctypes.byref(s), _rope(rope, qkv.shape[0]), _bf16(q_out, "q_out"),
@@ -354,7 +372,7 @@ def prefill_attend(cfg: AttnConfig, q, cu_seqlens, max_seqlen: int, kv: KVCache,
     """Second half of ``prefill``: attention over the prepared Q ``q``
     [N, Hq, D] (the cache already holds the new K/V)."""
     B = cu_seqlens.numel() - 1
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_prefill_attend(ctypes.byref(cfg), _bf16(q, "q"), _ptr(cu_seqlens), B, q.shape[0],
                                       int(max_seqlen), ctypes.byref(s), _bf16(out, "out"), _ptr(workspace),
                                       workspace.numel(), _stream(stream)))
@@ -363,7 +381,7 @@ def prefill_attend(cfg: AttnConfig, q, cu_seqlens, max_seqlen: int, kv: KVCache,
 def decode_attend(cfg: AttnConfig, qkv, q_norm_w, max_cache_len: int, kv: KVCache, out, workspace,
                   stream=None, rope=None):
     """Attention half of ``decode`` (the cache already holds the new K/V)."""
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_decode_attend_axes(ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"),
                                           qkv.shape[0], int(max_cache_len), ctypes.byref(s),
                                           _rope(rope, qkv.shape[0]), _bf16(out, "out"), _ptr(workspace),
@@ -374,7 +392,7 @@ def decode_static_scratch(cfg: AttnConfig, qkv, q_norm_w, k_norm_w, max_cache_le
                           out, device_status=None, stream=None):
     """``decode`` with the split-KV scratch in the library's static device
     buffer (no workspace; for callers that cannot allocate)."""
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_decode_static_scratch(
         ctypes.byref(cfg), _bf16(qkv, "qkv"), _bf16(q_norm_w, "q_norm_w"), _bf16(k_norm_w, "k_norm_w"),
         qkv.shape[0], int(max_cache_len), ctypes.byref(s), _bf16(out, "out"), _ptr(device_status),
@@ -388,7 +406,7 @@ def qkv_proj_prepare(cfg: AttnConfig, hidden, w_qkv, q_norm_w, k_norm_w, cu_seql
     prepared Q written to ``q_out`` [N, Hq, D]."""
     assert hidden.dim() == 2 and w_qkv.dim() == 2 and w_qkv.shape[1] == hidden.shape[1]
     B = cu_seqlens.numel() - 1
-    s = kv.struct()
+    s = kv.struct_for(cfg)
     _check(load().attn_qkv_proj_prepare_axes(ctypes.byref(cfg), _bf16(hidden, "hidden"), hidden.shape[1],
                                              _bf16(w_qkv, "w_qkv"), _bf16(q_norm_w, "q_norm_w"),
                                              _bf16(k_norm_w, "k_norm_w"), _ptr(cu_seqlens), B, hidden.shape[0],
@@ -411,8 +429,10 @@ def kv_gather(cfg: AttnConfig, kv: KVCache, cu_seqlens, start, k_out, v_out, wor
     assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and cu_seqlens.is_contiguous(), "cu_seqlens"
     B = cu_seqlens.numel() - 1
     assert start.dtype == torch.int32 and start.is_cuda and start.is_contiguous() and start.numel() >= B, "start"
+    rows = kv.slot_base.numel() if kv.page_table is None else kv.page_table.shape[0]
+    assert min(rows, kv.slot_capacity.numel()) >= B, "cu_seqlens"
     assert k_out.shape == v_out.shape and tuple(k_out.shape[1:]) == (cfg.num_kv_heads, cfg.head_dim), "k_out"
-    s = kv.struct()
+    s = kv.struct_for(cfg, exact=True)
     _check(load().attn_kv_gather(ctypes.byref(cfg), ctypes.byref(s), _ptr(cu_seqlens), _ptr(start), B,
                                  k_out.shape[0], _bf16(k_out, "k_out"), _bf16(v_out, "v_out"), _ptr(workspace),
                                  workspace.numel(), _stream(stream)))
@@ -446,7 +466,7 @@ def pages_fork(cfg: AttnConfig, kv: KVCache, ref_count, src_rows, dst_rows, work
     """Row dst_rows[i] becomes a copy of the request in row src_rows[i]: full
     pages shared, the open one copied."""
     assert src_rows.numel() == dst_rows.numel(), "dst_rows"
-    s, p = kv.struct(), kv.pages_struct(ref_count)
+    s, p = kv.struct_for(cfg, exact=True), kv.pages_struct(ref_count)
     _check(load().attn_pages_fork(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _i32(src_rows, "src_rows"),
                                   _i32(dst_rows, "dst_rows"), src_rows.numel(), _ptr(workspace), workspace.numel(),
                                   _stream(stream)))
@@ -463,7 +483,7 @@ def pages_free(kv: KVCache, ref_count, rows, workspace, stream=None):
 def pages_copy(cfg: AttnConfig, kv: KVCache, src_pages, dst_pages, workspace, stream=None):
     """Page dst_pages[i] becomes a copy of page src_pages[i]."""
     assert src_pages.numel() == dst_pages.numel(), "dst_pages"
-    s = kv.struct()
+    s = kv.struct_for(cfg, exact=True)
     _check(load().attn_pages_copy(ctypes.byref(cfg), ctypes.byref(s), _i32(src_pages, "src_pages"),
                                   _i32(dst_pages, "dst_pages"), src_pages.numel(), _ptr(workspace), workspace.numel(),
                                   _stream(stream)))
@@ -472,7 +492,7 @@ def pages_copy(cfg: AttnConfig, kv: KVCache, src_pages, dst_pages, workspace, st
 def pages_compact(cfg: AttnConfig, kv: KVCache, ref_count, workspace, stream=None):
     """Moves the pages in use to the front of the pool; kv.page_table and
     ``ref_count`` follow."""
-    s, p = kv.struct(), kv.pages_struct(ref_count)
+    s, p = kv.struct_for(cfg, exact=True), kv.pages_struct(ref_count)
     _check(load().attn_pages_compact(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _ptr(workspace),
                                      workspace.numel(), _stream(stream)))
 
