@@ -1,10 +1,12 @@
 """GPU tests of what calls read at their edges: pages whose number lies outside the
-cache, infinite entries under rotary axes."""
+cache, infinite entries under rotary axes, the precision of decode with axes."""
+import numpy as np
 import pytest
 import torch
 
 import ref64
 from causal_gqa_attention_qkv_gb300 import inputs as gen
+from parity_util import written_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +56,102 @@ def test_a_page_outside_the_cache_reads_as_zeros(kind, hq, hkv, d, ps, lens, cac
 
 
 AXES = ([24, 20, 20], [12, 10, 10])
+
+
+def axes_call(w, host, seed, top=5000):
+    from causal_gqa_attention_qkv_gb300 import attn, step
+    sections = AXES[0] if w.head_dim == 128 else AXES[1]
+    pos = torch.randint(0, top, (3, w.batch), generator=torch.Generator().manual_seed(seed), dtype=torch.int32)
+    ds = step.upload(w, host)
+    return ds, pos, sections, attn.RopeAxes(pos.cuda(), sections, True)
+
+
+def attend_within(w, host, q, keys, vals, h):
+    """ref64.attend's derivation with Q and P rounded with half a step of h: (out, bound)."""
+    cl, G, D = host["cache_lens"].numpy(), w.num_q_heads // w.num_kv_heads, w.head_dim
+    out, tol = np.zeros_like(q), np.zeros_like(q)
+    for b in range(w.batch):
+        s = ref64.slots_of(host, b, int(cl[b]) + 1)
+        for hd in range(w.num_q_heads):
+            k, v, x = keys[s, hd // G], vals[s, hd // G], q[b, hd]
+            sc = k @ x / np.sqrt(D)
+            d = ((h + 2.0 ** -16) * np.abs(k) @ np.abs(x) + ref64.PAIR_REL * np.abs(k) @ ref64.pair_norm(x)) / np.sqrt(D)
+            p = np.exp(sc - sc.max())
+            p /= p.sum()
+            out[b, hd] = p @ v
+            grow = np.exp(2 * d.max()) - 1 + 2 * h + 2.0 ** -15
+            tol[b, hd] = 2.0 ** -8 * 1.01 * np.abs(out[b, hd]) + grow * 1.01 * (p @ np.abs(v))
+    return out, tol
+
+
+@pytest.mark.parametrize("hq,hkv,d,cache,ps", [
+    (32, 8, 128, [60, 700, 1, 3000], 0),
+    (8, 1, 64, [9000, 300, 17], 64),              # groups of 8, several splits
+    (3, 3, 128, [500, 5000], 0),
+])
+@pytest.mark.parametrize("attend", [False, True])
+def test_decode_with_axes_keeps_q_and_p_to_sixteen_bits(attend, hq, hkv, d, cache, ps):
+    """Norm weights of about 4 make the scores large, so that a Q rounded to bf16 alone
+    moves the weights by several per cent of themselves: far outside this bound."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    w = gen.custom(f"fineq_{hq}_{d}", hq, hkv, d, [1] * len(cache), cache, seed=d + hq, decode_from=0)
+    host = gen.make_inputs(w, page_size=ps)
+    host["q_norm_w"] = host["q_norm_w"] * 4
+    ds, pos, sections, rope = axes_call(w, host, seed=d)
+    kv = ds.kv_decode
+    if attend:
+        cu = torch.arange(w.batch + 1, dtype=torch.int32, device="cuda")
+        attn.kv_append(ds.cfg, ds.qkv, ds.k_norm_w, cu, kv, ds.workspace, rope=rope)
+        attn.decode_attend(ds.cfg, ds.qkv, ds.q_norm_w, ds.max_cache_len, kv, ds.out, ds.workspace, rope=rope)
+    else:
+        attn.decode(ds.cfg, ds.qkv, ds.q_norm_w, ds.k_norm_w, ds.max_cache_len, kv, ds.out, ds.workspace, rope=rope)
+    assert ds.status() == 0
+    q, _, _ = ref64.prepared(w, host, (pos.numpy(), sections, True))
+    keys, vals = ref64.entries(kv.k_cache, "bf16", 1), ref64.entries(kv.v_cache, "bf16", 1)
+    got = ds.out.double().cpu().numpy().reshape(q.shape)
+    ref, tol = attend_within(w, host, q, keys, vals, 2.0 ** -16)
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+    # the bound tells: with Q rounded to bf16 the oracle itself leaves it
+    q16 = torch.from_numpy(q).bfloat16().double().numpy()
+    plain, _ = attend_within(w, host, q16, keys, vals, 2.0 ** -16)
+    assert (np.abs(plain - ref) > tol).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_with_axes_where_the_values_cancel(d):
+    """V such that the weighted sum is nearly 0: the output's own rounding is nothing
+    there and a P rounded to bf16 alone leaves the bound."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    h, cache = 4, [6 + b % 9 for b in range(24)]
+    w = gen.custom(f"cancel_{d}", h, h, d, [1] * len(cache), cache, seed=d, decode_from=0)
+    host = gen.make_inputs(w)
+    host["qkv"].view(-1, 3 * h, d)[:, 2 * h:] = 0  # the new token's V
+    ds, pos, sections, rope = axes_call(w, host, seed=d)
+    q, k, _ = ref64.prepared(w, host, (pos.numpy(), sections, True))
+    keys, vals = host["k_cache"].double().numpy(), host["v_cache"].double().numpy()
+    keys[written_slots(host)] = torch.from_numpy(k).bfloat16().double().numpy()
+    bf16 = lambda x: torch.from_numpy(x).bfloat16().double().numpy()
+    rounded = np.zeros_like(q)
+    for b, c in enumerate(cache):
+        s = ref64.slots_of(host, b, c + 1)
+        vals[s[c]] = 0
+        for hd in range(h):
+            p = np.exp(keys[s, hd] @ q[b, hd] / np.sqrt(d))
+            p /= p.max()
+            first, second = np.argsort(-p[:c])[:2]  # two heavy keys take the sum away, the second what the first left
+            vals[s[first], hd] = vals[s[second], hd] = 0
+            vals[s[first], hd] = -bf16(p @ vals[s, hd] / p[first])
+            vals[s[second], hd] = -bf16(p @ vals[s, hd] / p[second])
+            rounded[b, hd] = bf16(p) @ vals[s, hd] / p.sum()
+    v = torch.from_numpy(vals).bfloat16()
+    ds.v_cache[:v.shape[0]] = v.cuda()
+    attn.decode(ds.cfg, ds.qkv, ds.q_norm_w, ds.k_norm_w, ds.max_cache_len, ds.kv_decode, ds.out, ds.workspace, rope=rope)
+    assert ds.status() == 0
+    keys = ref64.entries(ds.kv_decode.k_cache, "bf16", 1)
+    ref, tol = attend_within(w, host, q, keys, vals, 2.0 ** -16)
+    got = ds.out.double().cpu().numpy().reshape(q.shape)
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+    assert (np.abs(rounded - ref) > tol).mean() > 0.1
 
 
 @pytest.mark.parametrize("d", [64, 128])
