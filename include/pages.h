@@ -15,14 +15,23 @@
  * page_size.  The pages handed out are always the lowest-numbered free ones, in
  * the order the call states, so results do not depend on timing.
  *
+ * A call changes the table and the counts and moves the bytes of the one attn_kv_t
+ * that it is given.  So the layers of a model share a pool: one attn_kv_t over all
+ * their slots, layer l of request b being row l * requests + b.  One call then
+ * reserves, forks, frees or compacts all layers by one plan, and the attention of
+ * layer l takes the rows [l * requests, (l + 1) * requests) of page_table,
+ * cache_lens and slot_capacity (and that layer's k_scale and v_scale).  With a pool
+ * per layer, each has a table, counts and lengths of its own.
+ *
  * The calls are asynchronous on `stream`, allocate nothing, may be recorded by
  * stream capture, and report problems that only the device sees by
  * ATTN_STATUS_PAGES in the workspace's status word (attn_get_status).  Calls on
  * one pool, and calls that share a workspace, must be ordered on one stream.
  * Host-side checks: ATTN_EINVAL for NULL pointers, negative counts, a cache that
- * is not paged, num_rows < 1, more than 2^24 pages or 2^24 rows, or lists longer
- * than num_rows (reserve, fork); ATTN_EWORKSPACE, ATTN_EDEVICE, ATTN_ELAUNCH as
- * in attn.h.  A call with n == 0 does nothing (its lists may be NULL).
+ * is not paged, num_rows < 1, more than 2^24 pages or 2^24 rows, lists longer
+ * than num_rows (reserve, fork), or more than 2^31 - 1 units of 32 KB in the n
+ * pages of a fork or copy; ATTN_EWORKSPACE, ATTN_EDEVICE, ATTN_ELAUNCH as in
+ * attn.h.  A call with n == 0 does nothing (its lists may be NULL).
  */
 #ifndef GB300_PAGES_H
 #define GB300_PAGES_H
