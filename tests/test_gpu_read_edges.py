@@ -181,3 +181,32 @@ def test_infinite_entries_under_axes(d):
     for h in heads:
         assert torch.isfinite(a[2, h]).all() and torch.isfinite(b[2, h]).all()
     assert torch.equal(torch.isfinite(a), torch.isfinite(b))
+
+
+@pytest.mark.parametrize("hq,hkv,d,ps", [(8, 2, 128, 64), (6, 3, 64, 64), (8, 1, 64, 128), (16, 8, 64, 64)])
+@pytest.mark.parametrize("extra", [1, 2, 3, 7])
+def test_a_four_bit_pool_that_ends_inside_a_page(extra, hq, hkv, d, ps):
+    """Heads' block scales then start at odd multiples of D / 16 bytes: the bits of a
+    pool of whole pages, from decode, prefill and gather."""
+    from causal_gqa_attention_qkv_gb300 import attn, step
+    for lens, cache, df in (([1, 1, 1], [200, 3000, 5], 0), ([70, 3, 130], [200, 300, 0], 3)):
+        w = gen.custom(f"tail_{hq}_{d}", hq, hkv, d, lens, cache, seed=d + hq, decode_from=df)
+        host = gen.make_inputs(w, page_size=ps, kv_dtype="e2m1")
+        more = dict(host)
+        for n in ("k_cache", "v_cache"):
+            more[n] = torch.cat([host[n], host[n][:extra]])
+        for n in ("k_block_scale", "v_block_scale"):
+            more[n] = torch.cat([host[n], host[n][:, :extra]], 1).contiguous()
+        got = []
+        for x in (host, more):
+            ds = step.upload(w, x)
+            ds.run()
+            n = sum(cache)
+            k, v = [torch.empty(n, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            cu = torch.tensor([0, cache[0], cache[0] + cache[1], n], dtype=torch.int32, device="cuda")
+            attn.kv_gather(ds.cfg, ds.kv_prefill or ds.kv_decode, cu, torch.zeros(3, dtype=torch.int32, device="cuda"), k, v,
+                           ds.workspace)
+            assert ds.status() == 0
+            got.append((ds.out, k, v))
+        for a, b in zip(*got):
+            assert torch.equal(bits(a), bits(b))
