@@ -512,9 +512,12 @@ __device__ __forceinline__ void store_e2m1_pair(const float (&xa)[8], const floa
 
 // ---------------------------------------------------------------- K to the last bit of fp32
 // A four-bit code moves by up to a third of its value when its input crosses a
-// rounding boundary, so K is brought to the fp32 value nearest to the exact one
-// before it is coded (the plain fp32 steps are off by some 1e-7 and crossed a
-// boundary about ten times as often).  Values are pairs hi + lo of floats: the
+// rounding boundary, so the prologue and the decode kernels bring K to within an
+// fp32 ulp of the exact value before it is coded: of the 10.2 M codes of K of the
+// Qwen3-4B prefill none differs from the exact value's, with plain fp32 steps 5 do
+// (its prepare then takes 56 us in place of 68, back to back).  The fused projection
+// (proj.cu) codes K from its plain fp32 steps: its accumulators are off by more.
+// Values are pairs hi + lo of floats: the
 // error-free sum and product are Knuth's and Dekker's (by fma).
 struct F2 {
   float hi, lo;

@@ -8,9 +8,9 @@
 // much the work per byte: every code has to become an f16 operand (one
 // conversion and one product with its block scale for two codes), so the layout
 // below is chosen to need nothing else per code.  64 requests of 512 .. 8192 keys
-// (Hkv 8, D 128, 322 MB): 81 us on the device, 4.0 TB/s; the loads by themselves
+// (Hkv 8, D 128, 322 MB): 79 us on the device, 4.1 TB/s; the loads by themselves
 // take 65 us, the products 74.  16 requests of 30001 .. 65000 keys with groups of 8
-// (876 MB): 190 us with the gather of the new entries, 4.6 TB/s; 152 and 161.
+// (876 MB): 188 us with the gather of the new entries, 4.7 TB/s; 152 and 161.
 //
 // Same grid as decode.cu: (split, KV head, request).  A producer warp brings stages
 // of 2 x 64 keys, codes by TMA, block scales by untiled bulk copies (a head's scales

@@ -216,8 +216,8 @@ __device__ void epi_plain(const ProjPar& p, int row, int n0, uint32_t taddr) {
   }
 }
 
-// Store 32 values of a head vector: bf16 (or f16 for a prepared Q next to an
-// E4M3 cache), or E4M3 codes of value * r.
+// Store 32 values of a head vector: bf16 (or f16 for a prepared Q next to a
+// cache of codes), or E4M3 codes of value * r.
 template <bool F16>
 __device__ __forceinline__ void store_half32(uint16_t* dst, const float (&y)[32]) {
 #pragma unroll
@@ -274,7 +274,9 @@ __device__ __forceinline__ void store_e2m1x32(uint8_t* codes, uint8_t* scales, c
 // (D columns) of the tile, Q and K heads are RMS-normalised with their weight
 // and rotated at the token's position (pairs (i, i + D/2)); Q goes to q_out,
 // K and V to the cache slot of the token.  The accumulators are used as they
-// are (fp32, never rounded to bf16 before the norm).
+// are (fp32, never rounded to bf16 before the norm).  K of an E2M1 cache is coded
+// from these fp32 steps too: the sums over C are off by more than the fine angle
+// and norm of the other appends (common.cuh) would take away.
 template <int D, int KV, bool Axes>
 __device__ void epi_qkv(const ProjPar& p, int row, int n0, uint32_t taddr, const float* qw, const float* kw) {
   constexpr bool F8 = KV == ATTN_KV_E4M3, F4 = KV == ATTN_KV_E2M1;

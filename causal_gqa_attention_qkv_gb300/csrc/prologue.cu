@@ -67,7 +67,7 @@ struct ProloguePar {
 // positions of its own D/64 pairs, read one token ahead (32768 tokens, Hq 32, Hkv 8,
 // D 128, three axes: 132 us, 6.1 TB/s, the same as without axes; read where they are
 // used: 143).  E2M1: the fine K and the codes bound the 9942-token Qwen3-4B prologue
-// at 68 us, where a bf16 cache takes 43.7.
+// at 69 us, where a bf16 cache takes 43.4.
 template <int D, int KV, bool Axes>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) kv_append_kernel(const ProloguePar p) {
   constexpr int L = D / 16;     // lanes per head vector

@@ -19,7 +19,8 @@
  *   below) and the output are bf16 (IEEE bfloat16 bits, round-to-nearest-even
  *   on every store).  All
  *   arithmetic is fp32 (norm, rotation, scores, softmax, accumulation); Q and
- *   the softmax probabilities enter the tensor-core products rounded to bf16.
+ *   the softmax probabilities enter the tensor-core products rounded to bf16,
+ *   next to an E4M3 or E2M1 cache to f16.
  * Positions.  Request b has cache_lens[b] = c_b entries already cached and
  *   n_b new tokens; new token j sits at position c_b + j and is written to
  *   slot slot_base[b] + c_b + j.  The query at position p attends to the keys
@@ -81,7 +82,7 @@ typedef struct attn_config {
 } attn_config_t;
 
 /* The KV cache of one layer (host struct holding device pointers).
- * k_cache, v_cache: [num_slots, Hkv, D] entries (bf16, or E4M3 codes: see
+ * k_cache, v_cache: [num_slots, Hkv, D] entries (bf16, or codes: see
  * kv_dtype below), contiguous, row = one slot.
  * The entry at position p of request b lives in one slot:
  *   contiguous (page_table == NULL): slot slot_base[b] + p; request b owns
@@ -124,7 +125,10 @@ typedef struct attn_config {
  *     v_scale) as y = fp32(x * r), block scale s = e4m3(fp32(max |y| / 6)) over
  *     its block, code = e2m1(fp32(y / s)) (0 where s is 0): both rounded to
  *     nearest even and clamped to the largest finite value.  Readers take
- *     code * s * k_scale.  A NaN anywhere in a block makes s, and with it every
+ *     code * s * k_scale.  K is x to within an fp32 ulp (8e-8 of its rotation
+ *     pair near position 2^24); attn_qkv_proj_prepare, whose fp32 accumulators
+ *     are off by more, takes it as its plain fp32 steps give it.  A NaN anywhere
+ *     in a block makes s, and with it every
  *     entry of the block, NaN; an infinity is clamped.  A quarter of the bytes
  *     of a bf16 cache and an eighth of a byte per entry for the scales.  Every
  *     call takes it; the prepared Q is f16. */
@@ -138,7 +142,7 @@ typedef struct attn_kv {
   const int32_t* page_table;    /* NULL, or [B, pages_per_req] page numbers (paged layout) */
   int32_t page_size;            /* slots per page (paged layout) */
   int32_t pages_per_req;        /* row length of page_table (paged layout) */
-  int32_t kv_dtype;             /* ATTN_KV_BF16 or ATTN_KV_E4M3 */
+  int32_t kv_dtype;             /* ATTN_KV_BF16, ATTN_KV_E4M3 or ATTN_KV_E2M1 */
   float k_scale;                /* E4M3: K entry = byte * k_scale; E2M1: the tensor's scale */
   float v_scale;                /* E4M3: V entry = byte * v_scale; E2M1: the tensor's scale */
   /* read only with kv_dtype == ATTN_KV_E2M1 (else callers need not set them) */
@@ -193,8 +197,12 @@ enum {
   ATTN_STATUS_PAGES = 32    /* a page call refused or skipped something (pages.h) */
 };
 
-/* Workspace bytes needed by any call with at most `max_tokens` new tokens,
- * `max_batch` requests and `max_kv_len` keys per request (c_b + n_b).  The
+/* Workspace bytes needed by a prefill of at most `max_tokens` new tokens and by
+ * a decode of `max_batch` requests with a host bound of `max_kv_len` keys per
+ * request (c_b + 1).  The splits of a decode follow from both, and one of fewer
+ * or shorter requests may be cut into more: a workspace for several sizes takes
+ * the largest of their answers (a call whose workspace is too small returns
+ * ATTN_EWORKSPACE).  The
  * workspace is a caller-owned device buffer, 256-byte aligned: a 256-byte
  * header holding the status word and the prefill work-item counters (the
  * prefill attention kernel hands its work items out through them and leaves
@@ -220,7 +228,7 @@ ATTN_API int attn_kv_append(const attn_config_t* cfg, const void* qkv, const voi
 /* First half of attn_prefill: split qkv, RMSNorm + RoPE on Q and K, append
  * K and V to the cache, and write the prepared (normed, rotated) Q to q_out
  * [N, Hq, D] (device, caller-owned, 16-byte aligned): bf16, or f16 next to
- * an E4M3 cache.  cu_seqlens,
+ * an E4M3 or E2M1 cache.  cu_seqlens,
  * B, N and kv as for attn_prefill.  Code walkthrough section 3.3; basics
  * "Attention calculation: part 1" (q_norm / k_norm after .view) and "Prefill
  * vs Decode" (past_key_values.update). */
@@ -271,8 +279,8 @@ ATTN_API int attn_decode(const attn_config_t* cfg, const void* qkv, const void* 
  *   tensor cores.  The fp32 qkv is never stored or rounded: each Q and K head
  *   is RMS-normalised and rotated from the accumulators, V rounded once, and
  *   then exactly as attn_prefill_prepare: K and V appended to the cache (bf16
- *   or E4M3 codes), the prepared Q written to q_out [N, Hq, D] (bf16, f16 next
- *   to an E4M3 cache; 16-byte aligned), ready for attn_prefill_attend.
+ *   or codes), the prepared Q written to q_out [N, Hq, D] (bf16, f16 next to an
+ *   E4M3 or E2M1 cache; 16-byte aligned), ready for attn_prefill_attend.
  * hidden, w_qkv: bf16, row-major, 16-byte aligned; C = hidden_size, a
  * multiple of 8.  cu_seqlens, B, N and kv as for attn_prefill; decode rows
  * are requests with n_b = 1.  The workspace needs only its 256-byte header

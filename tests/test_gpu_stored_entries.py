@@ -1,5 +1,6 @@
 """GPU tests of what the appends store over a four-bit cache, held to the format
-at the values where a code is decided: K far out in its positions."""
+where a code is decided: K to its exact value, far out in its positions too, V byte
+for byte, and a K whose squares overflow."""
 import dataclasses
 
 import numpy as np
