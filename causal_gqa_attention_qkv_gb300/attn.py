@@ -198,12 +198,14 @@ class KVCache:
         d = self.__dict__
         if (cfg.num_kv_heads, cfg.head_dim, exact) != d["_fits"]:  # not as in the last call with this struct
             H, D, k = cfg.num_kv_heads, cfg.head_dim, self.k_cache
+            n = k.shape[0] * H * D
             if self.k_block_scale is not None:
-                assert tuple(k.shape[1:]) == (H, D // 2), "cfg is not the cache's"
+                fits = tuple(k.shape[1:]) == (H, D // 2)
             else:
-                n = k.shape[0] * H * D
-                assert k.numel() == n if exact else k.numel() >= n, "cfg is not the cache's"
-                assert self.v_cache.numel() >= n, "cfg is not the cache's"
+                fits = (k.numel() == n if exact else k.numel() >= n) and self.v_cache.numel() >= n
+            if not fits and load().attn_decode_splits(ctypes.byref(cfg), 1, 0) < 0:
+                return self.struct()  # a cfg that the library refuses by itself, with its own code
+            assert fits, "cfg is not the cache's"
             self.struct()
             d["_fits"] = (H, D, exact)
         return d["_built"]

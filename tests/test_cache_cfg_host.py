@@ -38,3 +38,12 @@ def test_another_cfg_is_refused(kind):
 def test_a_flat_view_of_the_slots_stays_accepted():
     assert not refused(cache("bf16", flat=True), attn.config(8, 4, 64), False)
     assert not refused(cache("bf16", flat=True), attn.config(8, 4, 64), True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e2m1"])
+@pytest.mark.parametrize("heads", [(8, 3, 64), (8, 16, 64), (8, 4, 96), (256, 128, 128)])
+def test_a_cfg_that_the_library_refuses_is_left_to_it(kind, heads):
+    """Its own code (ATTN_EINVAL, ATTN_EGQA) reaches the caller, as for calls without a cache."""
+    from causal_gqa_attention_qkv_gb300 import build
+    build.build()
+    assert not refused(cache(kind), attn.config(*heads), True)
