@@ -50,6 +50,22 @@ class AttnPages(ctypes.Structure):
                 ("num_rows", ctypes.c_int32)]
 
 
+class AttnBlocks(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("num_rows", ctypes.c_int64), ("row_base", ctypes.c_void_p),
+                ("block_size", ctypes.c_int32)]
+
+
+class AttnLogitsRules(ctypes.Structure):
+    _fields_ = [("seen", ctypes.c_void_p), ("seen_ld", ctypes.c_int64), ("seen_rows", ctypes.c_int32),
+                ("seen_row", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_start", ctypes.c_void_p), ("bias_token", ctypes.c_void_p),
+                ("bias_value", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_ld", ctypes.c_int64),
+                ("mask_rows", ctypes.c_int32), ("mask_row", ctypes.c_void_p)]
+
+
+ATTN_SEEN_PROMPT = 1
+ATTN_SEEN_CLEAR = 2
+
 ATTN_KV_BF16 = 0
 ATTN_KV_E4M3 = 1
 ATTN_KV_E2M1 = 2
@@ -70,6 +86,9 @@ _CFG = ctypes.POINTER(AttnConfig)
 _KV = ctypes.POINTER(AttnKV)
 _ROPE = ctypes.POINTER(AttnRopeAxes)
 _PAGES = ctypes.POINTER(AttnPages)
+_BLOCKS = ctypes.POINTER(AttnBlocks)
+_RULES = ctypes.POINTER(AttnLogitsRules)
+_I64 = ctypes.c_int64
 
 EXPORTS = {
     "attn_workspace_size": (_SZ, [_CFG, _I32, _I32, _I32]),
@@ -99,6 +118,13 @@ EXPORTS = {
     "attn_pages_free": (ctypes.c_int, [_KV, _PAGES, _P, _I32, _P, _SZ, _P]),
     "attn_pages_copy": (ctypes.c_int, [_CFG, _KV, _P, _P, _I32, _P, _SZ, _P]),
     "attn_pages_compact": (ctypes.c_int, [_CFG, _KV, _PAGES, _P, _SZ, _P]),
+    "attn_block_workspace_size": (_SZ, [_CFG, _I32, _I32, _I32, _I32]),
+    "attn_block_bounds": (ctypes.c_int, [_CFG, _KV, _BLOCKS, _P, _P, _I32, _P, _SZ, _P]),
+    "attn_block_select": (ctypes.c_int, [_CFG, _P, _P, _I32, _I32, _I32, _KV, _BLOCKS, _I32, _I32, _I32, _P, _P, _SZ,
+                                         _P]),
+    "attn_block_attend": (ctypes.c_int, [_CFG, _P, _P, _I32, _I32, _KV, _I32, _P, _I32, _P, _P, _SZ, _P]),
+    "attn_logits_adjust": (ctypes.c_int, [_P, _I32, _I32, _I64, _RULES, _P, _I64, _P]),
+    "attn_tokens_seen": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _P]),
     "attn_get_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "attn_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sample_tokens": (ctypes.c_int, [_P, _I32, _I32, ctypes.c_int64, _P, _P, _P, _P, _P, _P]),
@@ -497,6 +523,192 @@ def pages_compact(cfg: AttnConfig, kv: KVCache, ref_count, workspace, stream=Non
     s, p = kv.struct_for(cfg, exact=True), kv.pages_struct(ref_count)
     _check(load().attn_pages_compact(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(p), _ptr(workspace),
                                      workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- blocks (include/blocks.h)
+@dataclasses.dataclass
+class BlockBounds:
+    """Bounds of the keys of one layer's blocks (see attn_blocks_t): ``bounds`` bf16
+    [rows, Hkv, 2, D], the lowest and the highest entry of each component; row of a
+    paged cache's block: its first slot / block_size; of a contiguous one:
+    row_base[b] + i (int64 [B])."""
+
+    bounds: torch.Tensor
+    block_size: int = 64
+    row_base: torch.Tensor | None = None
+
+    def struct(self, cfg: AttnConfig, rows: int) -> AttnBlocks:
+        t, base = self.bounds, self.row_base
+        assert t.dtype == torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.dim() == 4, "bounds"
+        assert tuple(t.shape[1:]) == (cfg.num_kv_heads, 2, cfg.head_dim), "bounds"
+        if base is not None:
+            assert base.dtype == torch.int64 and base.is_cuda and base.is_contiguous() and base.numel() >= rows, "row_base"
+        return AttnBlocks(t.data_ptr(), t.shape[0], _ptr(base), int(self.block_size))
+
+
+def new_block_bounds(cfg: AttnConfig, kv: KVCache, block_size: int = 64) -> BlockBounds:
+    """Bounds for all blocks of a paged cache (zeros until block_bounds makes them)."""
+    assert kv.page_table is not None and block_size > 0, "the cache is not paged"
+    rows = kv.k_cache.shape[0] // block_size
+    return BlockBounds(torch.zeros(rows, cfg.num_kv_heads, 2, cfg.head_dim, dtype=torch.bfloat16,
+                                   device=kv.k_cache.device), block_size)
+
+
+def new_block_workspace(cfg: AttnConfig, max_tokens: int, max_kv_len: int, block_size: int, keep: int,
+                        device="cuda") -> torch.Tensor:
+    """Allocate and initialise a workspace for the block calls."""
+    n = load().attn_block_workspace_size(ctypes.byref(cfg), int(max_tokens), int(max_kv_len), int(block_size), int(keep))
+    if n == 0:
+        raise AttnError(-1, "invalid workspace query")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _check(load().attn_workspace_init(_ptr(ws), n, _stream()))
+    return ws
+
+
+def _requests(cu_seqlens, kv: KVCache, n=None):
+    """(pointer, B) of cu_seqlens; None: one token for each of the n requests (by default
+    those of the cache's lengths)."""
+    if cu_seqlens is None:
+        p, B = None, kv.cache_lens.numel() if n is None else n
+    else:
+        p, B = _i32(cu_seqlens, "cu_seqlens"), cu_seqlens.numel() - 1
+    rows = kv.slot_base.numel() if kv.page_table is None else kv.page_table.shape[0]
+    assert 0 <= B <= min(rows, kv.slot_capacity.numel(), kv.cache_lens.numel()), "cu_seqlens"
+    return p, B
+
+
+def _prepared_q(cfg: AttnConfig, q, kv: KVCache):
+    want = torch.bfloat16 if kv.kv_dtype == ATTN_KV_BF16 else torch.float16
+    assert q.dtype == want and q.is_cuda and q.is_contiguous(), "q"
+    assert q.dim() == 3 and tuple(q.shape[1:]) == (cfg.num_q_heads, cfg.head_dim), "q"
+    return q.data_ptr()
+
+
+def block_bounds(cfg: AttnConfig, kv: KVCache, blocks: BlockBounds, cu_seqlens, workspace, start=None, stream=None):
+    """Bounds of the blocks that the new tokens fill (the cache already holds them), or
+    of all full blocks from position start[b] (int32 [B]) on.  cu_seqlens None: one new
+    token per request."""
+    cu, B = _requests(cu_seqlens, kv)
+    if start is not None:
+        assert start.numel() >= B, "start"
+    s, k = kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
+    _check(load().attn_block_bounds(ctypes.byref(cfg), ctypes.byref(s), ctypes.byref(k),
+                                    None if start is None else _i32(start, "start"), cu, B, _ptr(workspace),
+                                    workspace.numel(), _stream(stream)))
+
+
+def block_select(cfg: AttnConfig, q, cu_seqlens, max_kv_len: int, kv: KVCache, blocks: BlockBounds, first: int,
+                 last: int, out_list, workspace, stream=None):
+    """The blocks of each query into ``out_list`` (int32 [N, Hkv, keep]): all, or the
+    ``first`` first, the ``last`` last and the best of the others, ascending, -1
+    behind them.  q: the prepared Q [N, Hq, D] of prefill_prepare."""
+    cu, B = _requests(cu_seqlens, kv, q.shape[0])
+    N = q.shape[0]
+    assert out_list.dim() == 3 and tuple(out_list.shape[:2]) == (N, cfg.num_kv_heads), "out_list"
+    qp, s, k = _prepared_q(cfg, q, kv), kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
+    _check(load().attn_block_select(ctypes.byref(cfg), qp, cu, B, N, int(max_kv_len), ctypes.byref(s), ctypes.byref(k),
+                                    int(first), int(last), out_list.shape[2], _i32(out_list, "out_list"),
+                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def block_attend(cfg: AttnConfig, q, cu_seqlens, kv: KVCache, block_size: int, block_list, out, workspace, stream=None):
+    """Causal attention of the prepared Q ``q`` [N, Hq, D] over the blocks listed in
+    ``block_list`` (int32 [N, Hkv, keep]) into ``out`` (bf16 [N, Hq*D])."""
+    cu, B = _requests(cu_seqlens, kv, q.shape[0])
+    N = q.shape[0]
+    assert block_list.dim() == 3 and tuple(block_list.shape[:2]) == (N, cfg.num_kv_heads), "block_list"
+    assert out.numel() >= q.numel(), "out"
+    qp, s = _prepared_q(cfg, q, kv), kv.struct_for(cfg, exact=True)
+    _check(load().attn_block_attend(ctypes.byref(cfg), qp, cu, B, N, ctypes.byref(s), int(block_size),
+                                    _i32(block_list, "block_list"), block_list.shape[2], _bf16(out, "out"),
+                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- logits (include/logits.h)
+def new_seen(rows: int, vocab: int, device="cuda") -> torch.Tensor:
+    """An empty table of seen tokens: int16 [rows, ld], of which the first ``vocab``
+    words count (the sign bit: in the prompt; the rest: times generated)."""
+    return torch.zeros(rows, -(-vocab // 8) * 8, dtype=torch.int16, device=device)
+
+
+def tokens_seen(seen, vocab: int, rows, tokens, cu_seqlens=None, prompt: bool = False, clear: bool = False, stream=None):
+    """tokens[cu_seqlens[b] : cu_seqlens[b + 1]] (None: tokens[b]) enter row rows[b]
+    (None: b) of the table: counted as generated, or marked as the prompt; ``clear``
+    empties the rows first."""
+    assert seen.dtype == torch.int16 and seen.is_cuda and seen.is_contiguous() and seen.dim() == 2, "seen"
+    B = tokens.numel() if cu_seqlens is None else cu_seqlens.numel() - 1
+    assert rows is None or rows.numel() == B, "rows"
+    flags = (ATTN_SEEN_PROMPT if prompt else 0) | (ATTN_SEEN_CLEAR if clear else 0)
+    _check(load().attn_tokens_seen(_ptr(seen), seen.shape[1], seen.shape[0], int(vocab),
+                                   None if rows is None else _i32(rows, "rows"),
+                                   None if cu_seqlens is None else _i32(cu_seqlens, "cu_seqlens"),
+                                   _i32(tokens, "tokens"), B, tokens.numel(), flags, _stream(stream)))
+
+
+@dataclasses.dataclass
+class LogitsRules:
+    """Rules for the rows of logits_adjust (see attn_logits_rules_t); None leaves a
+    rule out."""
+
+    seen: torch.Tensor | None = None        # int16 [rows, ld] (new_seen)
+    seen_row: torch.Tensor | None = None    # int32 [B]: each request's row (None: b)
+    repetition: torch.Tensor | None = None  # fp32 [B]
+    presence: torch.Tensor | None = None
+    frequency: torch.Tensor | None = None
+    bias_start: torch.Tensor | None = None  # int32 [B + 1]: row b's entries of the next two
+    bias_token: torch.Tensor | None = None  # int32
+    bias_value: torch.Tensor | None = None  # fp32
+    mask: torch.Tensor | None = None        # int32 [rows, words]: bit v % 32 of word v / 32 allows token v
+    mask_row: torch.Tensor | None = None    # int32 [B]: each request's mask (None: b; -1: none)
+
+    # Built (and the tensors checked) once, and again when a field is assigned.
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_built":
+            object.__setattr__(self, "_built", None)
+
+    def struct(self, B: int) -> AttnLogitsRules:
+        built = self.__dict__["_built"]
+        if built is None or built[0] != B:
+            built = (B, self._make_struct(B))
+            object.__setattr__(self, "_built", built)
+        return built[1]
+
+    def _make_struct(self, B: int) -> AttnLogitsRules:
+        for name, dt, n in (("seen_row", torch.int32, B), ("repetition", torch.float32, B),
+                            ("presence", torch.float32, B), ("frequency", torch.float32, B),
+                            ("bias_start", torch.int32, B + 1), ("bias_token", torch.int32, None),
+                            ("bias_value", torch.float32, None), ("mask_row", torch.int32, B)):
+            t = getattr(self, name)
+            if t is not None:
+                assert t.dtype == dt and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n), name
+        for name, dt in (("seen", torch.int16), ("mask", torch.int32)):
+            t = getattr(self, name)
+            if t is not None:
+                assert t.dtype == dt and t.is_cuda and t.is_contiguous() and t.dim() == 2, name
+        if self.bias_start is not None:
+            assert self.bias_token is not None and self.bias_value is not None, "bias_token"
+            assert self.bias_token.numel() == self.bias_value.numel(), "bias_value"
+        s, m = self.seen, self.mask
+        return AttnLogitsRules(_ptr(s), 0 if s is None else s.shape[1], 0 if s is None else s.shape[0],
+                               _ptr(self.seen_row), _ptr(self.repetition), _ptr(self.presence), _ptr(self.frequency),
+                               _ptr(self.bias_start), _ptr(self.bias_token), _ptr(self.bias_value), _ptr(m),
+                               0 if m is None else m.shape[1], 0 if m is None else m.shape[0], _ptr(self.mask_row))
+
+
+def logits_adjust(logits, rules: LogitsRules, out=None, stream=None):
+    """The rules applied to fp32 logits [B, V] (rows may be strided), into ``out``
+    (None: in place).  Returns the tensor written."""
+    if out is None:
+        out = logits
+    for t in (logits, out):
+        assert t.dtype == torch.float32 and t.is_cuda and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "logits"
+    B, V = logits.shape
+    assert out.shape == logits.shape, "out"
+    lds = [t.stride(0) if B > 1 else V for t in (logits, out)]
+    _check(load().attn_logits_adjust(_ptr(logits), B, V, lds[0], ctypes.byref(rules.struct(B)), _ptr(out), lds[1],
+                                     _stream(stream)))
+    return out
 
 
 def get_status(workspace, stream=None) -> int:

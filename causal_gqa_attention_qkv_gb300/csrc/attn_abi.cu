@@ -261,7 +261,7 @@ int decode_attend(const attn_config_t* cfg, const void* qkv, const void* q_norm_
                                          longer_splits(kv->kv_dtype, rope != nullptr));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t rows = (size_t)B * cfg->num_q_heads * max_splits;
-  DecodeArgs d;
+  DecodeArgs d = {};
   d.cfg = *cfg;
   d.B = B;
   d.kv = load_kv(kv);

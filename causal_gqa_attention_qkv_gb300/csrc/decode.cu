@@ -48,6 +48,28 @@ __device__ __forceinline__ uint32_t f8_off(uint32_t key, uint32_t chunk) {
   return D == 128 ? sw128(key, chunk) : key * (uint32_t)D + (chunk << 4);
 }
 
+// Fragments of a prepared Q row: the plain column order, or the quarters' of E4M3.
+template <int D, bool F8>
+__device__ __forceinline__ void prepared_q_frags(const uint16_t* row, bool valid, uint32_t (&frag)[D / 16][2]) {
+  const int c = threadIdx.x & 3;
+  if constexpr (F8) {
+#pragma unroll
+    for (int v = 0; v < D / 32; ++v) {
+      const uint4 u = valid ? __ldg(reinterpret_cast<const uint4*>(row + c * (D / 4) + 8 * v)) : make_uint4(0, 0, 0, 0);
+      frag[2 * v][0] = u.x;
+      frag[2 * v][1] = u.y;
+      frag[2 * v + 1][0] = u.z;
+      frag[2 * v + 1][1] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      frag[ks][0] = valid ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * ks + 2 * c)) : 0u;
+      frag[ks][1] = valid ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * ks + 8 + 2 * c)) : 0u;
+    }
+  }
+}
+
 // A sum of products with what the rounding of one factor left of them.
 __device__ __forceinline__ float plus_rest(float x, float rest) {
   return fabsf(x) < -kNegInf ? x + rest : x;
@@ -65,7 +87,10 @@ __device__ __forceinline__ float plus_rest(float x, float rest) {
 // order); for P.V, lane (g, c) takes columns [g D/8, (g+1) D/8) of its four
 // keys 2c, 2c+1, 2c+8, 2c+9, byte-interleaved in pairs of keys, so n-tile t
 // of the output holds column g D/8 + t.
-template <int D, bool F8, bool Axes>
+// Blocks: the keys are those of listed blocks (include/blocks.h), a CTA takes a split of one
+// token's list for one KV head, and Q is there already prepared.  P over a bf16 cache
+// then goes in with its rest, as with Axes (Q has none).
+template <int D, bool F8, bool Axes, bool Blocks>
 __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const DecodePar p) {
@@ -78,13 +103,25 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   __shared__ int s_abort;       // written by the producer only
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
-  const int split = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
+  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_count;
+
+  // b: the request, or the token (Blocks)
+  const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
+  const int b = Blocks ? blockIdx.x / p.max_splits : blockIdx.z;
   launch_dependents();  // the merge kernel may be scheduled as CTAs finish
   ReqInfo r;
-  int k0, k1, n_splits;
-  if (!decode_begin<D, KV, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
-  const bool append = p.k_norm_w != nullptr;
-  const int ntiles = (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
+  int k0 = 0, k1, n_splits;
+  if constexpr (Blocks) {
+    grid_dependency_wait();  // the list
+    if (!blocks_begin(p, split, kh, b, s_block, &s_count, &r, &k1)) return;
+    n_splits = p.max_splits;
+  } else {
+    if (!decode_begin<D, KV, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
+  }
+  const bool append = !Blocks && p.k_norm_w != nullptr;
+  Tiles<Blocks> tiles{k0, s_block, p.log2_bs - 6, 0};
+  tiles.n = Blocks ? s_count << tiles.sh : (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
+  const int ntiles = tiles.n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -97,10 +134,11 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     fence_barrier_init();
   }
   __syncthreads();
-  grid_dependency_wait();  // the append kernel's cache entries, earlier kernels' reads of the outputs
+  if (!Blocks) grid_dependency_wait();  // the append kernel's cache entries, earlier kernels' reads of the outputs
 
   if (warp == kConsumerWarps) {  // producer warp: one thread issues all TMA loads
-    if (append && split == n_splits - 1) append_new_kv<D, KV, Axes>(p, r, b, kh, lane);  // before the last tile's load
+    if constexpr (!Blocks)
+      if (append && split == n_splits - 1) append_new_kv<D, KV, Axes>(p, r, b, kh, lane);  // before the last tile's load
     if (lane == 0) {
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
@@ -115,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         uint8_t* kt = smem + st * Lay::kStageBytes;
         uint8_t* vt = kt + Lay::kTileBytes;
         // a 64-key tile lies in one page; a page outside the cache reads as zeros
-        const int64_t slot = cache_slot(p.kv, r, k0 + i * kKeysPerTile, -kKeysPerTile);
+        const int64_t slot = cache_slot(p.kv, r, tiles.pos(i, 0), -kKeysPerTile);
         if (slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
 #pragma unroll
         for (int rg = 0; rg < Lay::kRegions; ++rg) {  // x: 64 bf16 (128 B) per box, or 0
@@ -139,15 +177,16 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   const int G = p.G;
   const int h0 = kh * G;
   const int qrow = lane >> 2;  // A/C fragment row of this thread (rows >= G are padding)
-  constexpr bool Rest = Axes && !F8;
+  constexpr bool RestQ = Axes && !F8, Rest = (Axes || Blocks) && !F8;
   uint32_t qa[D / 16][2];  // rows 0-7 of the A fragment; rows 8-15 are zero
-  uint32_t qr[D / 16][2];  // Rest: rows 8-15
+  uint32_t qr[D / 16][2];  // RestQ: rows 8-15
   auto load_q = [&](const auto& pos) {
     const uint16_t* row = p.qkv + (int64_t)b * p.W + (int64_t)(h0 + min(qrow, G - 1)) * D;
     if constexpr (F8) q_row_frags_quarters<D>(row, qrow < G, p.q_norm_w, p.eps, pos, p.freqs, qa);
-    else q_row_frags<D, Rest>(row, qrow < G, p.q_norm_w, p.eps, pos, p.freqs, qa, qr);
+    else q_row_frags<D, RestQ>(row, qrow < G, p.q_norm_w, p.eps, pos, p.freqs, qa, qr);
   };
-  if constexpr (Axes) load_q(AxisPos{p.axes, b});
+  if constexpr (Blocks) prepared_q_frags<D, F8>(p.q + ((int64_t)b * p.Hq + h0 + min(qrow, G - 1)) * D, qrow < G, qa);
+  else if constexpr (Axes) load_q(AxisPos{p.axes, b});
   else load_q(OnePos{(float)r.cached});
   const int qc = lane & 3;  // quad member
   // E4M3: transposed products, O^T = V^T P^T and S^T = K Q^T: the warp's 16
@@ -209,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
       int kg[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        kg[t] = k0 + (i + t) * kKeysPerTile + warp * 16 + g;
+        kg[t] = tiles.pos(i + t, k1) + warp * 16 + g;
         sc[t][0] = kg[t] < k1 ? s[t][0] * p.scale_log2 : kNegInf;
         sc[t][1] = kg[t] < k1 ? s[t][1] * p.scale_log2 : kNegInf;
         sc[t][2] = kg[t] + 8 < k1 ? s[t][2] * p.scale_log2 : kNegInf;
@@ -266,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
           }
         }
         // keys past the end hold arbitrary bits: zero their V entries so 0 * NaN cannot occur
-        const int kq = k0 + (i + t) * kKeysPerTile + warp * 16 + 2 * qc;
-        const bool partial = k0 + (i + t) * kKeysPerTile + warp * 16 + 16 > k1;
+        const int kt = tiles.pos(i + t, k1) + warp * 16;
+        const int kq = kt + 2 * qc;
+        const bool partial = kt + 16 > k1;
         const uint32_t mAB = (kq < k1 ? 0x0000FFFFu : 0u) | (kq + 1 < k1 ? 0xFFFF0000u : 0u);
         const uint32_t mCD = (kq + 8 < k1 ? 0x0000FFFFu : 0u) | (kq + 9 < k1 ? 0xFFFF0000u : 0u);
 #pragma unroll
@@ -310,19 +350,19 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         const int chunk = 2 * ks + (mi & 1);
         uint32_t b0, b1, b2, b3;
         ldsm_x4(kb + (chunk >> 3) * Lay::kRegionBytes + sw128(key, chunk & 7), b0, b1, b2, b3);
-        const uint32_t a[4] = {qa[ks][0], Rest ? qr[ks][0] : 0u, qa[ks][1], Rest ? qr[ks][1] : 0u};
+        const uint32_t a[4] = {qa[ks][0], RestQ ? qr[ks][0] : 0u, qa[ks][1], RestQ ? qr[ks][1] : 0u};
         mma_bf16_16816(s[0], a, b0, b1);
         mma_bf16_16816(s[1], a, b2, b3);
       }
     }
-    if constexpr (Rest) {
+    if constexpr (RestQ) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         s[e][0] = plus_rest(s[e][0], s[e][2]);
         s[e][1] = plus_rest(s[e][1], s[e][3]);
       }
     }
-    const int kfirst = k0 + i * kKeysPerTile + warp * 16;  // first key of this warp's slice
+    const int kfirst = tiles.pos(i, k1) + warp * 16;  // first key of this warp's slice
     const int kA = kfirst + 2 * (lane & 3);
     float sc[4];
     sc[0] = kA < k1 ? s[0][0] * p.scale_log2 : kNegInf;
@@ -437,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     float L = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < kConsumerWarps; ++w) {
-      const float sw = fast_exp2(mm[w * G + row] - M);
+      const float sw = Blocks && M == kNegInf ? 0.f : fast_exp2(mm[w * G + row] - M);  // a list may leave no key
       L += sw * ml[w * G + row];
       acc += sw * mo[(w * G + row) * D + d];
     }
     const int64_t hrow = (int64_t)b * p.Hq + h0 + row;
     if (direct) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(acc / L);
+      const __nv_bfloat16 v = __float2bfloat16_rn(Blocks && L == 0.f ? 0.f : acc / L);
       p.out[hrow * D + d] = *reinterpret_cast<const uint16_t*>(&v);
     } else {
       const int64_t prow = hrow * p.max_splits + split;
@@ -478,17 +518,69 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const DecodePar p) {
   p.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&v);
 }
 
+// The merge over the splits of listed blocks: some, or all, may have had no key.
+template <int D>
+__global__ void __launch_bounds__(D) block_combine_kernel(const DecodePar p) {
+  const int64_t row = blockIdx.x;  // token * Hq + head
+  const int d = threadIdx.x;
+  grid_dependency_wait();  // the split kernel's partial results
+  int b, n, j;
+  if (!find_token(p.cu_seqlens, p.B, (int)(row / p.Hq), &b, &n, &j)) return;
+  if (!load_request(p.kv, b, n).valid) return;
+  const float* ml = p.part_ml + row * p.max_splits * 2;
+  float M = kNegInf;
+  for (int s = 0; s < p.max_splits; ++s) M = fmaxf(M, ml[2 * s]);
+  float L = 0.f, acc = 0.f;
+  for (int s = 0; s < p.max_splits; ++s) {
+    const float w = M == kNegInf ? 0.f : fast_exp2(ml[2 * s] - M);
+    L += w * ml[2 * s + 1];
+    acc += w * p.part_o[(row * p.max_splits + s) * D + d];
+  }
+  const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+  p.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&v);
+}
+
+template <int D, bool F8, bool Blocks>
+int launch_block_attend_t(const DecodeArgs& a, cudaStream_t stream) {
+  using Lay = DecodeLayout<D, F8>;
+  CacheMaps maps;
+  if (make_cache_maps(a.kv, a.cfg.num_kv_heads, D, kKeysPerTile, &maps) != 0) return ATTN_ELAUNCH;
+  if (cudaFuncSetAttribute(decode_split_kernel<D, F8, false, Blocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Lay::kSmemBytes) != cudaSuccess)
+    return ATTN_ELAUNCH;
+  const dim3 grid((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads);
+  return launch_dependent(decode_split_kernel<D, F8, false, Blocks>, grid, dim3(kThreads), Lay::kSmemBytes, stream,
+                          maps.k, maps.v, decode_par(a)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ELAUNCH;
+}
+
+template <int D>
+int launch_block_attend_d(const DecodeArgs& a, cudaStream_t stream) {
+  int rc;
+  switch (a.kv.kv_dtype) {
+    case ATTN_KV_E4M3: rc = launch_block_attend_t<D, true, true>(a, stream); break;
+    case ATTN_KV_E2M1: rc = launch_block_attend_e2m1(a, stream); break;
+    default: rc = launch_block_attend_t<D, false, true>(a, stream);
+  }
+  if (rc) return rc;
+  if (a.max_splits > 1 && launch_dependent(block_combine_kernel<D>, dim3((unsigned)(a.N * a.cfg.num_q_heads)), dim3(D),
+                                           0, stream, decode_par(a)) != cudaSuccess)
+    return ATTN_ELAUNCH;
+  return ATTN_OK;
+}
+
 template <int D, bool F8, bool Axes>
 int launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
   using Lay = DecodeLayout<D, F8>;
   CacheMaps maps;
   if (make_cache_maps(a.kv, a.cfg.num_kv_heads, D, kKeysPerTile, &maps) != 0) return ATTN_ELAUNCH;
   const DecodePar p = decode_par(a);
-  if (cudaFuncSetAttribute(decode_split_kernel<D, F8, Axes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(decode_split_kernel<D, F8, Axes, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Lay::kSmemBytes) != cudaSuccess)
     return ATTN_ELAUNCH;
   dim3 grid(a.max_splits, a.cfg.num_kv_heads, a.B);
-  if (launch_dependent(decode_split_kernel<D, F8, Axes>, grid, dim3(kThreads), Lay::kSmemBytes, stream, maps.k,
+  if (launch_dependent(decode_split_kernel<D, F8, Axes, false>, grid, dim3(kThreads), Lay::kSmemBytes, stream, maps.k,
                        maps.v, p) != cudaSuccess)
     return ATTN_ELAUNCH;
   return ATTN_OK;
@@ -534,6 +626,25 @@ int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits, bool longe
   len = (len + 63) / 64 * 64;
   *max_splits = (int)std::max<int64_t>(1, ((int64_t)max_kv_len + len - 1) / len);
   return (int)len;
+}
+
+void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per) {
+  const int64_t tiles = (int64_t)keep * (block_size / 64);
+  int64_t n = (kSplitPairs + pairs - 1) / pairs;
+  n = std::min<int64_t>(std::min<int64_t>(n, 16), std::max<int64_t>(1, tiles / 4));
+  n = std::max<int64_t>(n, (keep + kMaxSplitBlocks - 1) / kMaxSplitBlocks);
+  *per = (int)((keep + n - 1) / n);
+  *splits = (keep + *per - 1) / *per;
+}
+
+size_t block_partial_bytes(const attn_config_t& c, int64_t N, int splits) {
+  if (splits <= 1) return 0;
+  const size_t rows = (size_t)N * c.num_q_heads * splits;
+  return align_up(rows * c.head_dim * 4, 256) + align_up(rows * 2 * 4, 256);
+}
+
+int launch_block_attend(const DecodeArgs& a, cudaStream_t stream) {
+  return a.cfg.head_dim == 128 ? launch_block_attend_d<128>(a, stream) : launch_block_attend_d<64>(a, stream);
 }
 
 int launch_decode(const DecodeArgs& a, cudaStream_t stream) {

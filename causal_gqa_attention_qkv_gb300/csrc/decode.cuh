@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kernels.cuh"
+#include "kv_read.cuh"
 
 namespace gb300 {
 
@@ -33,6 +34,28 @@ struct DecodePar {
   int32_t Hq, Hkv, G, split_len, max_splits;
   float scale_log2;  // log2(e) / sqrt(D), times k_scale for a cache of codes
   float v_scale;     // 1, or v_scale for a cache of codes
+  // attention over listed blocks
+  const uint16_t* q;          // [N, Hq, D] prepared
+  const int32_t* cu_seqlens;  // NULL: one token per request
+  const int32_t* list;        // [N, Hkv, keep]
+  int32_t B, keep, log2_bs;
+};
+
+constexpr int kMaxSplitBlocks = 1024;  // entries of a list that one split may take
+
+// The tiles of 64 keys of a split: consecutive from k0, or those of listed blocks.
+template <bool Blocks>
+struct Tiles {
+  int k0;            // consecutive
+  const int* block;  // listed: shared memory
+  int sh;            // log2 of the tiles per block
+  int n;
+  // First position of tile i; of a tile past the last (one that was not loaded) `past`.
+  __device__ __forceinline__ int pos(int i, int past) const {
+    if constexpr (!Blocks) return k0 + i * kKeysPerTile;
+    if (i >= n) return past;
+    return (block[i >> sh] << (sh + 6)) + ((i & ((1 << sh) - 1)) << 6);
+  }
 };
 
 __device__ __forceinline__ void named_sync_consumers() {
@@ -146,6 +169,43 @@ __device__ __forceinline__ bool decode_begin(const DecodePar& p, int split, int 
   return true;
 }
 
+// The same for token t over its listed blocks: the entries of the split that hold a
+// visible key go to `block` (shared memory, kMaxSplitBlocks), *count of them; k1 is
+// the end of the visible positions.  False: a token without output.
+__device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int kh, int t, int* block, int* count,
+                                             ReqInfo* req, int* k1) {
+  int b, n, j;
+  const bool report = split == 0 && kh == 0 && threadIdx.x == 0;
+  if (!find_token(p.cu_seqlens, p.B, t, &b, &n, &j)) {
+    if (report) set_status(p.status, ATTN_STATUS_SEQLENS);
+    return false;
+  }
+  const ReqInfo r = load_request(p.kv, b, n);
+  if (!r.valid) {
+    if (report) set_status(p.status, ATTN_STATUS_CAPACITY);
+    return false;
+  }
+  const int end = r.cached + j + 1;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int32_t* list = p.list + ((int64_t)t * p.Hkv + kh) * p.keep;
+    const int e1 = min((split + 1) * p.split_len, p.keep);
+    int at = 0;
+    for (int e0 = split * p.split_len; e0 < e1; e0 += 32) {
+      const int i = e0 + lane < e1 ? __ldcg(list + e0 + lane) : -1;
+      const bool live = i >= 0 && ((int64_t)i << p.log2_bs) < end;
+      const uint32_t all = __ballot_sync(0xffffffffu, live);
+      if (live) block[at + __popc(all & ((1u << lane) - 1u))] = i;
+      at += __popc(all);
+    }
+    if (lane == 0) *count = at;
+  }
+  __syncthreads();
+  *req = r;
+  *k1 = end;
+  return true;
+}
+
 // The kernels' form of a call's arguments.
 inline DecodePar decode_par(const DecodeArgs& a) {
   const int D = a.cfg.head_dim;
@@ -176,6 +236,12 @@ inline DecodePar decode_par(const DecodeArgs& a) {
   p.max_splits = a.max_splits;
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)D) * (codes ? a.kv.k_scale : 1.0f);
   p.v_scale = codes ? a.kv.v_scale : 1.0f;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.cu_seqlens = a.cu_seqlens;
+  p.list = a.list;
+  p.B = a.B;
+  p.keep = a.keep;
+  p.log2_bs = a.log2_bs;
   return p;
 }
 

@@ -128,8 +128,18 @@ __device__ __forceinline__ void stage_q(const DecodePar& p, const ReqInfo& r, in
   *reinterpret_cast<uint4*>(dst + D) = vb;
 }
 
-// Wide: groups of more than 4 query heads.
-template <int D, bool Wide, bool Axes>
+// The same from prepared rows [Hq, D] f16.
+template <int D, bool Wide>
+__device__ __forceinline__ void copy_q(const uint16_t* q, int G, int thread, uint8_t* q_smem) {
+  constexpr int NH = Wide ? 8 : 4, C = D / 8;  // 16-byte chunks per head
+  for (int i = thread; i < NH * C; i += kConsumerWarps * 32) {
+    const uint4 v = i / C < G ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(q_smem + i * 16) = v;
+  }
+}
+
+// Wide: groups of more than 4 query heads.  Blocks: the keys of listed blocks, as in decode.cu.
+template <int D, bool Wide, bool Axes, bool Blocks>
 __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     decode_split_e2m1_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                              const DecodePar p) {
@@ -141,12 +151,24 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   uint64_t* empty = full + S;
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
-  const int split = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
+  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_count;
+
+  // b: the request, or the token (Blocks)
+  const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
+  const int b = Blocks ? blockIdx.x / p.max_splits : blockIdx.z;
   launch_dependents();  // the merge kernel may be scheduled as CTAs finish
   ReqInfo r;
-  int k0, k1, n_splits;
-  if (!decode_begin<D, ATTN_KV_E2M1, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
-  const int npass = (k1 - k0 + 2 * kKeysPerTile - 1) / (2 * kKeysPerTile);
+  int k0 = 0, k1, n_splits;
+  if constexpr (Blocks) {
+    grid_dependency_wait();  // the list
+    if (!blocks_begin(p, split, kh, b, s_block, &s_count, &r, &k1)) return;
+    n_splits = p.max_splits;
+  } else {
+    if (!decode_begin<D, ATTN_KV_E2M1, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
+  }
+  Tiles<Blocks> tiles{k0, s_block, p.log2_bs - 6, 0};
+  tiles.n = Blocks ? s_count << tiles.sh : (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
+  const int npass = (tiles.n + 1) / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -158,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     fence_barrier_init();
   }
   __syncthreads();
-  grid_dependency_wait();  // the append kernel's cache entries, earlier kernels' reads of the outputs
+  if (!Blocks) grid_dependency_wait();  // the append kernel's cache entries, earlier kernels' reads of the outputs
 
   if (warp == kConsumerWarps) {  // ---------------- producer warp
-    const bool append = p.k_norm_w && split == n_splits - 1;  // the new token's key is in the last stage
+    const bool append = !Blocks && p.k_norm_w && split == n_splits - 1;  // the new token's key is in the last stage
     if (lane == 0) {
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
@@ -171,10 +193,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     const int64_t end = (int64_t)p.Hkv * p.kv.num_slots * SB;
     // First slots of the tiles [w0, w0 + 32) (slot_now, one per lane) and of the 32 after
     // them, read ahead: no page-table read stands between a free stage and its refill.
-    const int ntiles = (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
+    const int ntiles = tiles.n;
     // A page outside the cache reads as zeros; its scales are not read.
     auto tile_slot = [&](int t) -> int64_t {
-      return t < ntiles ? cache_slot(p.kv, r, k0 + t * kKeysPerTile, -kKeysPerTile) : 0;
+      return t < ntiles ? cache_slot(p.kv, r, tiles.pos(t, 0), -kKeysPerTile) : 0;
     };
     int w0 = 0;
     int64_t slot_now = tile_slot(lane), slot_next = tile_slot(32 + lane);
@@ -189,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       }
       if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
       if (!ok) break;
-      if (append && i == npass - 1) append_new_kv<D, ATTN_KV_E2M1, Axes>(p, r, b, kh, lane);
+      if constexpr (!Blocks)
+        if (append && i == npass - 1) append_new_kv<D, ATTN_KV_E2M1, Axes>(p, r, b, kh, lane);
       const int halves = min(2, ntiles - 2 * i);
       const uint32_t stage = smem_u32(smem) + st * Lay::kStageBytes;
       // Lanes 0 .. 3 issue the copies of K and V (bit 0) of the halves (bit 1): one
@@ -246,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   // ---------------- consumer warps: warp w owns keys [16w, 16w + 16) of each half
   const int G = p.G;
   const int g = lane >> 2, q = lane & 3;  // fragment row and quad member
-  stage_q<D, Wide, Axes>(p, r, b, kh, warp, lane, smem + Lay::kQOffset);
+  if constexpr (Blocks) copy_q<D, Wide>(p.q + ((int64_t)b * p.Hq + kh * G) * D, G, threadIdx.x, smem + Lay::kQOffset);
+  else stage_q<D, Wide, Axes>(p, r, b, kh, warp, lane, smem + Lay::kQOffset);
   named_sync_consumers();
   uint32_t qb[D / 16][2];  // Q of S column g (head g mod NH): columns q D/4 + 4 ks + {0, 1} and {2, 3}
   {
@@ -336,12 +360,13 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
         }
       }
     }
-    const int kt0 = k0 + i * 2 * kKeysPerTile + warp * 16;  // the warp's first key of the first half
-    const bool partial = kt0 + kKeysPerTile + 16 > k1;
+    // the warp's first keys in the halves
+    const int kt[2] = {tiles.pos(2 * i, k1) + warp * 16, tiles.pos(2 * i + 1, k1) + warp * 16};
+    const bool partial = kt[1] + 16 > k1 || (Blocks && kt[0] + 16 > k1);
     if (partial) {  // keys past the end: arbitrary bits, no part in the softmax
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = kt0 + t * kKeysPerTile + key_g;
+        const int key = kt[t] + key_g;
         if (key >= k1) s[t][0] = s[t][1] = kNegInf;
         if (key + 8 >= k1) s[t][2] = s[t][3] = kNegInf;
       }
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       if (partial) {  // keys past the end hold arbitrary bits: a scale of 0 makes their entries 0 (codes are finite)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int ka = kt0 + t * kKeysPerTile + key_a + 8 * h, kc = kt0 + t * kKeysPerTile + key_b + 8 * h;
+          const int ka = kt[t] + key_a + 8 * h, kc = kt[t] + key_b + 8 * h;
           if constexpr (Wide) {
             sc[2 * h] &= (ka < k1 ? 0xFFu : 0u) | (kc < k1 ? 0xFF00u : 0u);
           } else {
@@ -509,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     float L = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < kConsumerWarps; ++w) {
-      const float sw = fast_exp2(mm[w * G + row] - M);
+      const float sw = Blocks && M == kNegInf ? 0.f : fast_exp2(mm[w * G + row] - M);  // a list may leave no key
       L += sw * ml[w * G + row];
       acc += sw * mo[(w * G + row) * D + d];
     }
     const int64_t hrow = (int64_t)b * p.Hq + kh * G + row;
     if (direct) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(acc / L);
+      const __nv_bfloat16 v = __float2bfloat16_rn(Blocks && L == 0.f ? 0.f : acc / L);
       p.out[hrow * D + d] = *reinterpret_cast<const uint16_t*>(&v);
     } else {
       const int64_t prow = hrow * p.max_splits + split;
@@ -528,16 +553,17 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   }
 }
 
-template <int D, bool Wide, bool Axes>
+template <int D, bool Wide, bool Axes, bool Blocks>
 int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using Lay = E2m1Layout<D>;
   CacheMaps maps;
   if (make_cache_maps(a.kv, a.cfg.num_kv_heads, D, kKeysPerTile, &maps) != 0) return ATTN_ELAUNCH;
-  if (cudaFuncSetAttribute(decode_split_e2m1_kernel<D, Wide, Axes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(decode_split_e2m1_kernel<D, Wide, Axes, Blocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Lay::kSmemBytes) != cudaSuccess)
     return ATTN_ELAUNCH;
-  const dim3 grid(a.max_splits, a.cfg.num_kv_heads, a.B);
-  return launch_dependent(decode_split_e2m1_kernel<D, Wide, Axes>, grid, dim3(kThreads), Lay::kSmemBytes, stream,
+  const dim3 grid = Blocks ? dim3((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads)
+                           : dim3(a.max_splits, a.cfg.num_kv_heads, a.B);
+  return launch_dependent(decode_split_e2m1_kernel<D, Wide, Axes, Blocks>, grid, dim3(kThreads), Lay::kSmemBytes, stream,
                           maps.k, maps.v, decode_par(a)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ELAUNCH;
@@ -545,7 +571,7 @@ int launch_t(const DecodeArgs& a, cudaStream_t stream) {
 
 template <int D, bool Wide>
 int launch_n(const DecodeArgs& a, cudaStream_t stream) {
-  return a.axes.positions ? launch_t<D, Wide, true>(a, stream) : launch_t<D, Wide, false>(a, stream);
+  return a.axes.positions ? launch_t<D, Wide, true, false>(a, stream) : launch_t<D, Wide, false, false>(a, stream);
 }
 
 }  // namespace
@@ -554,6 +580,13 @@ int launch_decode_e2m1(const DecodeArgs& a, cudaStream_t stream) {
   const bool wide = a.cfg.num_q_heads / a.cfg.num_kv_heads > 4;
   if (a.cfg.head_dim == 128) return wide ? launch_n<128, true>(a, stream) : launch_n<128, false>(a, stream);
   return wide ? launch_n<64, true>(a, stream) : launch_n<64, false>(a, stream);
+}
+
+int launch_block_attend_e2m1(const DecodeArgs& a, cudaStream_t stream) {
+  const bool wide = a.cfg.num_q_heads / a.cfg.num_kv_heads > 4;
+  if (a.cfg.head_dim == 128)
+    return wide ? launch_t<128, true, false, true>(a, stream) : launch_t<128, false, false, true>(a, stream);
+  return wide ? launch_t<64, true, false, true>(a, stream) : launch_t<64, false, false, true>(a, stream);
 }
 
 }  // namespace gb300

@@ -78,7 +78,7 @@ extern "C" int attn_decode_static_scratch(const attn_config_t* cfg, const void* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
 
-  DecodeArgs d;
+  DecodeArgs d = {};
   d.cfg = *cfg;
   d.B = B;
   d.kv = load_kv(kv);

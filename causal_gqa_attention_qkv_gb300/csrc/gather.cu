@@ -5,6 +5,7 @@
 // positions, Hkv 8, D 128, 64-slot pages: bf16 155 us, 6.9 TB/s; E4M3 121 us, 6.7;
 // E2M1 116 us, 5.9); a decode step's 64 new entries by the launch, 3.9 us.
 #include "kernels.cuh"
+#include "kv_read.cuh"
 
 namespace gb300 {
 
@@ -25,32 +26,6 @@ struct GatherPar {
   uint4* v_out;
   int32_t* status;
 };
-
-// Eight entries at chunk c of head kh's vector in a slot, as bf16 pairs.
-template <int KV>
-__device__ __forceinline__ uint4 read8(const void* cache, const uint8_t* bscale, float scale, int64_t num_slots,
-                                       int64_t slot, int Hkv, int kh, int c, int log2_chunks) {
-  const int64_t row = ((slot * Hkv + kh) << log2_chunks) + c;  // in chunks
-  if constexpr (KV == ATTN_KV_BF16) return __ldg(static_cast<const uint4*>(cache) + row);
-  uint32_t h[4];
-  float s = 1.f;
-  if constexpr (KV == ATTN_KV_E4M3) {
-    const uint2 w = __ldg(static_cast<const uint2*>(cache) + row);
-    e4m3x4_to_f16(w.x, h[0], h[1]);
-    e4m3x4_to_f16(w.y, h[2], h[3]);
-  } else {
-    const int64_t blk = (((int64_t)kh * num_slots + slot) << (log2_chunks - 1)) + (c >> 1);
-    s = f16_lo(e4m3x2_to_f16(__ldg(bscale + blk)));
-    e2m1x8_to_f16(__ldg(static_cast<const uint32_t*>(cache) + row), h[0], h[1], h[2], h[3]);
-  }
-  uint32_t r[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
-    r[e] = pack_bf16(__fmul_rn(__fmul_rn(f.x, s), scale), __fmul_rn(__fmul_rn(f.y, s), scale));
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
 
 template <int KV>
 __global__ void __launch_bounds__(kWarps * 32) kv_gather_kernel(const GatherPar p) {

@@ -141,10 +141,24 @@ struct DecodeArgs {
   float* part_ml; // [B, Hq, max_splits, 2] fp32 (running max in log2 units, sum)
   int32_t split_len, max_splits;
   int32_t* status;
+  // attention over listed blocks (include/blocks.h): q, and list in place of qkv and
+  // its norm and rotation; a split is split_len entries of the list
+  const void* q;              // [N, Hq, D] prepared
+  const int32_t* cu_seqlens;  // NULL: one token per request
+  const int32_t* list;        // [N, Hkv, keep]
+  int32_t N, keep, log2_bs;
 };
 int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits, bool longer);
 int launch_decode(const DecodeArgs& a, cudaStream_t stream);
 int launch_decode_e2m1(const DecodeArgs& a, cudaStream_t stream);  // the split kernel over an E2M1 cache
+
+constexpr int kMaxListed = 4096;  // blocks of a list
+constexpr int kSplitPairs = 608;  // (token, KV head) pairs above which lists are not cut for more CTAs
+// How lists of `keep` blocks are cut: `per` entries in each of `splits` parts.
+void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per);
+size_t block_partial_bytes(const attn_config_t& c, int64_t N, int splits);
+int launch_block_attend(const DecodeArgs& a, cudaStream_t stream);
+int launch_block_attend_e2m1(const DecodeArgs& a, cudaStream_t stream);
 
 struct PrefillArgs {
   attn_config_t cfg;
