@@ -585,15 +585,7 @@ size_t attn_block_workspace_size(const attn_config_t* cfg, int32_t max_tokens, i
   if (abi_check_config(cfg) != ATTN_OK || max_tokens < 0 || max_kv_len < 1 || max_kv_len > (1 << 24)) return 0;
   if (!block_size_ok(block_size) || keep < 1 || keep > kMaxListed) return 0;
   const size_t scores = scores_bytes(cfg, max_tokens, blocks_of(max_kv_len, block_size));
-  // fewer tokens may be cut into more splits: the largest need of them all (from
-  // kSplitPairs tokens on the number of splits stays)
-  size_t parts = 0;
-  for (int64_t n = 1; n <= max_tokens; n = n == kSplitPairs && max_tokens > n ? max_tokens : n + 1) {
-    int splits, per;
-    block_splits(n * cfg->num_kv_heads, keep, block_size, &splits, &per);
-    parts = std::max(parts, block_partial_bytes(*cfg, n, splits));
-  }
-  return kWsHeader + align_up(std::max(scores, parts), 256);
+  return kWsHeader + align_up(scores, 256);
 }
 
 int attn_block_bounds(const attn_config_t* cfg, const attn_kv_t* kv, const attn_blocks_t* blocks,
@@ -662,11 +654,10 @@ int attn_block_attend(const attn_config_t* cfg, const void* q, const int32_t* cu
   if (B < 0 || N < 0 || (!cu_seqlens && N != B) || keep < 1 || keep > kMaxListed) return ATTN_EINVAL;
   DecodeArgs a = {};
   block_splits((int64_t)std::max(N, 1) * cfg->num_kv_heads, keep, block_size, &a.max_splits, &a.split_len);
-  if ((int64_t)N * std::max(a.max_splits, cfg->num_q_heads) > 0x7fffffff) return ATTN_EINVAL;
-  if (!ws_fits(workspace, ws_bytes, kWsHeader + block_partial_bytes(*cfg, N, a.max_splits))) return ATTN_EWORKSPACE;
+  if ((int64_t)N * a.max_splits > 0x7fffffff) return ATTN_EINVAL;
+  if (!ws_fits(workspace, ws_bytes, kWsHeader)) return ATTN_EWORKSPACE;
   if ((rc = abi_check_device())) return rc;
   if (N == 0 || B == 0) return ATTN_OK;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.cfg = *cfg;
   a.B = B;
   a.kv = load_kv(kv);
@@ -677,9 +668,6 @@ int attn_block_attend(const attn_config_t* cfg, const void* q, const int32_t* cu
   a.keep = keep;
   a.log2_bs = log2_of(block_size);
   a.out = out;
-  a.part_o = reinterpret_cast<float*>(ws + kWsHeader);
-  a.part_ml = reinterpret_cast<float*>(
-      ws + kWsHeader + align_up((size_t)N * cfg->num_q_heads * a.max_splits * cfg->head_dim * 4, 256));
   a.status = static_cast<int32_t*>(workspace);
   return launch_block_attend(a, static_cast<cudaStream_t>(stream));
 }

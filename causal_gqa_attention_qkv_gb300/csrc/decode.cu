@@ -170,6 +170,10 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         set_status(p.status, ATTN_STATUS_TIMEOUT);
       }
     }
+    if constexpr (Blocks) {
+      __syncwarp();
+      block_merge_rest(p);
+    }
     return;
   }
 
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
 
   // ---------------- merge the four warps' partial softmax states
   named_sync_consumers();  // every consumer is done with the stage buffers
-  if (s_cons_abort) return;  // same value for every consumer thread
+  if (!Blocks && s_cons_abort) return;  // same value for every consumer thread
   float* mo = reinterpret_cast<float*>(smem);                 // [warps][G][D]
   float* mm = mo + kConsumerWarps * G * D;                      // [warps][G]
   float* ml = mm + kConsumerWarps * G;                          // [warps][G]
@@ -468,6 +472,10 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     }
   }
   named_sync_consumers();
+  if constexpr (Blocks) {
+    block_merge<D>(p, mo, mm, ml, kh, b);
+    return;
+  }
   const bool direct = n_splits == 1;
   for (int idx = threadIdx.x; idx < G * D; idx += kConsumerWarps * 32) {
     const int row = idx / D, d = idx % D;
@@ -477,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
     float L = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < kConsumerWarps; ++w) {
-      const float sw = Blocks && M == kNegInf ? 0.f : fast_exp2(mm[w * G + row] - M);  // a list may leave no key
+      const float sw = fast_exp2(mm[w * G + row] - M);
       L += sw * ml[w * G + row];
       acc += sw * mo[(w * G + row) * D + d];
     }
     const int64_t hrow = (int64_t)b * p.Hq + h0 + row;
     if (direct) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(Blocks && L == 0.f ? 0.f : acc / L);
+      const __nv_bfloat16 v = __float2bfloat16_rn(acc / L);
       p.out[hrow * D + d] = *reinterpret_cast<const uint16_t*>(&v);
     } else {
       const int64_t prow = hrow * p.max_splits + split;
@@ -518,56 +526,20 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const DecodePar p) {
   p.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&v);
 }
 
-// The merge over the splits of listed blocks: some, or all, may have had no key.
-template <int D>
-__global__ void __launch_bounds__(D) block_combine_kernel(const DecodePar p) {
-  const int64_t row = blockIdx.x;  // token * Hq + head
-  const int d = threadIdx.x;
-  grid_dependency_wait();  // the split kernel's partial results
-  int b, n, j;
-  if (!find_token(p.cu_seqlens, p.B, (int)(row / p.Hq), &b, &n, &j)) return;
-  if (!load_request(p.kv, b, n).valid) return;
-  const float* ml = p.part_ml + row * p.max_splits * 2;
-  float M = kNegInf;
-  for (int s = 0; s < p.max_splits; ++s) M = fmaxf(M, ml[2 * s]);
-  float L = 0.f, acc = 0.f;
-  for (int s = 0; s < p.max_splits; ++s) {
-    const float w = M == kNegInf ? 0.f : fast_exp2(ml[2 * s] - M);
-    L += w * ml[2 * s + 1];
-    acc += w * p.part_o[(row * p.max_splits + s) * D + d];
-  }
-  const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-  p.out[row * D + d] = *reinterpret_cast<const uint16_t*>(&v);
-}
-
-template <int D, bool F8, bool Blocks>
+template <int D, bool F8>
 int launch_block_attend_t(const DecodeArgs& a, cudaStream_t stream) {
-  using Lay = DecodeLayout<D, F8>;
   CacheMaps maps;
   if (make_cache_maps(a.kv, a.cfg.num_kv_heads, D, kKeysPerTile, &maps) != 0) return ATTN_ELAUNCH;
-  if (cudaFuncSetAttribute(decode_split_kernel<D, F8, false, Blocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Lay::kSmemBytes) != cudaSuccess)
-    return ATTN_ELAUNCH;
-  const dim3 grid((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads);
-  return launch_dependent(decode_split_kernel<D, F8, false, Blocks>, grid, dim3(kThreads), Lay::kSmemBytes, stream,
-                          maps.k, maps.v, decode_par(a)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ELAUNCH;
+  return launch_block_splits(decode_split_kernel<D, F8, false, true>, DecodeLayout<D, F8>::kSmemBytes, a, maps, stream);
 }
 
 template <int D>
 int launch_block_attend_d(const DecodeArgs& a, cudaStream_t stream) {
-  int rc;
   switch (a.kv.kv_dtype) {
-    case ATTN_KV_E4M3: rc = launch_block_attend_t<D, true, true>(a, stream); break;
-    case ATTN_KV_E2M1: rc = launch_block_attend_e2m1(a, stream); break;
-    default: rc = launch_block_attend_t<D, false, true>(a, stream);
+    case ATTN_KV_E4M3: return launch_block_attend_t<D, true>(a, stream);
+    case ATTN_KV_E2M1: return launch_block_attend_e2m1(a, stream);
+    default: return launch_block_attend_t<D, false>(a, stream);
   }
-  if (rc) return rc;
-  if (a.max_splits > 1 && launch_dependent(block_combine_kernel<D>, dim3((unsigned)(a.N * a.cfg.num_q_heads)), dim3(D),
-                                           0, stream, decode_par(a)) != cudaSuccess)
-    return ATTN_ELAUNCH;
-  return ATTN_OK;
 }
 
 template <int D, bool F8, bool Axes>
@@ -635,12 +607,6 @@ void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per
   n = std::max<int64_t>(n, (keep + kMaxSplitBlocks - 1) / kMaxSplitBlocks);
   *per = (int)((keep + n - 1) / n);
   *splits = (keep + *per - 1) / *per;
-}
-
-size_t block_partial_bytes(const attn_config_t& c, int64_t N, int splits) {
-  if (splits <= 1) return 0;
-  const size_t rows = (size_t)N * c.num_q_heads * splits;
-  return align_up(rows * c.head_dim * 4, 256) + align_up(rows * 2 * 4, 256);
 }
 
 int launch_block_attend(const DecodeArgs& a, cudaStream_t stream) {

@@ -206,6 +206,87 @@ __device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int 
   return true;
 }
 
+// ---------------------------------------------------------------- merge of listed blocks
+// The splits of a list are one cluster and merge through distributed shared memory: no
+// partial results in memory and no second launch.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at `addr` (a shared memory address of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+constexpr int kMergeBytes = 2 * 8 * 4;  // behind the warps' partial results: this CTA's maxima and sums
+
+// The output rows of token t's group from the warps' partial results mo [warps][G][D], mm
+// and ml [warps][G] (maximum, sum) of every split.  All consumer threads call this;
+// the producer warp calls block_merge_rest().  A list may leave a warp, a split or the token
+// without a key: their maxima are -inf, and no key at all gives zeros.
+template <int D>
+__device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const float* mm, float* ml, int kh, int t) {
+  const int G = p.G, splits = p.max_splits;
+  float* cm = ml + kConsumerWarps * G;  // [G]
+  float* cl = cm + G;
+  uint16_t* out = p.out + ((int64_t)t * p.Hq + kh * G) * D;
+  auto store = [&](int idx, float acc, float L) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+    out[idx] = *reinterpret_cast<const uint16_t*>(&v);
+  };
+  for (int idx = threadIdx.x; idx < G * D; idx += kConsumerWarps * 32) {
+    const int row = idx / D;
+    float M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, mm[w * G + row]);
+    float L = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConsumerWarps; ++w) {
+      const float sw = M == kNegInf ? 0.f : fast_exp2(mm[w * G + row] - M);
+      L += sw * ml[w * G + row];
+      acc += sw * mo[w * G * D + idx];
+    }
+    if (splits == 1) {
+      store(idx, acc, L);
+    } else {
+      mo[idx] = acc;  // read by this thread only
+      if (idx % D == 0) {
+        cm[row] = M;
+        cl[row] = L;
+      }
+    }
+  }
+  if (splits == 1) return;
+  cluster_sync();
+  for (int idx = cluster_rank() * kConsumerWarps * 32 + threadIdx.x; idx < G * D; idx += splits * kConsumerWarps * 32) {
+    const uint32_t am = smem_u32(cm + idx / D), al = smem_u32(cl + idx / D), ao = smem_u32(mo + idx);
+    float M = kNegInf;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) M = fmaxf(M, peer_f32(am, s));
+    float L = 0.f, acc = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float w = M == kNegInf ? 0.f : fast_exp2(peer_f32(am, s) - M);
+      L += w * peer_f32(al, s);
+      acc += w * peer_f32(ao, s);
+    }
+    store(idx, acc, L);
+  }
+  cluster_sync();  // no CTA leaves while another reads from it
+}
+__device__ __forceinline__ void block_merge_rest(const DecodePar& p) {
+  if (p.max_splits == 1) return;
+  cluster_sync();
+  cluster_sync();
+}
+
 // The kernels' form of a call's arguments.
 inline DecodePar decode_par(const DecodeArgs& a) {
   const int D = a.cfg.head_dim;
@@ -243,6 +324,28 @@ inline DecodePar decode_par(const DecodeArgs& a) {
   p.keep = a.keep;
   p.log2_bs = a.log2_bs;
   return p;
+}
+
+// Launch of a split kernel over listed blocks: the splits of a (token, KV head) form a cluster.
+template <typename Kernel>
+int launch_block_splits(Kernel kernel, size_t smem, const DecodeArgs& a, const CacheMaps& maps, cudaStream_t stream) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return ATTN_ELAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.max_splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, maps.k, maps.v, decode_par(a)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 }  // namespace

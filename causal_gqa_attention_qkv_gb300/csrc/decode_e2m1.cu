@@ -62,7 +62,7 @@ struct E2m1Layout {
   static constexpr int kQOffset = kStages * kStageBytes;            // prepared Q: 8 heads x D f16
   static constexpr int kBarOffset = kQOffset + 8 * D * 2;
   static constexpr int kSmemBytes = kBarOffset + 2 * kStages * 8 + 1024;  // + alignment slack
-  static_assert(kQOffset >= kConsumerWarps * 8 * D * 4 + 2 * kConsumerWarps * 8 * 4, "the warps' partial results fit the stages");
+  static_assert(kQOffset >= kConsumerWarps * 8 * D * 4 + 2 * kConsumerWarps * 8 * 4 + kMergeBytes, "the warps' partial results fit the stages");
 };
 
 // Byte offset of `byte` of key row `key` in a tile of codes (D = 128: the 16-byte
@@ -262,6 +262,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     if (!ok) {  // let the copies still in flight land before exit
       for (int i = max(0, issued - S); i < issued; ++i) (void)mbar_wait(&full[i % S], (i / S) & 1);
       if (lane == 0) set_status(p.status, ATTN_STATUS_TIMEOUT);
+    }
+    if constexpr (Blocks) {
+      __syncwarp();
+      block_merge_rest(p);
     }
     return;
   }
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
 
   // ---------------- merge the warps' partial softmax states
   named_sync_consumers();  // every consumer is done with the stage buffers
-  if (s_cons_abort) return;  // same value for every consumer thread
+  if (!Blocks && s_cons_abort) return;  // same value for every consumer thread
   float* mo = reinterpret_cast<float*>(smem);  // [warps][G][D]
   float* mm = mo + kConsumerWarps * G * D;         // [warps][G]
   float* ml = mm + kConsumerWarps * G;                 // [warps][G]
@@ -525,6 +529,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       ml[warp * G + 2 * q + e] = l[e];
     }
   named_sync_consumers();
+  if constexpr (Blocks) {
+    block_merge<D>(p, mo, mm, ml, kh, b);
+    return;
+  }
   const bool direct = n_splits == 1;
   for (int idx = threadIdx.x; idx < G * D; idx += kConsumerWarps * 32) {
     const int row = idx / D, d = idx % D;
@@ -534,13 +542,13 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     float L = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < kConsumerWarps; ++w) {
-      const float sw = Blocks && M == kNegInf ? 0.f : fast_exp2(mm[w * G + row] - M);  // a list may leave no key
+      const float sw = fast_exp2(mm[w * G + row] - M);
       L += sw * ml[w * G + row];
       acc += sw * mo[(w * G + row) * D + d];
     }
     const int64_t hrow = (int64_t)b * p.Hq + kh * G + row;
     if (direct) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(Blocks && L == 0.f ? 0.f : acc / L);
+      const __nv_bfloat16 v = __float2bfloat16_rn(acc / L);
       p.out[hrow * D + d] = *reinterpret_cast<const uint16_t*>(&v);
     } else {
       const int64_t prow = hrow * p.max_splits + split;
@@ -558,15 +566,18 @@ int launch_t(const DecodeArgs& a, cudaStream_t stream) {
   using Lay = E2m1Layout<D>;
   CacheMaps maps;
   if (make_cache_maps(a.kv, a.cfg.num_kv_heads, D, kKeysPerTile, &maps) != 0) return ATTN_ELAUNCH;
-  if (cudaFuncSetAttribute(decode_split_e2m1_kernel<D, Wide, Axes, Blocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Lay::kSmemBytes) != cudaSuccess)
-    return ATTN_ELAUNCH;
-  const dim3 grid = Blocks ? dim3((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads)
-                           : dim3(a.max_splits, a.cfg.num_kv_heads, a.B);
-  return launch_dependent(decode_split_e2m1_kernel<D, Wide, Axes, Blocks>, grid, dim3(kThreads), Lay::kSmemBytes, stream,
-                          maps.k, maps.v, decode_par(a)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ELAUNCH;
+  if constexpr (Blocks) {
+    return launch_block_splits(decode_split_e2m1_kernel<D, Wide, Axes, true>, Lay::kSmemBytes, a, maps, stream);
+  } else {
+    if (cudaFuncSetAttribute(decode_split_e2m1_kernel<D, Wide, Axes, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Lay::kSmemBytes) != cudaSuccess)
+      return ATTN_ELAUNCH;
+    const dim3 grid(a.max_splits, a.cfg.num_kv_heads, a.B);
+    return launch_dependent(decode_split_e2m1_kernel<D, Wide, Axes, false>, grid, dim3(kThreads), Lay::kSmemBytes,
+                            stream, maps.k, maps.v, decode_par(a)) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ELAUNCH;
+  }
 }
 
 template <int D, bool Wide>

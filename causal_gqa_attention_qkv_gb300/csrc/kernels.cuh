@@ -156,7 +156,6 @@ constexpr int kMaxListed = 4096;  // blocks of a list
 constexpr int kSplitPairs = 608;  // (token, KV head) pairs above which lists are not cut for more CTAs
 // How lists of `keep` blocks are cut: `per` entries in each of `splits` parts.
 void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per);
-size_t block_partial_bytes(const attn_config_t& c, int64_t N, int splits);
 int launch_block_attend(const DecodeArgs& a, cudaStream_t stream);
 int launch_block_attend_e2m1(const DecodeArgs& a, cudaStream_t stream);
 
