@@ -600,11 +600,14 @@ int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits, bool longe
   return (int)len;
 }
 
+// One split per (token, KV head) where those fill the card at two CTAs per SM, as many as
+// fit there where they do not, of 256 keys or more.  64 tokens with 8 KV heads, 4096 keys
+// each: 161 us (one split), 174, 186, 182 (2, 3, 4); one token with 8: 41, 24, 15, 10.9, 9.1 us
+// (1, 2, 4, 8, 16).
 void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per) {
   const int64_t tiles = (int64_t)keep * (block_size / 64);
-  int64_t n = (kSplitPairs + pairs - 1) / pairs;
-  n = std::min<int64_t>(std::min<int64_t>(n, 16), std::max<int64_t>(1, tiles / 4));
-  n = std::max<int64_t>(n, (keep + kMaxSplitBlocks - 1) / kMaxSplitBlocks);
+  int64_t n = std::min<int64_t>(std::min<int64_t>(304 / pairs, 16), tiles / 4);
+  n = std::max<int64_t>(std::max<int64_t>(n, 1), (keep + kMaxSplitBlocks - 1) / kMaxSplitBlocks);
   *per = (int)((keep + n - 1) / n);
   *splits = (keep + *per - 1) / *per;
 }

@@ -153,7 +153,6 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream);
 int launch_decode_e2m1(const DecodeArgs& a, cudaStream_t stream);  // the split kernel over an E2M1 cache
 
 constexpr int kMaxListed = 4096;  // blocks of a list
-constexpr int kSplitPairs = 608;  // (token, KV head) pairs above which lists are not cut for more CTAs
 // How lists of `keep` blocks are cut: `per` entries in each of `splits` parts.
 void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per);
 int launch_block_attend(const DecodeArgs& a, cudaStream_t stream);
