@@ -202,6 +202,7 @@ class KVCache:
             object.__setattr__(self, "_built", None)
             object.__setattr__(self, "_built_pages", None)
             object.__setattr__(self, "_fits", None)
+            object.__setattr__(self, "_requests", None)
 
     @property
     def kv_dtype(self) -> int:
@@ -279,6 +280,15 @@ class KVCache:
             object.__setattr__(self, "_built_pages", built)
         assert ref_count.numel() >= built[3], "ref_count"
         return AttnPages(built[0], _i32(ref_count, "ref_count"), built[1], built[2])
+
+    def requests(self) -> int:
+        """How many requests the cache's tensors have room for (looked up once, like struct())."""
+        n = self.__dict__.get("_requests")
+        if n is None:
+            rows = self.slot_base.numel() if self.page_table is None else self.page_table.shape[0]
+            n = min(rows, self.slot_capacity.numel(), self.cache_lens.numel())
+            object.__setattr__(self, "_requests", n)
+        return n
 
     def rows(self, lo: int, hi: int, cache_lens: torch.Tensor | None = None) -> "KVCache":
         """The same cache seen by the requests [lo, hi) (with other cached
@@ -537,13 +547,25 @@ class BlockBounds:
     block_size: int = 64
     row_base: torch.Tensor | None = None
 
+    # Built (and the tensors checked) once, and again when a field is assigned.
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_built":
+            object.__setattr__(self, "_built", None)
+
     def struct(self, cfg: AttnConfig, rows: int) -> AttnBlocks:
-        t, base = self.bounds, self.row_base
-        assert t.dtype == torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.dim() == 4, "bounds"
-        assert tuple(t.shape[1:]) == (cfg.num_kv_heads, 2, cfg.head_dim), "bounds"
-        if base is not None:
-            assert base.dtype == torch.int64 and base.is_cuda and base.is_contiguous() and base.numel() >= rows, "row_base"
-        return AttnBlocks(t.data_ptr(), t.shape[0], _ptr(base), int(self.block_size))
+        built, key = self.__dict__["_built"], (cfg.num_kv_heads, cfg.head_dim)
+        if built is None or built[0] != key:
+            t, base = self.bounds, self.row_base
+            assert t.dtype == torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.dim() == 4, "bounds"
+            assert tuple(t.shape[1:]) == (cfg.num_kv_heads, 2, cfg.head_dim), "bounds"
+            if base is not None:
+                assert base.dtype == torch.int64 and base.is_cuda and base.is_contiguous(), "row_base"
+            most = (1 << 31) if base is None else base.numel()
+            built = (key, most, AttnBlocks(t.data_ptr(), t.shape[0], _ptr(base), int(self.block_size)))
+            object.__setattr__(self, "_built", built)
+        assert rows <= built[1], "row_base"
+        return built[2]
 
 
 def new_block_bounds(cfg: AttnConfig, kv: KVCache, block_size: int = 64) -> BlockBounds:
@@ -568,20 +590,22 @@ def new_block_workspace(cfg: AttnConfig, max_tokens: int, max_kv_len: int, block
 def _requests(cu_seqlens, kv: KVCache, n=None):
     """(pointer, B) of cu_seqlens; None: one token for each of the n requests (by default
     those of the cache's lengths)."""
+    most = kv.requests()
     if cu_seqlens is None:
-        p, B = None, kv.cache_lens.numel() if n is None else n
+        p, B = None, most if n is None else n
     else:
         p, B = _i32(cu_seqlens, "cu_seqlens"), cu_seqlens.numel() - 1
-    rows = kv.slot_base.numel() if kv.page_table is None else kv.page_table.shape[0]
-    assert 0 <= B <= min(rows, kv.slot_capacity.numel(), kv.cache_lens.numel()), "cu_seqlens"
+    assert 0 <= B <= most, "cu_seqlens"
     return p, B
 
 
 def _prepared_q(cfg: AttnConfig, q, kv: KVCache):
+    """The address of a prepared Q [N, Hq, D] for this cache, and N."""
     want = torch.bfloat16 if kv.kv_dtype == ATTN_KV_BF16 else torch.float16
     assert q.dtype == want and q.is_cuda and q.is_contiguous(), "q"
-    assert q.dim() == 3 and tuple(q.shape[1:]) == (cfg.num_q_heads, cfg.head_dim), "q"
-    return q.data_ptr()
+    N, H, D = q.shape
+    assert H == cfg.num_q_heads and D == cfg.head_dim, "q"
+    return q.data_ptr(), N
 
 
 def block_bounds(cfg: AttnConfig, kv: KVCache, blocks: BlockBounds, cu_seqlens, workspace, start=None, stream=None):
@@ -602,26 +626,28 @@ def block_select(cfg: AttnConfig, q, cu_seqlens, max_kv_len: int, kv: KVCache, b
     """The blocks of each query into ``out_list`` (int32 [N, Hkv, keep]): all, or the
     ``first`` first, the ``last`` last and the best of the others, ascending, -1
     behind them.  q: the prepared Q [N, Hq, D] of prefill_prepare."""
-    cu, B = _requests(cu_seqlens, kv, q.shape[0])
-    N = q.shape[0]
-    assert out_list.dim() == 3 and tuple(out_list.shape[:2]) == (N, cfg.num_kv_heads), "out_list"
-    qp, s, k = _prepared_q(cfg, q, kv), kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
-    _check(load().attn_block_select(ctypes.byref(cfg), qp, cu, B, N, int(max_kv_len), ctypes.byref(s), ctypes.byref(k),
-                                    int(first), int(last), out_list.shape[2], _i32(out_list, "out_list"),
-                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+    qp, N = _prepared_q(cfg, q, kv)
+    cu, B = _requests(cu_seqlens, kv, N)
+    n, H, keep = out_list.shape
+    assert n == N and H == cfg.num_kv_heads, "out_list"
+    s, k = kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
+    _check(load().attn_block_select(ctypes.byref(cfg), qp, cu, B, N, max_kv_len, ctypes.byref(s), ctypes.byref(k), first,
+                                    last, keep, _i32(out_list, "out_list"), workspace.data_ptr(), workspace.numel(),
+                                    _stream(stream)))
 
 
 def block_attend(cfg: AttnConfig, q, cu_seqlens, kv: KVCache, block_size: int, block_list, out, workspace, stream=None):
     """Causal attention of the prepared Q ``q`` [N, Hq, D] over the blocks listed in
     ``block_list`` (int32 [N, Hkv, keep]) into ``out`` (bf16 [N, Hq*D])."""
-    cu, B = _requests(cu_seqlens, kv, q.shape[0])
-    N = q.shape[0]
-    assert block_list.dim() == 3 and tuple(block_list.shape[:2]) == (N, cfg.num_kv_heads), "block_list"
+    qp, N = _prepared_q(cfg, q, kv)
+    cu, B = _requests(cu_seqlens, kv, N)
+    n, H, keep = block_list.shape
+    assert n == N and H == cfg.num_kv_heads, "block_list"
     assert out.numel() >= q.numel(), "out"
-    qp, s = _prepared_q(cfg, q, kv), kv.struct_for(cfg, exact=True)
-    _check(load().attn_block_attend(ctypes.byref(cfg), qp, cu, B, N, ctypes.byref(s), int(block_size),
-                                    _i32(block_list, "block_list"), block_list.shape[2], _bf16(out, "out"),
-                                    _ptr(workspace), workspace.numel(), _stream(stream)))
+    s = kv.struct_for(cfg, exact=True)
+    _check(load().attn_block_attend(ctypes.byref(cfg), qp, cu, B, N, ctypes.byref(s), block_size,
+                                    _i32(block_list, "block_list"), keep, _bf16(out, "out"), workspace.data_ptr(),
+                                    workspace.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- logits (include/logits.h)

@@ -15,6 +15,7 @@
 // bound; a score above t + 2 E belongs to the K largest whatever the errors
 // are, one below t - 2 E does not, and only those between are summed again in fp64.
 // (At least K exact scores are >= t - E and fewer than K of the others exceed t + E.)
+#include "cluster.cuh"
 #include "kernels.cuh"
 #include "kv_read.cuh"
 #include "../../include/blocks.h"
@@ -53,7 +54,9 @@ struct BlocksPar {
   // selection
   const uint16_t* q;         // [N, Hq, D]
   int32_t q_f16, N, G, first, last, keep, max_blocks, chunk, chunks;
-  float2* scores;            // [N, Hkv, max_blocks]: score, bound on its error
+  float* scores;             // [N, Hkv, max_blocks]
+  float* errors;             // [N, Hkv, chunks]: bounds on the errors of a chunk's scores
+  unsigned long long* keys;  // [N, Hkv, max_blocks] exact scores, where they are needed
   int32_t* list;             // [N, Hkv, keep]
 };
 
@@ -126,7 +129,20 @@ __device__ __forceinline__ float q_value(uint32_t bits, int f16) {
   return f16 ? __half2float(__ushort_as_half((uint16_t)bits)) : __uint_as_float(bits << 16);
 }
 
-// How many blocks a query sees, 0 if it gets no list; `report`: this thread sets the status.
+// How many blocks the query at place j of a request sees, 0 if it gets no list; `report`:
+// this thread sets the status.
+__device__ __forceinline__ int visible_blocks(const BlocksPar& p, const ReqInfo& r, int j, bool report) {
+  if (!r.valid) {
+    if (report) set_status(p.status, ATTN_STATUS_CAPACITY);
+    return 0;
+  }
+  const int blocks = ((r.cached + j) >> p.log2_bs) + 1;
+  if (blocks > p.max_blocks) {
+    if (report) set_status(p.status, ATTN_STATUS_BOUNDS);
+    return 0;
+  }
+  return blocks;
+}
 __device__ __forceinline__ int query_blocks(const BlocksPar& p, int t, ReqInfo* r, int* b, bool report) {
   int n, j;
   if (!find_token(p.cu_seqlens, p.B, t, b, &n, &j)) {
@@ -134,59 +150,62 @@ __device__ __forceinline__ int query_blocks(const BlocksPar& p, int t, ReqInfo* 
     return 0;
   }
   *r = load_request(p.kv, *b, n);
-  if (!r->valid) {
-    if (report) set_status(p.status, ATTN_STATUS_CAPACITY);
-    return 0;
-  }
-  const int blocks = ((r->cached + j) >> p.log2_bs) + 1;
-  if (blocks > p.max_blocks) {
-    if (report) set_status(p.status, ATTN_STATUS_BOUNDS);
-    return 0;
-  }
-  return blocks;
+  return visible_blocks(p, *r, j, report);
 }
 
-// Rounding of a score: each term goes through at most 7 additions in M or P, 8 in its
-// lane's chain and 5 between lanes, 20 half steps of its magnitude; the sum of magnitudes is
-// rounded likewise.  What products below the normal range lose is less than the constant.
+// M and P of token t and KV head kh, for component d; a NaN enters both.
+template <typename T>
+__device__ __forceinline__ void coefficients(const BlocksPar& p, int t, int kh, int D, int d, T* m, T* q) {
+  const uint16_t* row = p.q + ((int64_t)t * p.Hkv + kh) * p.G * D + d;
+  T lo = 0, hi = 0;
+#pragma unroll 4
+  for (int h = 0; h < p.G; ++h) {
+    const float x = q_value(__ldg(row + h * D), p.q_f16);
+    lo += x > 0.f ? T(0) : (T)x;
+    hi += x < 0.f ? T(0) : (T)x;
+  }
+  *m = lo;
+  *q = hi;
+}
+
+// Two fp32 operations in one instruction, each rounded to nearest even.
+__device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t v) {
+  return (uint64_t)(v & 0xFFFF0000u) << 32 | (uint64_t)(v << 16);
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Rounding of a score: each term goes through at most 7 additions in M or P, 5 in its
+// lane's two chains and 5 between lanes, 17 half steps of its magnitude.  The bound on the sum of
+// magnitudes takes for each component the largest magnitude among the blocks (half an
+// instruction per component, and the same for every token; sums of each block's own cost 24 us
+// more of 62 for 55 tokens over 1000 blocks), is rounded likewise, and what products below the
+// normal range lose is less than the constant.
 constexpr float kErrorOfMagnitude = 24.f * 5.9604645e-8f;
 constexpr float kErrorFloor = 1e-40f;
 
-// A warp takes 8 blocks at a time: lane l of the D / 4 lanes of a block holds 8
-// components of lo (the first half of the lanes) or hi.
-template <int D>
-__global__ void __launch_bounds__(kThreads) block_score_kernel(const BlocksPar p) {
+// Scores of the blocks [i0, i1) of a request for some tokens, by the CTA: a warp takes 8 blocks
+// (D = 64: 16) at a time, lane l of the D / 4 lanes of a block holds 8 components of lo (the
+// first half of the lanes) or hi.  coef: M, P of each token; put(k, block, score); err(k,
+// bound on the error of this warp's scores), by one lane.  Returns whether a row lay outside.
+template <int D, typename Put, typename Err>
+__device__ __forceinline__ bool score_blocks(const BlocksPar& p, const ReqInfo& r, int b, int kh, int i0, int i1,
+                                             int tokens, const float (*coef)[2 * D], Put&& put, Err&& err) {
   constexpr int L = D / 4, BPW = 32 / L;  // lanes per block, blocks per warp and load
-  __shared__ float coef[2 * D];           // M, P
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kh = blockIdx.x / p.chunks % p.Hkv, t = blockIdx.x / p.chunks / p.Hkv, c = blockIdx.x % p.chunks;
-  launch_dependents();
-  grid_dependency_wait();
-  ReqInfo r;
-  int b;
-  const int n = query_blocks(p, t, &r, &b, c == 0 && kh == 0 && threadIdx.x == 0);
-  const int i0 = p.first + c * p.chunk, i1 = min(i0 + p.chunk, n - p.last);
-  if (n <= p.keep || i0 >= i1) return;
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float m = 0.f, q = 0.f;
-    for (int h = 0; h < p.G; ++h) {
-      const float x = q_value(__ldg(p.q + ((int64_t)t * p.Hkv * p.G + kh * p.G + h) * D + d), p.q_f16);
-      // a NaN enters both
-      m += x > 0.f ? 0.f : x;
-      q += x < 0.f ? 0.f : x;
-    }
-    coef[d] = m;
-    coef[D + d] = q;
-  }
-  __syncthreads();
-  const int li = lane % L, sub = lane / L;
-  float w[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = coef[8 * li + e];
-  float2* out = p.scores + ((int64_t)t * p.Hkv + kh) * p.max_blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % L, sub = lane / L;
   bool outside = false;
+  uint4 big = make_uint4(0, 0, 0, 0);  // largest magnitudes
+  const uint4* rows = reinterpret_cast<const uint4*>(p.bounds) + kh * (D / 4) + li;
   for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
-    // rows of the warp's 8 * BPW blocks, one per lane
+    // rows of the warp's blocks, one per lane
     int64_t row = -1;
     if (lane < 8 * BPW && i + lane < i1) {
       row = bounds_row(p, r, b, i + lane);
@@ -196,42 +215,118 @@ __global__ void __launch_bounds__(kThreads) block_score_kernel(const BlocksPar p
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t rk = __shfl_sync(0xffffffffu, row, k * BPW + sub);
-      x[k] = rk < 0 ? make_uint4(0, 0, 0, 0)
-                    : __ldg(reinterpret_cast<const uint4*>(p.bounds + (rk * p.Hkv + kh) * (2 * D)) + li);
+      x[k] = rk < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + rk * (p.Hkv * (D / 4)));
     }
-    float s[8], a[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float y[8];
-      unpack_bf16x8(x[k], y);
-      s[k] = w[0] * y[0];
-      a[k] = fabsf(s[k]);
+    for (int k = 0; k < 8; ++k)
+      big = make_uint4(max2(big.x, x[k].x & 0x7FFF7FFFu), max2(big.y, x[k].y & 0x7FFF7FFFu),
+                       max2(big.z, x[k].z & 0x7FFF7FFFu), max2(big.w, x[k].w & 0x7FFF7FFFu));
 #pragma unroll
-      for (int e = 1; e < 8; ++e) {
-        s[k] = fmaf(w[e], y[e], s[k]);
-        a[k] = fmaf(fabsf(w[e]), fabsf(y[e]), a[k]);
+    for (int g = 0; g < 8; g += 4) {
+      uint64_t y[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        y[k][0] = bf16x2_to_f32x2(x[g + k].x);
+        y[k][1] = bf16x2_to_f32x2(x[g + k].y);
+        y[k][2] = bf16x2_to_f32x2(x[g + k].z);
+        y[k][3] = bf16x2_to_f32x2(x[g + k].w);
+      }
+#pragma unroll 1
+      for (int t = 0; t < tokens; ++t) {
+        uint64_t w[4];  // pairs of coefficients
+        float s[4];
+        *reinterpret_cast<ulonglong2*>(w) = *reinterpret_cast<const ulonglong2*>(&coef[t][8 * li]);
+        *reinterpret_cast<ulonglong2*>(w + 2) = *reinterpret_cast<const ulonglong2*>(&coef[t][8 * li + 4]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint64_t acc = mul_f32x2(w[0], y[k][0]);
+#pragma unroll
+          for (int e = 1; e < 4; ++e) acc = fma_f32x2(w[e], y[k][e], acc);
+          s[k] = __uint_as_float((uint32_t)acc) + __uint_as_float((uint32_t)(acc >> 32));
+        }
+        // sums over the block's lanes; of the 4 values each lane keeps the one of its bits 0, 1
+#pragma unroll
+        for (int half = 2; half >= 1; half >>= 1) {
+          const bool up = lane & half;
+#pragma unroll
+          for (int k = 0; k < half; ++k) {
+            const float give = up ? s[k] : s[k + half];
+            s[k] = (up ? s[k + half] : s[k]) + __shfl_xor_sync(0xffffffffu, give, half);
+          }
+        }
+#pragma unroll
+        for (int off = 4; off < L; off <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
+        const int at = i + (g + (lane & 3)) * BPW + sub;
+        if (li < 4 && at < i1) put(t, at, s[0]);
       }
     }
-    // sums over the block's lanes; of the 8 values each lane keeps the one of its bits 0 .. 2
-#pragma unroll
-    for (int half = 4; half >= 1; half >>= 1) {
-      const bool up = lane & half;
-#pragma unroll
-      for (int k = 0; k < half; ++k) {
-        const float give_s = up ? s[k] : s[k + half], give_a = up ? a[k] : a[k + half];
-        s[k] = (up ? s[k + half] : s[k]) + __shfl_xor_sync(0xffffffffu, give_s, half);
-        a[k] = (up ? a[k + half] : a[k]) + __shfl_xor_sync(0xffffffffu, give_a, half);
-      }
-    }
-#pragma unroll
-    for (int off = 8; off < L; off <<= 1) {
-      s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
-      a[0] += __shfl_xor_sync(0xffffffffu, a[0], off);
-    }
-    const int at = i + (lane & 7) * BPW + sub;
-    if (li < 8 && at < i1) out[at] = make_float2(s[0], fmaf(a[0], kErrorOfMagnitude, kErrorFloor));
   }
-  if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
+  float y[8];
+  unpack_bf16x8(big, y);
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    float a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaf(fabsf(coef[t][8 * li + e]), y[e], a);
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    if (BPW > 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, L & 31));
+    if (lane == 0) err(t, fmaf(a, kErrorOfMagnitude, kErrorFloor));
+  }
+  return outside;
+}
+
+// Largest of the warps' error bounds (NaN if one is).
+__device__ __forceinline__ float max_of_warps(const float* e) {
+  float m = e[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) m = max_nan(m, e[w]);
+  return m;
+}
+
+// Scores for the two-kernel selection: a CTA takes a run of blocks for kTokens
+// consecutive tokens, those of one request at a time, so that the bounds are read once for all.
+constexpr int kTokens = 8;
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
+  __shared__ __align__(16) float coef[kTokens][2 * D];  // M, P
+  __shared__ float errs[kTokens][kWarps];
+  const int warp = threadIdx.x >> 5;
+  const int kh = blockIdx.x / p.chunks % p.Hkv, t0 = blockIdx.x / p.chunks / p.Hkv * kTokens, c = blockIdx.x % p.chunks;
+  launch_dependents();
+  grid_dependency_wait();
+  const bool report = c == 0 && kh == 0 && threadIdx.x == 0;
+  const int t1 = min(t0 + kTokens, p.N);
+  for (int t = t0, next; t < t1; t = next) {
+    int b, n, j;
+    next = t + 1;
+    if (!find_token(p.cu_seqlens, p.B, t, &b, &n, &j)) {
+      if (report) set_status(p.status, ATTN_STATUS_SEQLENS);
+      continue;
+    }
+    const int run = min(n - j, t1 - t);
+    next = t + run;
+    const ReqInfo r = load_request(p.kv, b, n);
+    int most = 0;  // blocks of the last token that has a list; those of the others end no later
+    for (int k = 0; k < run; ++k) most = max(most, visible_blocks(p, r, j + k, report));
+    const int i0 = p.first + c * p.chunk, i1 = min(i0 + p.chunk, most - p.last);
+    if (most <= p.keep || i0 >= i1) continue;
+    for (int i = threadIdx.x; i < run * D; i += kThreads)
+      coefficients(p, t + i / D, kh, D, i % D, &coef[i / D][i % D], &coef[i / D][D + i % D]);
+    __syncthreads();
+    const int64_t list = (int64_t)t * p.Hkv + kh;
+    const bool outside = score_blocks<D>(
+        p, r, b, kh, i0, i1, run, coef,
+        [&](int k, int i, float v) {
+          p.scores[(list + (int64_t)k * p.Hkv) * p.max_blocks + i] = v;  // some past what the token sees
+        },
+        [&](int k, float e) { errs[k][warp] = e; });
+    if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
+    __syncthreads();
+    if ((int)threadIdx.x < run)
+      p.errors[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = max_of_warps(errs[threadIdx.x]);
+    __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------- selection
@@ -250,22 +345,39 @@ __device__ __forceinline__ unsigned long long order_key64(double x) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-constexpr int kHeld = 8;       // scores held in registers per thread: up to 2048 candidates
-constexpr int kMaxOpen = 256;  // candidates summed again and ranked in shared memory
+constexpr int kHeld = 8;                     // keys held in registers per thread
+constexpr int kHeldAll = kHeld * kThreads;   // candidates that are all held
+constexpr int kMaxOpen = 256;                // candidates summed again and ranked in shared memory
 
-// The sum over the CTA of one count per thread: alternating buffers, one barrier.
+template <int D>
+struct SelectSmem {
+  int part[2][3][kWarps];
+  double coef[2 * D];
+  int open_idx[kMaxOpen];
+  unsigned long long open_key[kMaxOpen];
+  int open_n;
+  uint32_t kmin[kWarps], kmax[kWarps];
+};
+
+// Sums over the CTA of up to three counts per thread: one barrier a call, alternating buffers.
 struct Counter {
-  int (*part)[kWarps];  // [2][kWarps]
+  int (*part)[3][kWarps];  // [2]
   int turn = 0;
-  __device__ __forceinline__ int operator()(int mine) {
-    const int s = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = s;
-    __syncthreads();
-    int sum = 0;
+  template <int N>
+  __device__ __forceinline__ void operator()(int (&c)[N]) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += part[turn][w];
+    for (int k = 0; k < N; ++k) {
+      c[k] = __reduce_add_sync(0xffffffffu, c[k]);
+      if ((threadIdx.x & 31) == 0) part[turn][k][threadIdx.x >> 5] = c[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      c[k] = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) c[k] += part[turn][k][w];
+    }
     turn ^= 1;
-    return sum;
   }
 };
 
@@ -286,78 +398,54 @@ __device__ __forceinline__ double exact_score(const BlocksPar& p, const ReqInfo&
   return s;
 }
 
-// One CTA per list.
-template <int D>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar p) {
-  extern __shared__ uint32_t bits[];  // candidate i is selected: bit i % 32 of word i / 32
-  __shared__ int part[2][kWarps];
-  __shared__ double coef[2 * D];
-  __shared__ int open_idx[kMaxOpen];
-  __shared__ unsigned long long open_key[kMaxOpen];
-  __shared__ int open_n, odd;
-  __shared__ float red[3][kWarps];
-  const int t = blockIdx.x / p.Hkv, kh = blockIdx.x % p.Hkv;
+// One CTA chooses the K largest of the m = n - first - last candidates of token t and KV head
+// kh and writes the list.  at(i): candidate i's score (read once for the first kHeldAll, again
+// and again for others); err: the bound on the scores' errors; bits: ceil(m / 32) words; keys: m
+// words of 64 bits.
+template <int D, typename At>
+__device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t, int kh, int n, At&& at, float err,
+                              uint32_t* bits, unsigned long long* keys, SelectSmem<D>& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  launch_dependents();
-  grid_dependency_wait();
-  ReqInfo r;
-  int b;
-  const int n = query_blocks(p, t, &r, &b, false);
-  if (n == 0) return;
   int32_t* list = p.list + ((int64_t)t * p.Hkv + kh) * p.keep;
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kThreads) list[i] = i < n ? i : -1;
-    return;
-  }
   const int m = n - p.first - p.last, K = p.keep - p.first - p.last;
   for (int i = tid; i < p.first; i += kThreads) list[i] = i;
   for (int i = tid; i < p.last; i += kThreads) list[p.keep - p.last + i] = n - p.last + i;
   if (K == 0) return;
-  float2* scores = p.scores + ((int64_t)t * p.Hkv + kh) * p.max_blocks + p.first;
 
-  // the largest error bound, the range of the keys, and whether anything is not finite
+  // the range of the keys, and whether anything is not finite
   uint32_t key[kHeld];
-  const bool held = m <= kHeld * kThreads;
-  float err = 0.f;
   uint32_t kmin = ~0u, kmax = 0u;
-  bool bad = false;
-  auto look = [&](float2 v) {
-    bad |= !(fabsf(v.x) <= 3.4028235e38f && v.y <= 3.4028235e38f);
-    err = fmaxf(err, v.y);
-    const uint32_t k = order_key(v.x);
+  bool bad = !(err <= 3.4028235e38f);
+  auto look = [&](float v) {
+    bad |= !(fabsf(v) <= 3.4028235e38f);
+    const uint32_t k = order_key(v);
     kmin = min(kmin, k);
     kmax = max(kmax, k);
     return k;
   };
 #pragma unroll
+  for (int e = 0; e < kHeld; ++e)
+    if (e * kThreads < m) key[e] = __float_as_uint(at(min(e * kThreads + tid, m - 1)));  // all loads first
+#pragma unroll
   for (int e = 0; e < kHeld; ++e) {
-    const int i = e * kThreads + tid;
-    key[e] = 0u;  // below every finite score's key
-    if (i < m) key[e] = look(__ldcg(scores + i));
+    if (e * kThreads + tid < m) key[e] = look(__uint_as_float(key[e]));
+    else key[e] = 0u;  // below every finite score's key
   }
-  if (!held)
-    for (int i = kHeld * kThreads + tid; i < m; i += kThreads) look(__ldcg(scores + i));
-  err = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(err)));
+  for (int i = kHeldAll + tid; i < m; i += kThreads) look(at(i));
+  if (tid == 0) sm.open_n = 0;
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   if (lane == 0) {
-    red[0][warp] = err;
-    red[1][warp] = __uint_as_float(kmin);
-    red[2][warp] = __uint_as_float(kmax);
+    sm.kmin[warp] = kmin;
+    sm.kmax[warp] = kmax;
   }
-  if (tid == 0) open_n = 0;
-  odd = 0;
-  __syncthreads();
-  if (bad) odd = 1;
+  const bool all_exact = __syncthreads_or(bad);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    err = fmaxf(err, red[0][w]);
-    kmin = min(kmin, __float_as_uint(red[1][w]));
-    kmax = max(kmax, __float_as_uint(red[2][w]));
+    kmin = min(kmin, sm.kmin[w]);
+    kmax = max(kmax, sm.kmax[w]);
   }
-  __syncthreads();
-  const bool all_exact = odd;
-  Counter count{part};
+  Counter count{sm.part};
 
   // f(i, key of candidate i) for this thread's candidates, i = tid, tid + 256, ...; the
   // lanes of a warp are at 32 consecutive candidates, and all of them call f
@@ -365,41 +453,47 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
 #pragma unroll
     for (int e = 0; e < kHeld; ++e)
       if (e * kThreads + warp * 32 < m) f(e * kThreads + tid, key[e]);
-    for (int i = kHeld * kThreads + tid; i - lane < m; i += kThreads)
-      f(i, i < m ? order_key(__ldcg(&scores[i].x)) : 0u);
+    for (int i = kHeldAll + tid; i - lane < m; i += kThreads) f(i, i < m ? order_key(at(i)) : 0u);
   };
 
   int sure = 0, open = m;
   float low = 0.f, high = 0.f;  // scores above high are in, those below low are out
   if (!all_exact) {
-    // the largest threshold with at least K keys at or above it, from the first bit in
-    // which keys differ; it is enough that exactly K are
-    const int top = 31 - __clz((int)(kmin ^ kmax));  // -1: all the same
-    uint32_t thr = top >= 31 ? 0u : kmax & ~((2u << max(top, 0)) - 1u);
-    if (top < 0) thr = kmax;
-    for (int bit = top; bit >= 0; --bit) {
-      const uint32_t cand = thr | (1u << bit);
-      int mine = 0;
+    // The largest threshold with at least K keys at or above it, from the first bit in
+    // which keys differ, two bits a step; it is enough that exactly K are.
+    int bit = 31 - __clz((int)(kmin ^ kmax));  // -1: all the same
+    uint32_t thr = bit < 0 ? kmax : bit == 31 ? 0u : kmax >> (bit + 1) << (bit + 1);
+    for (; bit >= 0; bit -= 2) {
+      const uint32_t hi = 1u << bit, lo = bit > 0 ? hi >> 1 : 0u;
+      int c[3] = {0, 0, 0};  // keys at or above thr + lo, thr + hi, thr + hi + lo
+      auto add = [&](uint32_t k) {
+        c[0] += k >= (thr | lo);
+        c[1] += k >= (thr | hi);
+        c[2] += k >= (thr | hi | lo);
+      };
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e) mine += key[e] >= cand;
-      if (!held)
-        for (int i = kHeld * kThreads + tid; i < m; i += kThreads) mine += order_key(__ldcg(&scores[i].x)) >= cand;
-      const int c = count(mine);
-      if (c >= K) thr = cand;
-      if (c == K) break;
+      for (int e = 0; e < kHeld; ++e) add(key[e]);
+      for (int i = kHeldAll + tid; i < m; i += kThreads) add(order_key(at(i)));
+      count(c);
+      const int take = c[2] >= K ? 3 : c[1] >= K ? 2 : c[0] >= K ? 1 : 0;
+      const int cnt = take == 0 ? m : c[take - 1];
+      if (take & 2) thr |= hi;
+      if (take & 1) thr |= lo;
+      if (cnt == K) break;
     }
     const float tau = key_value(thr), width = 2.02f * err;
     low = tau - width;
     high = tau + width;
-    int s = 0, o = 0;
+    int c[2] = {0, 0};
     each([&](int i, uint32_t k) {
       if (i >= m) return;
       const float x = key_value(k);
-      s += x > high;
-      o += x >= low && !(x > high);
+      c[0] += x > high;
+      c[1] += x >= low && !(x > high);
     });
-    sure = count(s);
-    open = count(o);
+    count(c);
+    sure = c[0];
+    open = c[1];
   }
   const int need = K - sure;  // of the open ones
   const int words = (m + 31) >> 5;
@@ -410,62 +504,54 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
     });
     __syncthreads();
   } else {
-    for (int d = tid; d < D; d += kThreads) {
-      double lo = 0.0, hi = 0.0;
-      for (int h = 0; h < p.G; ++h) {
-        const float x = q_value(__ldg(p.q + ((int64_t)t * p.Hkv * p.G + kh * p.G + h) * D + d), p.q_f16);
-        lo += x > 0.f ? 0.0 : (double)x;
-        hi += x < 0.f ? 0.0 : (double)x;
-      }
-      coef[d] = lo;
-      coef[D + d] = hi;
-    }
-    __syncthreads();
+    for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
     if (!all_exact && open <= kMaxOpen) {
       each([&](int i, uint32_t k) {
         const float x = key_value(k);
         const uint32_t v = __ballot_sync(0xffffffffu, i < m && x > high);
         if (lane == 0) bits[i >> 5] = v;
-        if (i < m && x >= low && !(x > high)) open_idx[atomicAdd(&open_n, 1)] = i;  // the order does not matter
+        if (i < m && x >= low && !(x > high)) sm.open_idx[atomicAdd(&sm.open_n, 1)] = i;  // in any order
       });
       __syncthreads();
       for (int o = warp; o < open; o += kWarps) {
-        const double s = exact_score<D>(p, r, b, kh, p.first + open_idx[o], coef, lane);
-        if (lane == 0) open_key[o] = order_key64(s);
+        const double s = exact_score<D>(p, r, b, kh, p.first + sm.open_idx[o], sm.coef, lane);
+        if (lane == 0) sm.open_key[o] = order_key64(s);
       }
       __syncthreads();
       if (tid < open) {
-        const unsigned long long mine = open_key[tid];
-        const int idx = open_idx[tid];
+        const unsigned long long mine = sm.open_key[tid];
+        const int idx = sm.open_idx[tid];
         int better = 0;
-        for (int o = 0; o < open; ++o) better += open_key[o] > mine || (open_key[o] == mine && open_idx[o] < idx);
+        for (int o = 0; o < open; ++o)
+          better += sm.open_key[o] > mine || (sm.open_key[o] == mine && sm.open_idx[o] < idx);
         if (better < need) atomicOr(&bits[idx >> 5], 1u << (idx & 31));
       }
       __syncthreads();
     } else {
-      // many equal scores, or some that are not finite: every candidate's key in 64 bits, in
-      // place of its score, and a search by bits
-      unsigned long long* keys = reinterpret_cast<unsigned long long*>(scores);
+      // many equal scores, or some that are not finite: every candidate's key in 64 bits and a
+      // search by bits
       __syncthreads();
       for (int i = warp; i < m; i += kWarps) {
-        const double s = exact_score<D>(p, r, b, kh, p.first + i, coef, lane);
-        if (lane == 0) __stcg(keys + i, order_key64(s));
+        const double s = exact_score<D>(p, r, b, kh, p.first + i, sm.coef, lane);
+        if (lane == 0) keys[i] = order_key64(s);
       }
       __syncthreads();
       unsigned long long thr = 0ull;
       for (int bit = 63; bit >= 0; --bit) {
         const unsigned long long cand = thr | (1ull << bit);
-        int mine = 0;
-        for (int i = tid; i < m; i += kThreads) mine += __ldcg(keys + i) >= cand;
-        if (count(mine) >= K) thr = cand;
+        int c[1] = {0};
+        for (int i = tid; i < m; i += kThreads) c[0] += keys[i] >= cand;
+        count(c);
+        if (c[0] >= K) thr = cand;
       }
-      int above = 0;
-      for (int i = tid; i < m; i += kThreads) above += __ldcg(keys + i) > thr;
-      int ties = K - count(above);  // of those at the threshold the lowest
+      int above[1] = {0};
+      for (int i = tid; i < m; i += kThreads) above[0] += keys[i] > thr;
+      count(above);
+      int ties = K - above[0];  // of those at the threshold the lowest
       if (warp == 0) {
         for (int w = 0; w < words; ++w) {
           const int i = 32 * w + lane;
-          const unsigned long long k = i < m ? __ldcg(keys + i) : 0ull;
+          const unsigned long long k = i < m ? keys[i] : 0ull;
           const uint32_t more = __ballot_sync(0xffffffffu, i < m && k > thr);
           const uint32_t same = __ballot_sync(0xffffffffu, i < m && k == thr);
           const bool take = (same >> lane & 1u) && __popc(same & ((1u << lane) - 1u)) < ties;
@@ -489,14 +575,96 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
     const int v = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += v;
   }
-  int* sums = &part[0][0];
-  __syncthreads();
+  int* sums = reinterpret_cast<int*>(sm.kmin);  // last read before several barriers
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  int at = p.first + incl - mine;
-  for (int w = 0; w < warp; ++w) at += sums[w];
+  int to = p.first + incl - mine;
+  for (int w = 0; w < warp; ++w) to += sums[w];
   for (int w = w0; w < w1; ++w)
-    for (uint32_t v = bits[w]; v; v &= v - 1) list[at++] = p.first + 32 * w + __ffs((int)v) - 1;
+    for (uint32_t v = bits[w]; v; v &= v - 1) list[to++] = p.first + 32 * w + __ffs((int)v) - 1;
+}
+
+__device__ __forceinline__ void whole_list(const BlocksPar& p, int t, int kh, int n) {
+  int32_t* list = p.list + ((int64_t)t * p.Hkv + kh) * p.keep;
+  for (int i = threadIdx.x; i < p.keep; i += kThreads) list[i] = i < n ? i : -1;
+}
+
+// The second of the two kernels: one CTA per list, scores in the workspace.
+template <int D>
+__global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar p) {
+  extern __shared__ uint32_t bits[];
+  __shared__ SelectSmem<D> sm;
+  const int t = blockIdx.x / p.Hkv, kh = blockIdx.x % p.Hkv;
+  launch_dependents();
+  grid_dependency_wait();
+  ReqInfo r;
+  int b;
+  const int n = query_blocks(p, t, &r, &b, false);
+  if (n == 0) return;
+  if (n <= p.keep) {
+    whole_list(p, t, kh, n);
+    return;
+  }
+  const int64_t list = (int64_t)t * p.Hkv + kh;
+  const float* scores = p.scores + list * p.max_blocks + p.first;
+  float err = 0.f;
+  for (int c = 0; p.first + c * p.chunk < n - p.last; ++c) err = max_nan(err, __ldcg(p.errors + list * p.chunks + c));
+  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, err, bits,
+                   p.keys + list * p.max_blocks, sm);
+}
+
+// Both in one kernel for lists of up to kHeldAll candidates: a cluster of p.chunks CTAs scores
+// runs of p.chunk candidates into shared memory, its first CTA selects.
+template <int D>
+__global__ void __launch_bounds__(kThreads) block_pick_kernel(const BlocksPar p) {
+  __shared__ SelectSmem<D> sm;
+  __shared__ __align__(16) float coef[1][2 * D];
+  __shared__ uint32_t bits[kHeldAll / 32];
+  __shared__ unsigned long long keys[kHeldAll];  // the scores of this CTA's candidates first
+  __shared__ float errs[kWarps], err;
+  float* mine = reinterpret_cast<float*>(keys);
+  const int rank = blockIdx.x % p.chunks, list = blockIdx.x / p.chunks, t = list / p.Hkv, kh = list % p.Hkv;
+  const int warp = threadIdx.x >> 5;
+  launch_dependents();
+  grid_dependency_wait();
+  ReqInfo r;
+  int b;
+  const int n = query_blocks(p, t, &r, &b, rank == 0 && kh == 0 && threadIdx.x == 0);
+  if (n == 0) return;
+  if (n <= p.keep) {
+    if (rank == 0) whole_list(p, t, kh, n);
+    return;
+  }
+  const int i0 = p.first + rank * p.chunk, i1 = min(i0 + p.chunk, n - p.last);
+  if (i0 < i1) {
+    for (int d = threadIdx.x; d < D; d += kThreads) coefficients(p, t, kh, D, d, &coef[0][d], &coef[0][D + d]);
+    __syncthreads();
+    if (score_blocks<D>(
+            p, r, b, kh, i0, i1, 1, coef, [&](int, int i, float v) { mine[i - i0] = v; },
+            [&](int, float e) { errs[warp] = e; }))
+      set_status(p.status, ATTN_STATUS_CAPACITY);
+  } else if (threadIdx.x < kWarps) {
+    errs[threadIdx.x] = 0.f;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) err = max_of_warps(errs);
+  if (p.chunks > 1) cluster_sync();
+  else __syncthreads();
+  if (rank == 0) {
+    const uint32_t base = smem_u32(mine);
+    const int lane = threadIdx.x & 31;
+    float e = lane < p.chunks ? peer_f32(smem_u32(&err), lane) : 0.f;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, off));
+    e = __shfl_sync(0xffffffffu, e, 0);
+    // a candidate's score is read once, into a register, and keys are written behind a
+    // barrier after those reads
+    const int sh = 31 - __clz(p.chunk);
+    select_blocks<D>(p, r, b, t, kh, n, [&](int i) {
+      return peer_f32(base + (uint32_t)(i & (p.chunk - 1)) * 4u, i >> sh);
+    }, e, bits, keys, sm);
+  }
+  if (p.chunks > 1) cluster_sync();  // no CTA leaves while the first one reads from it
 }
 
 // ---------------------------------------------------------------- host
@@ -541,8 +709,12 @@ BlocksPar blocks_par(const attn_config_t* cfg, const attn_kv_t& kv, const attn_b
 
 int blocks_of(int32_t max_kv_len, int32_t block_size) { return (int)(((int64_t)max_kv_len + block_size - 1) / block_size); }
 
+constexpr int kChunk = 128;  // blocks per CTA of the two-kernel selection
+
+// Behind the header: scores, exact scores, bounds on errors.
 size_t scores_bytes(const attn_config_t* cfg, int64_t N, int32_t max_blocks) {
-  return (size_t)N * cfg->num_kv_heads * max_blocks * sizeof(float2);
+  const size_t lists = (size_t)N * cfg->num_kv_heads;
+  return align_up(lists * max_blocks * (sizeof(float) + 8) + lists * ((max_blocks + kChunk - 1) / kChunk) * sizeof(float), 256);
 }
 
 template <int D, int KV>
@@ -561,11 +733,28 @@ int launch_bounds_d(const BlocksPar& p, int kv_dtype, cudaStream_t s) {
   }
 }
 
+// Tokens of one request next to each other share the reading of the bounds in the two kernels; a
+// token per request takes the one that spares a launch and the scores' way through memory.
 template <int D>
-int launch_select_t(const BlocksPar& p, cudaStream_t s) {
+int launch_select_t(BlocksPar& p, cudaStream_t s) {
   const int64_t lists = (int64_t)p.N * p.Hkv;
-  if (lists * p.chunks > 0x7fffffff) return ATTN_EINVAL;
-  if (launch_dependent(block_score_kernel<D>, dim3((unsigned)(lists * p.chunks)), dim3(kThreads), 0, s, p) != cudaSuccess)
+  if (p.N < 2 * (int64_t)p.B && p.max_blocks <= kHeldAll) {
+    int c = 1;
+    while (c < 16 && lists * c < 304 && p.max_blocks > 64 * c) c *= 2;
+    p.chunks = c;
+    p.chunk = 64;
+    while (p.chunk * c < p.max_blocks) p.chunk *= 2;
+    if (lists * c > 0x7fffffff) return ATTN_EINVAL;
+    return launch_cluster_dependent(block_pick_kernel<D>, dim3((unsigned)(lists * c)), dim3(kThreads), 0, c, s, p) ==
+                   cudaSuccess
+               ? ATTN_OK
+               : ATTN_ELAUNCH;
+  }
+  p.chunk = kChunk;
+  p.chunks = (p.max_blocks + p.chunk - 1) / p.chunk;
+  const int64_t ctas = ((int64_t)p.N + kTokens - 1) / kTokens * p.Hkv * p.chunks;
+  if (ctas > 0x7fffffff || lists > 0x7fffffff) return ATTN_EINVAL;
+  if (launch_dependent(block_score_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p) != cudaSuccess)
     return ATTN_ELAUNCH;
   const size_t smem = (size_t)((p.max_blocks + 31) / 32) * 4;  // at most 32 KB
   return launch_dependent(block_select_kernel<D>, dim3((unsigned)lists), dim3(kThreads), smem, s, p) == cudaSuccess
@@ -585,7 +774,7 @@ size_t attn_block_workspace_size(const attn_config_t* cfg, int32_t max_tokens, i
   if (abi_check_config(cfg) != ATTN_OK || max_tokens < 0 || max_kv_len < 1 || max_kv_len > (1 << 24)) return 0;
   if (!block_size_ok(block_size) || keep < 1 || keep > kMaxListed) return 0;
   const size_t scores = scores_bytes(cfg, max_tokens, blocks_of(max_kv_len, block_size));
-  return kWsHeader + align_up(scores, 256);
+  return kWsHeader + scores;
 }
 
 int attn_block_bounds(const attn_config_t* cfg, const attn_kv_t* kv, const attn_blocks_t* blocks,
@@ -634,10 +823,11 @@ int attn_block_select(const attn_config_t* cfg, const void* q, const int32_t* cu
   p.last = last;
   p.keep = keep;
   p.max_blocks = max_blocks;
-  p.scores = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kWsHeader);
+  const size_t slots = (size_t)N * p.Hkv * max_blocks;
+  p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + kWsHeader);
+  p.scores = reinterpret_cast<float*>(p.keys + slots);
+  p.errors = p.scores + slots;
   p.list = list;
-  p.chunk = 64;
-  p.chunks = (max_blocks + p.chunk - 1) / p.chunk;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cfg->head_dim == 128 ? launch_select_t<128>(p, s) : launch_select_t<64>(p, s);
 }

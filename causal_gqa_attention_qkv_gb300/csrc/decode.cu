@@ -606,7 +606,7 @@ int decode_split_len(int B, int Hkv, int max_kv_len, int* max_splits, bool longe
 // (1, 2, 4, 8, 16).
 void block_splits(int64_t pairs, int keep, int block_size, int* splits, int* per) {
   const int64_t tiles = (int64_t)keep * (block_size / 64);
-  int64_t n = std::min<int64_t>(std::min<int64_t>(304 / pairs, 16), tiles / 4);
+  int64_t n = std::min<int64_t>(std::min<int64_t>(304 / pairs, kMaxSplits), tiles / 4);
   n = std::max<int64_t>(std::max<int64_t>(n, 1), (keep + kMaxSplitBlocks - 1) / kMaxSplitBlocks);
   *per = (int)((keep + n - 1) / n);
   *splits = (keep + *per - 1) / *per;

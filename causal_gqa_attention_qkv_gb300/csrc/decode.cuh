@@ -2,6 +2,7 @@
 // and the split of a request's keys.
 #pragma once
 
+#include "cluster.cuh"
 #include "kernels.cuh"
 #include "kv_read.cuh"
 
@@ -209,22 +210,7 @@ __device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int 
 // ---------------------------------------------------------------- merge of listed blocks
 // The splits of a list are one cluster and merge through distributed shared memory: no
 // partial results in memory and no second launch.
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The float at `addr` (a shared memory address of this CTA) in CTA `rank` of the cluster.
-__device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
+constexpr int kMaxSplits = 16;        // of a list: the largest cluster
 constexpr int kMergeBytes = 2 * 8 * 4;  // behind the warps' partial results: this CTA's maxima and sums
 
 // The output rows of token t's group from the warps' partial results mo [warps][G][D], mm
@@ -265,19 +251,28 @@ __device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const
   }
   if (splits == 1) return;
   cluster_sync();
-  for (int idx = cluster_rank() * kConsumerWarps * 32 + threadIdx.x; idx < G * D; idx += splits * kConsumerWarps * 32) {
-    const uint32_t am = smem_u32(cm + idx / D), al = smem_u32(cl + idx / D), ao = smem_u32(mo + idx);
-    float M = kNegInf;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, peer_f32(am, s));
-    float L = 0.f, acc = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float w = M == kNegInf ? 0.f : fast_exp2(peer_f32(am, s) - M);
-      L += w * peer_f32(al, s);
-      acc += w * peer_f32(ao, s);
-    }
-    store(idx, acc, L);
+  // a warp's 32 components are of one head: lane s looks at split s for the weights
+  const int lane = threadIdx.x & 31;
+  for (int i0 = (cluster_rank() * kConsumerWarps + (threadIdx.x >> 5)) * 32; i0 < G * D;
+       i0 += splits * kConsumerWarps * 32) {
+    const int idx = i0 + lane, row = i0 / D;
+    float v[kMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) v[s] = s < splits ? peer_f32(smem_u32(mo + idx), s) : 0.f;
+    const bool there = lane < splits;
+    const float ms = there ? peer_f32(smem_u32(cm + row), lane) : kNegInf;
+    float L = there ? peer_f32(smem_u32(cl + row), lane) : 0.f, M = ms;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float w = M == kNegInf ? 0.f : fast_exp2(ms - M);
+    L *= w;
+    float acc = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+      if (s < splits) acc += __shfl_sync(0xffffffffu, w, s) * v[s];
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    store(idx, acc, __shfl_sync(0xffffffffu, L, 0));
   }
   cluster_sync();  // no CTA leaves while another reads from it
 }
@@ -329,23 +324,12 @@ inline DecodePar decode_par(const DecodeArgs& a) {
 // Launch of a split kernel over listed blocks: the splits of a (token, KV head) form a cluster.
 template <typename Kernel>
 int launch_block_splits(Kernel kernel, size_t smem, const DecodeArgs& a, const CacheMaps& maps, cudaStream_t stream) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ELAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.max_splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, maps.k, maps.v, decode_par(a)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
+  return launch_cluster_dependent(kernel, dim3((unsigned)(a.N * a.max_splits), a.cfg.num_kv_heads), dim3(kThreads), smem,
+                                  a.max_splits, stream, maps.k, maps.v, decode_par(a)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ELAUNCH;
 }
 
 }  // namespace
