@@ -36,6 +36,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+struct Range;
+
 struct BlocksPar {
   uint16_t* bounds;          // [num_rows, Hkv, 2, D]
   int64_t num_rows;
@@ -55,7 +57,7 @@ struct BlocksPar {
   const uint16_t* q;         // [N, Hq, D]
   int32_t q_f16, N, G, first, last, keep, max_blocks, chunk, chunks;
   float* scores;             // [N, Hkv, max_blocks]
-  float* errors;             // [N, Hkv, chunks]: bounds on the errors of a chunk's scores
+  Range* ranges;      // [N, Hkv, chunks]
   unsigned long long* keys;  // [N, Hkv, max_blocks] exact scores, where they are needed
   int32_t* list;             // [N, Hkv, keep]
 };
@@ -67,6 +69,22 @@ __device__ __forceinline__ int64_t bounds_row(const BlocksPar& p, const ReqInfo&
   if (r.pages) {
     const int64_t slot = cache_slot(p.kv, r, i << p.log2_bs);
     row = slot < 0 ? -1 : slot >> p.log2_bs;
+  } else {
+    row = __ldg(p.row_base + b) + i;
+  }
+  return row < p.num_rows ? row : -1;
+}
+
+// The same from the arguments alone; any i >= 0.
+__device__ __forceinline__ int64_t bounds_row_at(const BlocksPar& p, int b, int i) {
+  int64_t row;
+  if (p.kv.page_table) {
+    const int64_t pos = (int64_t)i << p.log2_bs;
+    const int64_t pg = pos >> p.kv.log2_page;
+    if (pg >= p.kv.pages_per_req) return -1;
+    const int64_t page = __ldg(p.kv.page_table + (int64_t)b * p.kv.pages_per_req + pg);
+    const int64_t slot = (page << p.kv.log2_page) + (pos & ((1 << p.kv.log2_page) - 1));
+    row = page >= 0 && slot < p.kv.num_slots ? slot >> p.log2_bs : -1;
   } else {
     row = __ldg(p.row_base + b) + i;
   }
@@ -172,6 +190,12 @@ __device__ __forceinline__ void coefficients(const BlocksPar& p, int t, int kh, 
 __device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t v) {
   return (uint64_t)(v & 0xFFFF0000u) << 32 | (uint64_t)(v << 16);
 }
+__device__ __forceinline__ void unpack_pairs(const uint4& x, uint64_t (&y)[4]) {
+  y[0] = bf16x2_to_f32x2(x.x);
+  y[1] = bf16x2_to_f32x2(x.y);
+  y[2] = bf16x2_to_f32x2(x.z);
+  y[3] = bf16x2_to_f32x2(x.w);
+}
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -182,6 +206,24 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+
+// Larger float -> larger key.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// What a warp (a CTA) knows of its scores: a bound on their errors, the range of their keys.
+struct Range {
+  float err;
+  uint32_t kmin, kmax;
+};
+__device__ __forceinline__ Range join(const Range& a, const Range& b) {
+  return {max_nan(a.err, b.err), min(a.kmin, b.kmin), max(a.kmax, b.kmax)};
+}
+__device__ __forceinline__ Range no_scores() { return {0.f, ~0u, 0u}; }
 
 // Rounding of a score: each term goes through at most 7 additions in M or P, 5 in its
 // lane's two chains and 5 between lanes, 17 half steps of its magnitude.  The bound on the sum of
@@ -194,21 +236,24 @@ constexpr float kErrorFloor = 1e-40f;
 
 // Scores of the blocks [i0, i1) of a request for some tokens, by the CTA: a warp takes 8 blocks
 // (D = 64: 16) at a time, lane l of the D / 4 lanes of a block holds 8 components of lo (the
-// first half of the lanes) or hi.  coef: M, P of each token; put(k, block, score); err(k,
-// bound on the error of this warp's scores), by one lane.  Returns whether a row lay outside.
-template <int D, typename Put, typename Err>
-__device__ __forceinline__ bool score_blocks(const BlocksPar& p, const ReqInfo& r, int b, int kh, int i0, int i1,
-                                             int tokens, const float (*coef)[2 * D], Put&& put, Err&& err) {
+// first half of the lanes) or hi.  coef: M, P of each token; put(k, block, score); tell(k,
+// range of this warp's scores), by one lane.  Returns whether a row lay outside.
+// row_of(i): the row of block i.  Many: more than one token; the entries are then unpacked once for all.
+template <int D, bool Many, typename Row, typename Put, typename Tell>
+__device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0, int i1, int tokens,
+                                             const float (*coef)[2 * D], Row&& row_of, Put&& put, Tell&& tell) {
   constexpr int L = D / 4, BPW = 32 / L;  // lanes per block, blocks per warp and load
+  constexpr int S = Many ? 4 : 8;         // blocks summed at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % L, sub = lane / L;
   bool outside = false;
   uint4 big = make_uint4(0, 0, 0, 0);  // largest magnitudes
+  uint32_t kmin = ~0u, kmax = 0u;        // of all tokens
   const uint4* rows = reinterpret_cast<const uint4*>(p.bounds) + kh * (D / 4) + li;
   for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
     // rows of the warp's blocks, one per lane
     int64_t row = -1;
     if (lane < 8 * BPW && i + lane < i1) {
-      row = bounds_row(p, r, b, i + lane);
+      row = row_of(i + lane);
       outside |= row < 0;
     }
     uint4 x[8];
@@ -222,31 +267,30 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, const ReqInfo& 
       big = make_uint4(max2(big.x, x[k].x & 0x7FFF7FFFu), max2(big.y, x[k].y & 0x7FFF7FFFu),
                        max2(big.z, x[k].z & 0x7FFF7FFFu), max2(big.w, x[k].w & 0x7FFF7FFFu));
 #pragma unroll
-    for (int g = 0; g < 8; g += 4) {
-      uint64_t y[4][4];
+    for (int g = 0; g < 8; g += S) {
+      uint64_t y[Many ? S : 1][4];
+      if constexpr (Many) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        y[k][0] = bf16x2_to_f32x2(x[g + k].x);
-        y[k][1] = bf16x2_to_f32x2(x[g + k].y);
-        y[k][2] = bf16x2_to_f32x2(x[g + k].z);
-        y[k][3] = bf16x2_to_f32x2(x[g + k].w);
+        for (int k = 0; k < S; ++k) unpack_pairs(x[g + k], y[k]);
       }
 #pragma unroll 1
       for (int t = 0; t < tokens; ++t) {
         uint64_t w[4];  // pairs of coefficients
-        float s[4];
+        float s[S];
         *reinterpret_cast<ulonglong2*>(w) = *reinterpret_cast<const ulonglong2*>(&coef[t][8 * li]);
         *reinterpret_cast<ulonglong2*>(w + 2) = *reinterpret_cast<const ulonglong2*>(&coef[t][8 * li + 4]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint64_t acc = mul_f32x2(w[0], y[k][0]);
+        for (int k = 0; k < S; ++k) {
+          if constexpr (!Many) unpack_pairs(x[g + k], y[0]);
+          const uint64_t(&v)[4] = y[Many ? k : 0];
+          uint64_t acc = mul_f32x2(w[0], v[0]);
 #pragma unroll
-          for (int e = 1; e < 4; ++e) acc = fma_f32x2(w[e], y[k][e], acc);
+          for (int e = 1; e < 4; ++e) acc = fma_f32x2(w[e], v[e], acc);
           s[k] = __uint_as_float((uint32_t)acc) + __uint_as_float((uint32_t)(acc >> 32));
         }
-        // sums over the block's lanes; of the 4 values each lane keeps the one of its bits 0, 1
+        // sums over the block's lanes; of the S values each lane keeps the one of its lowest bits
 #pragma unroll
-        for (int half = 2; half >= 1; half >>= 1) {
+        for (int half = S / 2; half >= 1; half >>= 1) {
           const bool up = lane & half;
 #pragma unroll
           for (int k = 0; k < half; ++k) {
@@ -255,12 +299,20 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, const ReqInfo& 
           }
         }
 #pragma unroll
-        for (int off = 4; off < L; off <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
-        const int at = i + (g + (lane & 3)) * BPW + sub;
-        if (li < 4 && at < i1) put(t, at, s[0]);
+        for (int off = S; off < L; off <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
+        const int at = i + (g + (lane & (S - 1))) * BPW + sub;
+        if (li < S && at < i1) {
+          put(t, at, s[0]);
+          const uint32_t k = order_key(s[0]);
+          kmin = min(kmin, k);
+          kmax = max(kmax, k);
+        }
+        if constexpr (!Many) break;
       }
     }
   }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
   float y[8];
   unpack_bf16x8(big, y);
 #pragma unroll 1
@@ -271,17 +323,9 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, const ReqInfo& 
 #pragma unroll
     for (int off = 1; off < L; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
     if (BPW > 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, L & 31));
-    if (lane == 0) err(t, fmaf(a, kErrorOfMagnitude, kErrorFloor));
+    if (lane == 0) tell(t, Range{fmaf(a, kErrorOfMagnitude, kErrorFloor), kmin, kmax});
   }
   return outside;
-}
-
-// Largest of the warps' error bounds (NaN if one is).
-__device__ __forceinline__ float max_of_warps(const float* e) {
-  float m = e[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) m = max_nan(m, e[w]);
-  return m;
 }
 
 // Scores for the two-kernel selection: a CTA takes a run of blocks for kTokens
@@ -290,7 +334,7 @@ constexpr int kTokens = 8;
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
   __shared__ __align__(16) float coef[kTokens][2 * D];  // M, P
-  __shared__ float errs[kTokens][kWarps];
+  __shared__ Range told[kTokens][kWarps];
   const int warp = threadIdx.x >> 5;
   const int kh = blockIdx.x / p.chunks % p.Hkv, t0 = blockIdx.x / p.chunks / p.Hkv * kTokens, c = blockIdx.x % p.chunks;
   launch_dependents();
@@ -315,30 +359,25 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
       coefficients(p, t + i / D, kh, D, i % D, &coef[i / D][i % D], &coef[i / D][D + i % D]);
     __syncthreads();
     const int64_t list = (int64_t)t * p.Hkv + kh;
-    const bool outside = score_blocks<D>(
-        p, r, b, kh, i0, i1, run, coef,
+    const bool outside = score_blocks<D, true>(
+        p, kh, i0, i1, run, coef, [&](int i) { return bounds_row(p, r, b, i); },
         [&](int k, int i, float v) {
           p.scores[(list + (int64_t)k * p.Hkv) * p.max_blocks + i] = v;  // some past what the token sees
         },
-        [&](int k, float e) { errs[k][warp] = e; });
+        [&](int k, const Range& v) { told[k][warp] = v; });
     if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
     __syncthreads();
-    if ((int)threadIdx.x < run)
-      p.errors[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = max_of_warps(errs[threadIdx.x]);
+    if ((int)threadIdx.x < run) {
+      Range v = told[threadIdx.x][0];
+      for (int w = 1; w < kWarps; ++w) v = join(v, told[threadIdx.x][w]);
+      p.ranges[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = v;
+    }
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- selection
-// Larger float -> larger key.
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-// The same in 64 bits; -0 as 0, and NaN above all.
+// order_key() in 64 bits; -0 as 0, and NaN above all.
 __device__ __forceinline__ unsigned long long order_key64(double x) {
   if (!(x == x)) return ~0ull;
   const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
@@ -348,6 +387,7 @@ __device__ __forceinline__ unsigned long long order_key64(double x) {
 constexpr int kHeld = 8;                     // keys held in registers per thread
 constexpr int kHeldAll = kHeld * kThreads;   // candidates that are all held
 constexpr int kMaxOpen = 256;                // candidates summed again and ranked in shared memory
+constexpr int kBins = 1024;
 
 template <int D>
 struct SelectSmem {
@@ -355,8 +395,12 @@ struct SelectSmem {
   double coef[2 * D];
   int open_idx[kMaxOpen];
   unsigned long long open_key[kMaxOpen];
-  int open_n;
-  uint32_t kmin[kWarps], kmax[kWarps];
+  int bins[kBins];
+  uint32_t bin_key[kMaxOpen];
+  int open_n, bin_n;
+  int bin, above, inside;  // the bin with the K-th key: keys above it, keys in it
+  uint32_t thr;
+  int sums[kWarps];
 };
 
 // Sums over the CTA of up to three counts per thread: one barrier a call, alternating buffers.
@@ -400,10 +444,10 @@ __device__ __forceinline__ double exact_score(const BlocksPar& p, const ReqInfo&
 
 // One CTA chooses the K largest of the m = n - first - last candidates of token t and KV head
 // kh and writes the list.  at(i): candidate i's score (read once for the first kHeldAll, again
-// and again for others); err: the bound on the scores' errors; bits: ceil(m / 32) words; keys: m
-// words of 64 bits.
+// and again for others), range: of them all; bits: ceil(m / 32) words; keys: m words of 64
+// bits.  sm.bins, sm.open_n and sm.bin_n are zero.
 template <int D, typename At>
-__device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t, int kh, int n, At&& at, float err,
+__device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t, int kh, int n, At&& at, const Range& range,
                               uint32_t* bits, unsigned long long* keys, SelectSmem<D>& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* list = p.list + ((int64_t)t * p.Hkv + kh) * p.keep;
@@ -412,39 +456,16 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
   for (int i = tid; i < p.last; i += kThreads) list[p.keep - p.last + i] = n - p.last + i;
   if (K == 0) return;
 
-  // the range of the keys, and whether anything is not finite
   uint32_t key[kHeld];
-  uint32_t kmin = ~0u, kmax = 0u;
-  bool bad = !(err <= 3.4028235e38f);
-  auto look = [&](float v) {
-    bad |= !(fabsf(v) <= 3.4028235e38f);
-    const uint32_t k = order_key(v);
-    kmin = min(kmin, k);
-    kmax = max(kmax, k);
-    return k;
-  };
 #pragma unroll
   for (int e = 0; e < kHeld; ++e)
     if (e * kThreads < m) key[e] = __float_as_uint(at(min(e * kThreads + tid, m - 1)));  // all loads first
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e) {
-    if (e * kThreads + tid < m) key[e] = look(__uint_as_float(key[e]));
-    else key[e] = 0u;  // below every finite score's key
-  }
-  for (int i = kHeldAll + tid; i < m; i += kThreads) look(at(i));
-  if (tid == 0) sm.open_n = 0;
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
-  if (lane == 0) {
-    sm.kmin[warp] = kmin;
-    sm.kmax[warp] = kmax;
-  }
-  const bool all_exact = __syncthreads_or(bad);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    kmin = min(kmin, sm.kmin[w]);
-    kmax = max(kmax, sm.kmax[w]);
-  }
+  for (int e = 0; e < kHeld; ++e) key[e] = e * kThreads + tid < m ? order_key(__uint_as_float(key[e])) : 0u;
+  const uint32_t kmin = range.kmin, kmax = range.kmax;
+  // Magnitudes whose sum is finite give finite scores, or ones that just overflow.
+  const bool all_exact = !(range.err <= 3.4028235e38f && fabsf(key_value(kmin)) <= 3.4028235e38f &&
+                           fabsf(key_value(kmax)) <= 3.4028235e38f);
   Counter count{sm.part};
 
   // f(i, key of candidate i) for this thread's candidates, i = tid, tid + 256, ...; the
@@ -459,51 +480,101 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
   int sure = 0, open = m;
   float low = 0.f, high = 0.f;  // scores above high are in, those below low are out
   if (!all_exact) {
-    // The largest threshold with at least K keys at or above it, from the first bit in
-    // which keys differ, two bits a step; it is enough that exactly K are.
-    int bit = 31 - __clz((int)(kmin ^ kmax));  // -1: all the same
-    uint32_t thr = bit < 0 ? kmax : bit == 31 ? 0u : kmax >> (bit + 1) << (bit + 1);
-    for (; bit >= 0; bit -= 2) {
-      const uint32_t hi = 1u << bit, lo = bit > 0 ? hi >> 1 : 0u;
-      int c[3] = {0, 0, 0};  // keys at or above thr + lo, thr + hi, thr + hi + lo
-      auto add = [&](uint32_t k) {
-        c[0] += k >= (thr | lo);
-        c[1] += k >= (thr | hi);
-        c[2] += k >= (thr | hi | lo);
-      };
+    // A threshold with exactly K keys at or above it, or else the K-th key: the keys in bins of
+    // equal width, then those of the K-th's bin (one or two of 1000) by their ranks.
+    const int shift = max(0, 22 - __clz((int)(kmax - kmin)));  // the range in fewer than kBins steps
+    each([&](int i, uint32_t k) {
+      if (i < m) atomicAdd(&sm.bins[(k - kmin) >> shift], 1);
+    });
+    __syncthreads();
+    constexpr int R = kBins / kThreads;  // bins per thread, the highest first
+    int c[R], mine = 0;
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e) add(key[e]);
-      for (int i = kHeldAll + tid; i < m; i += kThreads) add(order_key(at(i)));
-      count(c);
-      const int take = c[2] >= K ? 3 : c[1] >= K ? 2 : c[0] >= K ? 1 : 0;
-      const int cnt = take == 0 ? m : c[take - 1];
-      if (take & 2) thr |= hi;
-      if (take & 1) thr |= lo;
-      if (cnt == K) break;
+    for (int e = 0; e < R; ++e) mine += c[e] = sm.bins[kBins - 1 - (tid * R + e)];
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
     }
-    const float tau = key_value(thr), width = 2.02f * err;
+    if (lane == 31) sm.sums[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) incl += sm.sums[w];
+    int before = incl - mine;
+    if (before < K && incl >= K) {
+#pragma unroll
+      for (int e = 0; e < R; ++e) {
+        if (before < K && before + c[e] >= K) {
+          sm.bin = kBins - 1 - (tid * R + e);
+          sm.above = before;
+          sm.inside = c[e];
+        }
+        before += c[e];
+      }
+    }
+    __syncthreads();
+    const int inside = sm.inside, want = K - sm.above;
+    uint32_t thr = kmin + ((uint32_t)sm.bin << shift);
+    if (inside > want && inside <= kMaxOpen) {
+      const uint32_t bin = sm.bin;
+      each([&](int i, uint32_t k) {
+        if (i < m && (k - kmin) >> shift == bin) sm.bin_key[atomicAdd(&sm.bin_n, 1)] = k;  // in any order
+      });
+      __syncthreads();
+      if (tid < inside) {
+        const uint32_t k = sm.bin_key[tid];
+        int larger = 0, same = 0;
+        for (int o = 0; o < inside; ++o) {
+          larger += sm.bin_key[o] > k;
+          same += sm.bin_key[o] == k;
+        }
+        if (larger < want && larger + same >= want) sm.thr = k;  // equal keys write the same
+      }
+      __syncthreads();
+      thr = sm.thr;
+    } else if (inside > want) {
+      // a crowded bin (a few scores far from all others): bit by bit below the bin's edge, two
+      // at a time; it is enough that exactly K keys are at or above
+      for (int bit = shift - 1; bit >= 0; bit -= 2) {
+        const uint32_t hi = 1u << bit, lo = bit > 0 ? hi >> 1 : 0u;
+        int n3[3] = {0, 0, 0};
+        each([&](int i, uint32_t k) {
+          if (i >= m) return;
+          n3[0] += k >= thr + lo;
+          n3[1] += k >= thr + hi;
+          n3[2] += k >= thr + hi + lo;
+        });
+        count(n3);
+        const int take = n3[2] >= K ? 3 : n3[1] >= K ? 2 : n3[0] >= K ? 1 : 0;
+        if (take & 2) thr += hi;
+        if (take & 1) thr += lo;
+        if (take != 0 && n3[take - 1] == K) break;
+      }
+    }
+    const float tau = key_value(thr), width = 2.02f * range.err;
     low = tau - width;
     high = tau + width;
-    int c[2] = {0, 0};
+    int so[2] = {0, 0};  // per warp
     each([&](int i, uint32_t k) {
-      if (i >= m) return;
       const float x = key_value(k);
-      c[0] += x > high;
-      c[1] += x >= low && !(x > high);
+      const uint32_t in = __ballot_sync(0xffffffffu, i < m && x >= low);
+      const int s = __popc(__ballot_sync(0xffffffffu, i < m && x > high));
+      if (lane == 0) {
+        bits[i >> 5] = in;
+        so[0] += s;
+        so[1] += __popc(in) - s;
+      }
     });
-    count(c);
-    sure = c[0];
-    open = c[1];
+    count(so);
+    sure = so[0];
+    open = so[1];
   }
   const int need = K - sure;  // of the open ones
   const int words = (m + 31) >> 5;
-  if (!all_exact && open == need) {
-    each([&](int i, uint32_t k) {
-      const uint32_t v = __ballot_sync(0xffffffffu, i < m && key_value(k) >= low);
-      if (lane == 0) bits[i >> 5] = v;
-    });
+  if (all_exact || open != need) {
     __syncthreads();
-  } else {
     for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
     if (!all_exact && open <= kMaxOpen) {
       each([&](int i, uint32_t k) {
@@ -564,7 +635,31 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     }
   }
 
-  // the selected candidates in ascending order: each thread writes out a run of words
+  // the selected candidates in ascending order
+  if (m <= kHeldAll) {  // every warp sums the words up for itself
+    const uint32_t w0 = lane < words ? bits[lane] : 0u, w1 = 32 + lane < words ? bits[32 + lane] : 0u;
+    int s0 = __popc(w0), s1 = __popc(w1);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v0 = __shfl_up_sync(0xffffffffu, s0, off), v1 = __shfl_up_sync(0xffffffffu, s1, off);
+      if (lane >= off) {
+        s0 += v0;
+        s1 += v1;
+      }
+    }
+    s1 += __shfl_sync(0xffffffffu, s0, 31) - __popc(w1);
+    s0 -= __popc(w0);
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int w = e * kWarps + warp;  // this warp's word
+      if (w >= words) break;
+      const uint32_t v = __shfl_sync(0xffffffffu, w < 32 ? w0 : w1, w & 31);
+      const int to = p.first + __shfl_sync(0xffffffffu, w < 32 ? s0 : s1, w & 31) + __popc(v & ((1u << lane) - 1u));
+      if (v >> lane & 1u) list[to] = p.first + 32 * w + lane;
+    }
+    return;
+  }
+  // each thread writes out a run of words
   const int per = (words + kThreads - 1) / kThreads;
   const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
   int mine = 0;
@@ -575,13 +670,26 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     const int v = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += v;
   }
-  int* sums = reinterpret_cast<int*>(sm.kmin);  // last read before several barriers
-  if (lane == 31) sums[warp] = incl;
+  __syncthreads();  // sums is read again
+  if (lane == 31) sm.sums[warp] = incl;
   __syncthreads();
   int to = p.first + incl - mine;
-  for (int w = 0; w < warp; ++w) to += sums[w];
+  for (int w = 0; w < warp; ++w) to += sm.sums[w];
   for (int w = w0; w < w1; ++w)
     for (uint32_t v = bits[w]; v; v &= v - 1) list[to++] = p.first + 32 * w + __ffs((int)v) - 1;
+}
+
+template <int D>
+__device__ __forceinline__ void clear_select(SelectSmem<D>& sm) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bins[i] = 0;
+  if (threadIdx.x == 0) sm.open_n = sm.bin_n = 0;
+}
+__device__ __forceinline__ Range join_lanes(Range v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v.err = max_nan(v.err, __shfl_xor_sync(0xffffffffu, v.err, off));
+  v.kmin = __reduce_min_sync(0xffffffffu, v.kmin);
+  v.kmax = __reduce_max_sync(0xffffffffu, v.kmax);
+  return v;
 }
 
 __device__ __forceinline__ void whole_list(const BlocksPar& p, int t, int kh, int n) {
@@ -607,64 +715,85 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   }
   const int64_t list = (int64_t)t * p.Hkv + kh;
   const float* scores = p.scores + list * p.max_blocks + p.first;
-  float err = 0.f;
-  for (int c = 0; p.first + c * p.chunk < n - p.last; ++c) err = max_nan(err, __ldcg(p.errors + list * p.chunks + c));
-  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, err, bits,
+  Range range = no_scores();
+  const int lane = threadIdx.x & 31;
+  for (int c = lane; p.first + c * p.chunk < n - p.last; c += 32) range = join(range, p.ranges[list * p.chunks + c]);
+  range = join_lanes(range);
+  clear_select(sm);
+  __syncthreads();
+  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, range, bits,
                    p.keys + list * p.max_blocks, sm);
 }
 
 // Both in one kernel for lists of up to kHeldAll candidates: a cluster of p.chunks CTAs scores
-// runs of p.chunk candidates into shared memory, its first CTA selects.
+// runs of p.chunk candidates into the shared memory of its first CTA, which selects.  One
+// token's call is a chain of latencies, so the loads that do not wait for each other go out
+// together (lengths, q, page numbers, then the bounds), scores are pushed rather than fetched,
+// and the other CTAs leave when theirs have arrived.
 template <int D>
 __global__ void __launch_bounds__(kThreads) block_pick_kernel(const BlocksPar p) {
   __shared__ SelectSmem<D> sm;
   __shared__ __align__(16) float coef[1][2 * D];
   __shared__ uint32_t bits[kHeldAll / 32];
-  __shared__ unsigned long long keys[kHeldAll];  // the scores of this CTA's candidates first
-  __shared__ float errs[kWarps], err;
-  float* mine = reinterpret_cast<float*>(keys);
+  __shared__ float scores[kHeldAll];  // of the first CTA
+  __shared__ Range told[16 * kWarps];
+  __shared__ unsigned long long keys[kHeldAll];
   const int rank = blockIdx.x % p.chunks, list = blockIdx.x / p.chunks, t = list / p.Hkv, kh = list % p.Hkv;
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
+  if (p.chunks > 1) cluster_arrive();  // this CTA has started
+  clear_select(sm);
   grid_dependency_wait();
-  ReqInfo r;
-  int b;
-  const int n = query_blocks(p, t, &r, &b, rank == 0 && kh == 0 && threadIdx.x == 0);
+  int b, nn, j;
+  const bool report = rank == 0 && kh == 0 && threadIdx.x == 0;
+  const bool found = find_token(p.cu_seqlens, p.B, t, &b, &nn, &j);
+  if (!found) {  // the whole cluster
+    if (p.chunks > 1) cluster_wait();
+    if (report) set_status(p.status, ATTN_STATUS_SEQLENS);
+    return;
+  }
+  for (int d = threadIdx.x; d < D; d += kThreads) coefficients(p, t, kh, D, d, &coef[0][d], &coef[0][D + d]);
+  const int i0 = p.first + rank * p.chunk;
+  // the row of the first block that this lane will look up, before it is known to be there
+  constexpr int PER = 8 * 32 / (D / 4);  // blocks per warp and pass
+  const int ahead = i0 + warp * PER + lane;
+  const int64_t row0 = lane < PER ? bounds_row_at(p, b, ahead) : -1;
+  const ReqInfo r = load_request(p.kv, b, nn);
+  const int n = visible_blocks(p, r, j, report);
+  if (p.chunks > 1) cluster_wait();  // every CTA has started: its shared memory is there
   if (n == 0) return;
   if (n <= p.keep) {
     if (rank == 0) whole_list(p, t, kh, n);
     return;
   }
-  const int i0 = p.first + rank * p.chunk, i1 = min(i0 + p.chunk, n - p.last);
-  if (i0 < i1) {
-    for (int d = threadIdx.x; d < D; d += kThreads) coefficients(p, t, kh, D, d, &coef[0][d], &coef[0][D + d]);
-    __syncthreads();
-    if (score_blocks<D>(
-            p, r, b, kh, i0, i1, 1, coef, [&](int, int i, float v) { mine[i - i0] = v; },
-            [&](int, float e) { errs[warp] = e; }))
-      set_status(p.status, ATTN_STATUS_CAPACITY);
-  } else if (threadIdx.x < kWarps) {
-    errs[threadIdx.x] = 0.f;
-  }
+  const int i1 = min(i0 + p.chunk, n - p.last);
   __syncthreads();
-  if (threadIdx.x == 0) err = max_of_warps(errs);
-  if (p.chunks > 1) cluster_sync();
-  else __syncthreads();
-  if (rank == 0) {
-    const uint32_t base = smem_u32(mine);
-    const int lane = threadIdx.x & 31;
-    float e = lane < p.chunks ? peer_f32(smem_u32(&err), lane) : 0.f;
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, off));
-    e = __shfl_sync(0xffffffffu, e, 0);
-    // a candidate's score is read once, into a register, and keys are written behind a
-    // barrier after those reads
-    const int sh = 31 - __clz(p.chunk);
-    select_blocks<D>(p, r, b, t, kh, n, [&](int i) {
-      return peer_f32(base + (uint32_t)(i & (p.chunk - 1)) * 4u, i >> sh);
-    }, e, bits, keys, sm);
+  const uint32_t to = peer_addr(smem_u32(scores), 0), to_range = peer_addr(smem_u32(told + rank * kWarps + warp), 0);
+  auto tell = [&](int, const Range& v) {
+    peer_store(to_range, v.err);
+    peer_store(to_range + 4, __uint_as_float(v.kmin));
+    peer_store(to_range + 8, __uint_as_float(v.kmax));
+  };
+  if (i0 < i1) {
+    if (score_blocks<D, false>(
+            p, kh, i0, i1, 1, coef, [&](int i) { return i == ahead ? row0 : bounds_row(p, r, b, i); },
+            [&](int, int i, float v) { peer_store(to + (uint32_t)(i - p.first) * 4u, v); },
+            tell))
+      set_status(p.status, ATTN_STATUS_CAPACITY);
+  } else if (lane == 0) {
+    tell(0, no_scores());
   }
-  if (p.chunks > 1) cluster_sync();  // no CTA leaves while the first one reads from it
+  if (p.chunks > 1) {
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  Range range = no_scores();
+  for (int w = lane; w < p.chunks * kWarps; w += 32) range = join(range, told[w]);
+  range = join_lanes(range);
+  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return scores[i]; }, range, bits, keys, sm);
 }
 
 // ---------------------------------------------------------------- host
@@ -711,10 +840,10 @@ int blocks_of(int32_t max_kv_len, int32_t block_size) { return (int)(((int64_t)m
 
 constexpr int kChunk = 128;  // blocks per CTA of the two-kernel selection
 
-// Behind the header: scores, exact scores, bounds on errors.
+// Behind the header: exact scores, scores, ranges.
 size_t scores_bytes(const attn_config_t* cfg, int64_t N, int32_t max_blocks) {
   const size_t lists = (size_t)N * cfg->num_kv_heads;
-  return align_up(lists * max_blocks * (sizeof(float) + 8) + lists * ((max_blocks + kChunk - 1) / kChunk) * sizeof(float), 256);
+  return align_up(lists * max_blocks * (sizeof(float) + 8) + lists * ((max_blocks + kChunk - 1) / kChunk) * sizeof(Range), 256);
 }
 
 template <int D, int KV>
@@ -826,7 +955,7 @@ int attn_block_select(const attn_config_t* cfg, const void* q, const int32_t* cu
   const size_t slots = (size_t)N * p.Hkv * max_blocks;
   p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + kWsHeader);
   p.scores = reinterpret_cast<float*>(p.keys + slots);
-  p.errors = p.scores + slots;
+  p.ranges = reinterpret_cast<Range*>(p.scores + slots);
   p.list = list;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cfg->head_dim == 128 ? launch_select_t<128>(p, s) : launch_select_t<64>(p, s);

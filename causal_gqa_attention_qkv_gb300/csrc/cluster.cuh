@@ -25,6 +25,25 @@ __device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// The two halves of cluster_sync(): a CTA that only hands over may leave after the first.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in CTA `rank` of what is at `addr` in this CTA's shared memory; a store to it.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t peer, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer), "f"(v) : "memory");
+}
+
 // launch_dependent() in clusters of `cluster` CTAs along x (up to 16).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
