@@ -247,7 +247,7 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % L, sub = lane / L;
   bool outside = false;
   uint4 big = make_uint4(0, 0, 0, 0);  // largest magnitudes
-  uint32_t kmin = ~0u, kmax = 0u;        // of all tokens
+  float lowest = -kNegInf, highest = kNegInf;  // scores of all tokens (a NaN shows in the error bound)
   const uint4* rows = reinterpret_cast<const uint4*>(p.bounds) + kh * (D / 4) + li;
   for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
     // rows of the warp's blocks, one per lane
@@ -303,23 +303,25 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
         const int at = i + (g + (lane & (S - 1))) * BPW + sub;
         if (li < S && at < i1) {
           put(t, at, s[0]);
-          const uint32_t k = order_key(s[0]);
-          kmin = min(kmin, k);
-          kmax = max(kmax, k);
+          lowest = fminf(lowest, s[0]);
+          highest = fmaxf(highest, s[0]);
         }
         if constexpr (!Many) break;
       }
     }
   }
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  const uint32_t kmin = __reduce_min_sync(0xffffffffu, order_key(lowest));
+  const uint32_t kmax = __reduce_max_sync(0xffffffffu, order_key(highest));
   float y[8];
   unpack_bf16x8(big, y);
 #pragma unroll 1
   for (int t = 0; t < tokens; ++t) {
+    const float4 u = *reinterpret_cast<const float4*>(&coef[t][8 * li]);
+    const float4 v = *reinterpret_cast<const float4*>(&coef[t][8 * li + 4]);
+    const float c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
     float a = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaf(fabsf(coef[t][8 * li + e]), y[e], a);
+    for (int e = 0; e < 8; ++e) a = fmaf(fabsf(c[e]), y[e], a);
 #pragma unroll
     for (int off = 1; off < L; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
     if (BPW > 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, L & 31));
@@ -328,51 +330,95 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
   return outside;
 }
 
-// Scores for the two-kernel selection: a CTA takes a run of blocks for kTokens
-// consecutive tokens, those of one request at a time, so that the bounds are read once for all.
+// Scores for the two-kernel selection: a CTA takes a run of blocks for up to kTokens tokens of a
+// request, so that the bounds are read once for all of them.
 constexpr int kTokens = 8;
+
+// The g-th group of up to kTokens tokens: request *b, its tokens from place *j on.  False past
+// the last one.  All threads of the CTA call this.
+__device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, int* j) {
+  if (!p.cu_seqlens) {
+    *b = g;
+    *j = 0;
+    return g < p.B;
+  }
+  __shared__ int sums[kWarps], found[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int i = b0 + threadIdx.x;
+    const int n = i < p.B ? __ldg(p.cu_seqlens + i + 1) - __ldg(p.cu_seqlens + i) : 0;
+    const int mine = (max(n, 0) + kTokens - 1) / kTokens;
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += sums[w];
+      total += sums[w];
+    }
+    if (g < total) {
+      if (g >= incl - mine && g < incl) {
+        found[0] = i;
+        found[1] = (g - (incl - mine)) * kTokens;
+      }
+      __syncthreads();
+      *b = found[0];
+      *j = found[1];
+      return true;
+    }
+    g -= total;
+    __syncthreads();
+  }
+  return false;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
+__global__ void __launch_bounds__(kThreads, 3) block_score_kernel(const BlocksPar p) {
   __shared__ __align__(16) float coef[kTokens][2 * D];  // M, P
   __shared__ Range told[kTokens][kWarps];
   const int warp = threadIdx.x >> 5;
-  const int kh = blockIdx.x / p.chunks % p.Hkv, t0 = blockIdx.x / p.chunks / p.Hkv * kTokens, c = blockIdx.x % p.chunks;
+  const int kh = blockIdx.x / p.chunks % p.Hkv, c = blockIdx.x % p.chunks;
   launch_dependents();
   grid_dependency_wait();
-  const bool report = c == 0 && kh == 0 && threadIdx.x == 0;
-  const int t1 = min(t0 + kTokens, p.N);
-  for (int t = t0, next; t < t1; t = next) {
-    int b, n, j;
-    next = t + 1;
-    if (!find_token(p.cu_seqlens, p.B, t, &b, &n, &j)) {
-      if (report) set_status(p.status, ATTN_STATUS_SEQLENS);
-      continue;
-    }
-    const int run = min(n - j, t1 - t);
-    next = t + run;
-    const ReqInfo r = load_request(p.kv, b, n);
-    int most = 0;  // blocks of the last token that has a list; those of the others end no later
-    for (int k = 0; k < run; ++k) most = max(most, visible_blocks(p, r, j + k, report));
-    const int i0 = p.first + c * p.chunk, i1 = min(i0 + p.chunk, most - p.last);
-    if (most <= p.keep || i0 >= i1) continue;
-    for (int i = threadIdx.x; i < run * D; i += kThreads)
-      coefficients(p, t + i / D, kh, D, i % D, &coef[i / D][i % D], &coef[i / D][D + i % D]);
-    __syncthreads();
-    const int64_t list = (int64_t)t * p.Hkv + kh;
-    const bool outside = score_blocks<D, true>(
-        p, kh, i0, i1, run, coef, [&](int i) { return bounds_row(p, r, b, i); },
-        [&](int k, int i, float v) {
-          p.scores[(list + (int64_t)k * p.Hkv) * p.max_blocks + i] = v;  // some past what the token sees
-        },
-        [&](int k, const Range& v) { told[k][warp] = v; });
-    if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
-    __syncthreads();
-    if ((int)threadIdx.x < run) {
-      Range v = told[threadIdx.x][0];
-      for (int w = 1; w < kWarps; ++w) v = join(v, told[threadIdx.x][w]);
-      p.ranges[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = v;
-    }
-    __syncthreads();
+  int b, j, n = 1, t = 0;
+  if (!find_group(p, blockIdx.x / p.chunks / p.Hkv, &b, &j)) return;
+  if (p.cu_seqlens) {
+    t = __ldg(p.cu_seqlens + b);
+    n = __ldg(p.cu_seqlens + b + 1) - t;
+    t += j;
+  } else {
+    t = b;
+  }
+  const int run = min(min(n - j, kTokens), p.N - t);  // tokens past N have no list
+  if (t < 0 || run <= 0) return;
+  const ReqInfo r = load_request(p.kv, b, n);
+  const int most = r.valid ? ((r.cached + j + run - 1) >> p.log2_bs) + 1 : 0;  // blocks that the last token sees
+  const int i0 = p.first + c * p.chunk, i1 = min(min(i0 + p.chunk, most - p.last), p.max_blocks);
+  if (most <= p.keep || i0 >= i1) return;
+  for (int i = threadIdx.x; i < run * D; i += kThreads)
+    coefficients(p, t + i / D, kh, D, i % D, &coef[i / D][i % D], &coef[i / D][D + i % D]);
+  __syncthreads();
+  const int64_t list = (int64_t)t * p.Hkv + kh;
+  float* to = p.scores + list * p.max_blocks;
+  const int stride = p.Hkv * p.max_blocks;  // to the next token's scores: below 2^26
+  const bool outside = score_blocks<D, true>(
+      p, kh, i0, i1, run, coef, [&](int i) { return bounds_row(p, r, b, i); },
+      [&](int k, int i, float v) {
+        to[k * stride + i] = v;  // some past what the token sees
+      },
+      [&](int k, const Range& v) { told[k][warp] = v; });
+  if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
+  __syncthreads();
+  if ((int)threadIdx.x < run) {
+    Range v = told[threadIdx.x][0];
+    for (int w = 1; w < kWarps; ++w) v = join(v, told[threadIdx.x][w]);
+    p.ranges[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = v;
   }
 }
 
@@ -483,8 +529,10 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     // A threshold with exactly K keys at or above it, or else the K-th key: the keys in bins of
     // equal width, then those of the K-th's bin (one or two of 1000) by their ranks.
     const int shift = max(0, 22 - __clz((int)(kmax - kmin)));  // the range in fewer than kBins steps
+    // (cu_seqlens that are not in order can leave scores unwritten: nothing may index past its array)
+    auto bin_of = [&](uint32_t k) { return min((k - kmin) >> shift, (uint32_t)kBins - 1u); };
     each([&](int i, uint32_t k) {
-      if (i < m) atomicAdd(&sm.bins[(k - kmin) >> shift], 1);
+      if (i < m) atomicAdd(&sm.bins[bin_of(k)], 1);
     });
     __syncthreads();
     constexpr int R = kBins / kThreads;  // bins per thread, the highest first
@@ -520,7 +568,7 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     if (inside > want && inside <= kMaxOpen) {
       const uint32_t bin = sm.bin;
       each([&](int i, uint32_t k) {
-        if (i < m && (k - kmin) >> shift == bin) sm.bin_key[atomicAdd(&sm.bin_n, 1)] = k;  // in any order
+        if (i < m && bin_of(k) == bin) sm.bin_key[atomicAdd(&sm.bin_n, 1)] = k;  // in any order
       });
       __syncthreads();
       if (tid < inside) {
@@ -655,7 +703,7 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
       if (w >= words) break;
       const uint32_t v = __shfl_sync(0xffffffffu, w < 32 ? w0 : w1, w & 31);
       const int to = p.first + __shfl_sync(0xffffffffu, w < 32 ? s0 : s1, w & 31) + __popc(v & ((1u << lane) - 1u));
-      if (v >> lane & 1u) list[to] = p.first + 32 * w + lane;
+      if ((v >> lane & 1u) && to < p.first + K) list[to] = p.first + 32 * w + lane;
     }
     return;
   }
@@ -676,7 +724,7 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
   int to = p.first + incl - mine;
   for (int w = 0; w < warp; ++w) to += sm.sums[w];
   for (int w = w0; w < w1; ++w)
-    for (uint32_t v = bits[w]; v; v &= v - 1) list[to++] = p.first + 32 * w + __ffs((int)v) - 1;
+    for (uint32_t v = bits[w]; v && to < p.first + K; v &= v - 1) list[to++] = p.first + 32 * w + __ffs((int)v) - 1;
 }
 
 template <int D>
@@ -707,7 +755,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   grid_dependency_wait();
   ReqInfo r;
   int b;
-  const int n = query_blocks(p, t, &r, &b, false);
+  const int n = query_blocks(p, t, &r, &b, kh == 0 && threadIdx.x == 0);
   if (n == 0) return;
   if (n <= p.keep) {
     whole_list(p, t, kh, n);
@@ -881,7 +929,8 @@ int launch_select_t(BlocksPar& p, cudaStream_t s) {
   }
   p.chunk = kChunk;
   p.chunks = (p.max_blocks + p.chunk - 1) / p.chunk;
-  const int64_t ctas = ((int64_t)p.N + kTokens - 1) / kTokens * p.Hkv * p.chunks;
+  const int64_t groups = std::min<int64_t>(p.N, p.N / kTokens + (int64_t)p.B);
+  const int64_t ctas = groups * p.Hkv * p.chunks;
   if (ctas > 0x7fffffff || lists > 0x7fffffff) return ATTN_EINVAL;
   if (launch_dependent(block_score_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), 0, s, p) != cudaSuccess)
     return ATTN_ELAUNCH;

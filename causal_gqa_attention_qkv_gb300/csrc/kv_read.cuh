@@ -34,7 +34,8 @@ __device__ __forceinline__ uint4 read8(const void* cache, const uint8_t* bscale,
 }
 
 // The request of packed token t, the number of its new tokens and the token's place j
-// among them; cu == NULL: one token per request.  False for a token of no request.
+// among them; cu == NULL: one token per request.  False for a token of no request.  The lanes
+// of a warp search together, 32 requests a step: all of them call this with the same t.
 __device__ __forceinline__ bool find_token(const int32_t* cu, int B, int t, int* b, int* n, int* j) {
   if (!cu) {
     *b = t;
@@ -42,10 +43,13 @@ __device__ __forceinline__ bool find_token(const int32_t* cu, int B, int t, int*
     *j = 0;
     return true;
   }
+  const int lane = threadIdx.x & 31;
   int lo = 0, hi = B;  // largest b with cu[b] <= t
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) >> 5, probe = lo + (lane + 1) * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, probe < hi && __ldg(cu + probe) <= t));
+    lo += below * step;
+    hi = min(hi, lo + step);
   }
   const int c0 = __ldg(cu + lo);
   *b = lo;
