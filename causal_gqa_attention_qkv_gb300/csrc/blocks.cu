@@ -3,7 +3,7 @@
 // decode_e2m1.cu).
 //
 // Bounds: one warp per (full block, KV head) reads the block's keys, 16 bytes per
-// lane, and keeps the minimum and maximum of 8 components in registers.  Bound by HBM.
+// lane, and keeps the minima and maxima of its components in registers.  Bound by HBM.
 //
 // Selection, with the group's heads h and a block's bounds lo, hi:
 //   score = sum_h sum_d max(q_hd lo_d, q_hd hi_d) = sum_d M_d lo_d + P_d hi_d,
@@ -92,9 +92,55 @@ __device__ __forceinline__ int64_t bounds_row_at(const BlocksPar& p, int b, int 
 }
 
 // ---------------------------------------------------------------- bounds
+// 16 bytes of a head's vector as pairs in which minimum and maximum are taken: bf16 entries as
+// they are; codes as f16 pairs, exact (code, or code times block scale).  The product with the
+// tensor's scale and the rounding to bf16 keep the order and are left to the end.
+template <int KV>
+struct Chunk {
+  static constexpr int kPairs = KV == ATTN_KV_BF16 ? 4 : KV == ATTN_KV_E4M3 ? 8 : 16;
+  uint32_t v[kPairs];
+};
+template <int KV>
+__device__ __forceinline__ void unpack_chunk(const uint4& x, uint32_t scales, Chunk<KV>& c) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (KV == ATTN_KV_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.v[i] = w[i];
+  } else if constexpr (KV == ATTN_KV_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e4m3x4_to_f16(w[i], c.v[2 * i], c.v[2 * i + 1]);
+  } else {
+    const uint32_t s = e4m3x2_to_f16(scales);  // the two blocks of 16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t* h = c.v + 4 * i;
+      e2m1x8_to_f16(w[i], h[0], h[1], h[2], h[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = i < 2 ? mul_f16x2_lo(h[e], s) : mul_f16x2_hi(h[e], s);
+    }
+  }
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) {
+  if constexpr (!F16) return min2(a, b);
+  const __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t higher(uint32_t a, uint32_t b) {
+  if constexpr (!F16) return max2(a, b);
+  const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One warp per (block, KV head), a lane 16 bytes of a key, 8 loads (or those of 64 keys) in flight.
 template <int D, int KV>
 __global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BlocksPar p) {
-  constexpr int L = D / 8, KPW = 32 / L;  // lanes per key, keys per warp and step
+  constexpr bool F16 = KV != ATTN_KV_BF16;
+  constexpr int kBytes = KV == ATTN_KV_BF16 ? 2 * D : KV == ATTN_KV_E4M3 ? D : D / 2;  // of a key
+  constexpr int L = kBytes / 16, KPW = 32 / L;   // lanes per key, keys per warp and load
+  constexpr int U = 64 / KPW < 8 ? 64 / KPW : 8;
+  constexpr int P = Chunk<KV>::kPairs;
   const int b = blockIdx.x / p.ctas_per_request, part = blockIdx.x % p.ctas_per_request;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
@@ -115,29 +161,60 @@ __global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BlocksPar 
     const int64_t row = bounds_row(p, r, b, i);
     if ((slot < 0 || row < 0) && lane == 0) set_status(p.status, ATTN_STATUS_CAPACITY);
     if (row < 0) continue;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    Chunk<KV> lo = {}, hi = {};
     if (slot >= 0) {
-      auto key = [&](int k) {
-        return read8<KV>(p.k_cache, p.k_block_scale, p.k_scale, p.kv.num_slots, slot + k, p.Hkv, kh, li, D == 128 ? 4 : 3);
-      };
-      lo = hi = key(sub);
+      const uint4* keys = static_cast<const uint4*>(p.k_cache) + ((slot + sub) * p.Hkv + kh) * L + li;
+      const uint16_t* scales = nullptr;  // of this lane's 32 codes
+      if constexpr (KV == ATTN_KV_E2M1)
+        scales = reinterpret_cast<const uint16_t*>(p.k_block_scale + ((int64_t)kh * p.kv.num_slots + slot + sub) * (D / 16)) + li;
       const int bs = 1 << p.log2_bs;
-#pragma unroll 8
-      for (int k = sub + KPW; k < bs; k += KPW) {
-        const uint4 x = key(k);
-        lo = make_uint4(min2(lo.x, x.x), min2(lo.y, x.y), min2(lo.z, x.z), min2(lo.w, x.w));
-        hi = make_uint4(max2(hi.x, x.x), max2(hi.y, x.y), max2(hi.z, x.z), max2(hi.w, x.w));
+#pragma unroll 1
+      for (int k0 = 0; k0 < bs; k0 += U * KPW) {
+        uint4 x[U];
+        uint32_t s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u] = __ldg(keys + (int64_t)(k0 + u * KPW) * (p.Hkv * L));
+          s[u] = KV == ATTN_KV_E2M1 ? __ldg(scales + (k0 + u * KPW) * (D / 32)) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Chunk<KV> c;
+          unpack_chunk<KV>(x[u], s[u], c);
+          if (u == 0 && k0 == 0) {
+            lo = hi = c;
+          } else {
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              lo.v[e] = lower<F16>(lo.v[e], c.v[e]);
+              hi.v[e] = higher<F16>(hi.v[e], c.v[e]);
+            }
+          }
+        }
       }
 #pragma unroll
-      for (int off = L; off < 32; off <<= 1) {
-        auto other = [&](uint32_t v) { return __shfl_xor_sync(0xffffffffu, v, off); };
-        lo = make_uint4(min2(lo.x, other(lo.x)), min2(lo.y, other(lo.y)), min2(lo.z, other(lo.z)), min2(lo.w, other(lo.w)));
-        hi = make_uint4(max2(hi.x, other(hi.x)), max2(hi.y, other(hi.y)), max2(hi.z, other(hi.z)), max2(hi.w, other(hi.w)));
+      for (int off = L; off < 32; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          lo.v[e] = lower<F16>(lo.v[e], __shfl_xor_sync(0xffffffffu, lo.v[e], off));
+          hi.v[e] = higher<F16>(hi.v[e], __shfl_xor_sync(0xffffffffu, hi.v[e], off));
+        }
+      if constexpr (F16) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo.v[e]));
+          const float2 c = __half22float2(*reinterpret_cast<__half2*>(&hi.v[e]));
+          lo.v[e] = pack_bf16(__fmul_rn(a.x, p.k_scale), __fmul_rn(a.y, p.k_scale));
+          hi.v[e] = pack_bf16(__fmul_rn(c.x, p.k_scale), __fmul_rn(c.y, p.k_scale));
+        }
       }
     }
-    if (lane < 2 * L) {
-      uint4* dst = reinterpret_cast<uint4*>(p.bounds + (row * p.Hkv + kh) * (2 * D));
-      dst[lane] = lane < L ? lo : hi;  // lanes L .. 2 L - 1: component run lane - L, as in lane % L
+    if (sub < 2) {  // the first group of lanes writes the minima, the second the maxima
+      uint4* dst = reinterpret_cast<uint4*>(p.bounds + ((row * p.Hkv + kh) * 2 + sub) * D) + li * (P / 4);
+#pragma unroll
+      for (int e = 0; e < P; e += 4)
+        dst[e / 4] = sub == 0 ? make_uint4(lo.v[e], lo.v[e + 1], lo.v[e + 2], lo.v[e + 3])
+                              : make_uint4(hi.v[e], hi.v[e + 1], hi.v[e + 2], hi.v[e + 3]);
     }
   }
 }
