@@ -3,9 +3,8 @@
 // Each logit goes through x + bias, the repetition penalty, the frequency and
 // presence penalties and the mask, each operation rounded to fp32.  Bound by memory:
 // 4 bytes read and 4 written per logit, 2 of the table, an eighth of a byte of the mask.
-// A CTA takes a run of one row; the row's biases, few and in any order, are filtered for the
-// run first and summed in shared memory, each token's by one thread in list order (no
-// atomics: the order decides the rounding).
+// A CTA takes a run of one row and filters the row's biases, few and in any order, for it;
+// those of one token are summed by one thread in list order (the order decides the rounding).
 #include "kernels.cuh"
 #include "../../include/logits.h"
 
@@ -23,32 +22,73 @@ struct AdjustPar {
   attn_logits_rules_t r;
 };
 
-// One logit through the rules after the bias.
-__device__ __forceinline__ float apply_rules(float x, uint32_t word, float rep, float freq, float pres, bool allowed) {
-  if (word) {
-    if (rep > 0.f) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-    const uint32_t n = word & 0x7FFFu;
-    if (n) {
-      x = __fsub_rn(x, __fmul_rn(freq, (float)n));
-      x = __fsub_rn(x, pres);
-    }
+struct Penalties {
+  float repetition, frequency, presence;
+};
+// A logit of a seen token, after the bias.
+__device__ __forceinline__ float penalised(float x, uint32_t word, const Penalties& c) {
+  if (c.repetition > 0.f) x = x > 0.f ? __fdiv_rn(x, c.repetition) : __fmul_rn(x, c.repetition);
+  const uint32_t n = word & 0x7FFFu;
+  if (n) {
+    x = __fsub_rn(x, __fmul_rn(c.frequency, (float)n));
+    x = __fsub_rn(x, c.presence);
   }
-  return allowed ? x : kNegInf;
+  return x;
+}
+
+constexpr int kListed = 1024;
+
+// The row's biases for the tokens of a run in list order, summed into bias[] (kRun floats): each
+// token's by one thread.  For rows with many of them.
+__device__ void sum_biases(const attn_logits_rules_t& r, int e0, int e1, int v0, int n, int run, float* bias, int* tok,
+                           float* val, int* cnt) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int k = tid; k < run; k += kThreads) bias[k] = 0.f;
+  for (int e = e0; e < e1; e += kThreads) {
+    const int i = e + tid;
+    const int t = i < e1 ? __ldg(r.bias_token + i) : -1;
+    const bool mine = t >= v0 && t < v0 + n;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) cnt[warp] = __popc(all);
+    __syncthreads();
+    int at = 0, m = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += cnt[w];
+      m += cnt[w];
+    }
+    if (mine) {
+      at += __popc(all & ((1u << lane) - 1u));
+      tok[at] = t - v0;
+      val[at] = __ldg(r.bias_value + i);
+    }
+    __syncthreads();
+    for (int k = 0; k < m; ++k)
+      if ((tok[k] & (kThreads - 1)) == tid) bias[tok[k]] += val[k];
+    __syncthreads();
+  }
 }
 
 // Four logits per thread and step, Q steps: all loads of a run go out before its biases are
 // looked at.  Vec: rows of logits and out are 16-byte aligned, a thread's four are neighbours;
-// else they are 256 apart (a row's start may lie anywhere).
+// else they are 256 apart (a row's start may lie anywhere).  Seen and biased tokens are few and
+// scattered (a division in place would keep most warps for one lane): they go to lists in shared
+// memory that the threads share out, and are stored after the others.  A list of seen
+// tokens that is full leaves the rest in place; a run with more than kThreads biases takes
+// sum_biases().
 template <int Q, bool Vec>
 __global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar p) {
   constexpr int kRun = Q * 4 * kThreads;
   __shared__ __align__(16) float bias[kRun];
-  __shared__ int tok[kThreads];
+  __shared__ int tok[kThreads], idx[kThreads];
   __shared__ float val[kThreads];
-  __shared__ int cnt[kThreads / 32];
+  __shared__ int cnt[kThreads / 32], listed, biases;
+  __shared__ float list_x[kListed];
+  __shared__ uint32_t list_at[kListed];  // place in the run, word << 16
   const int b = blockIdx.x / p.runs, v0 = blockIdx.x % p.runs * kRun;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   launch_dependents();
+  if (tid == 0) listed = biases = 0;
+  __syncthreads();
   grid_dependency_wait();
   const int n = min(kRun, p.V - v0);  // logits of this run
   const float* in = p.logits + b * p.ld + v0;
@@ -64,73 +104,124 @@ __global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar
     if (row >= 0 && row < p.r.mask_rows) mask = p.r.mask + row * p.r.mask_ld + (v0 >> 5);
   }
   auto place = [&](int q, int e) { return Vec ? (q * kThreads + tid) * 4 + e : (q * 4 + e) * kThreads + tid; };
+  auto allowed = [&](int i) { return !mask || (__ldg(mask + (i >> 5)) >> (i & 31) & 1u); };
   float x[Q][4];
-  uint32_t word[Q][4], allow[Q][4];
+  uint2 words[Q];     // of the four logits
+  uint32_t allow[Q];  // bit e
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int i0 = place(q, 0);
+    allow[q] = 15u;
     if (Vec && i0 + 4 <= n) {
       *reinterpret_cast<float4*>(x[q]) = *reinterpret_cast<const float4*>(in + i0);
-      const uint2 w = seen ? *reinterpret_cast<const uint2*>(seen + i0) : make_uint2(0u, 0u);
-      const uint32_t m = mask ? __ldg(mask + (i0 >> 5)) >> (i0 & 31) : 15u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        word[q][e] = ((e < 2 ? w.x : w.y) >> (16 * (e & 1))) & 0xFFFFu;
-        allow[q][e] = m >> e & 1u;
-      }
+      words[q] = seen ? *reinterpret_cast<const uint2*>(seen + i0) : make_uint2(0u, 0u);
+      if (mask) allow[q] = __ldg(mask + (i0 >> 5)) >> (i0 & 31);
     } else {
+      uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = place(q, e);
         const bool there = i < n;
         x[q][e] = there ? in[i] : 0.f;
-        word[q][e] = there && seen ? seen[i] : 0u;
-        allow[q][e] = there && mask ? __ldg(mask + (i >> 5)) >> (i & 31) & 1u : 1u;
+        w[e] = there && seen ? seen[i] : 0u;
+        if (mask && there && !allowed(i)) allow[q] &= ~(1u << e);
       }
+      words[q] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
   }
-  const float rep = p.r.repetition ? __ldg(p.r.repetition + b) : 0.f;
-  const float freq = p.r.frequency ? __ldg(p.r.frequency + b) : 0.f;
-  const float pres = p.r.presence ? __ldg(p.r.presence + b) : 0.f;
-  bool biased = false;
+  const Penalties c = {p.r.repetition ? __ldg(p.r.repetition + b) : 0.f, p.r.frequency ? __ldg(p.r.frequency + b) : 0.f,
+                       p.r.presence ? __ldg(p.r.presence + b) : 0.f};
+  int few = 0;  // biases in the run, if they fit the list
   if (p.r.bias_start) {
     const int e0 = __ldg(p.r.bias_start + b), e1 = __ldg(p.r.bias_start + b + 1);
-    for (int e = e0; e < e1; e += kThreads) {
-      const int i = e + tid;
-      const int t = i < e1 ? __ldg(p.r.bias_token + i) : -1;
-      const bool mine = t >= v0 && t < v0 + n;
-      const uint32_t all = __ballot_sync(0xffffffffu, mine);
-      if (lane == 0) cnt[warp] = __popc(all);
-      __syncthreads();
-      int at = 0, m = 0;
+    for (int i = e0 + tid; i < e1; i += kThreads) {
+      const int t = __ldg(p.r.bias_token + i) - v0;
+      if (t >= 0 && t < n) {
+        const int at = atomicAdd(&biases, 1);  // in any order
+        if (at < kThreads) {
+          tok[at] = t;
+          val[at] = __ldg(p.r.bias_value + i);
+          idx[at] = i;
+        }
+      }
+    }
+    __syncthreads();
+    few = biases;
+    if (few > kThreads) {
+      sum_biases(p.r, e0, e1, v0, n, kRun, bias, tok, val, cnt);
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) at += cnt[w];
-        m += cnt[w];
-      }
-      if (m > 0 && !biased) {
-        for (int k = tid; k < kRun; k += kThreads) bias[k] = 0.f;
-        biased = true;
-      }
-      if (mine) {
-        at += __popc(all & ((1u << lane) - 1u));
-        tok[at] = t - v0;
-        val[at] = __ldg(p.r.bias_value + i);
-      }
-      __syncthreads();
-      for (int k = 0; k < m; ++k)
-        if ((tok[k] & (kThreads - 1)) == tid) bias[tok[k]] += val[k];
-      __syncthreads();
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[q][e] = __fadd_rn(x[q][e], bias[place(q, e)]);
+      few = 0;
     }
   }
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
+    if (mask) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float y = x[q][e];
-      if (biased) y = __fadd_rn(y, bias[place(q, e)]);
-      x[q][e] = apply_rules(y, word[q][e], rep, freq, pres, allow[q][e] != 0u);
+      for (int e = 0; e < 4; ++e) x[q][e] = allow[q] >> e & 1u ? x[q][e] : kNegInf;
     }
+    if (words[q].x | words[q].y) {
+      uint32_t w[4] = {words[q].x & 0xFFFFu, words[q].x >> 16, words[q].y & 0xFFFFu, words[q].y >> 16};
+      int mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(allow[q] >> e & 1u)) w[e] = 0u;
+        mine += w[e] != 0u;
+      }
+      if (mine > 0) {
+        int at = atomicAdd(&listed, mine);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (w[e] == 0u) continue;
+          if (at < kListed) {
+            list_x[at] = x[q][e];
+            list_at[at] = (uint32_t)place(q, e) | (w[e] << 16);
+          } else {
+            x[q][e] = penalised(x[q][e], w[e], c);
+          }
+          ++at;
+        }
+      }
+    }
+  }
+  float special = 0.f;
+  bool owner = false;  // of a biased token: the first of its entries in list order
+  if (few > 0) {
+    if (tid < few) {
+      const int t = tok[tid], me = idx[tid];
+      owner = true;
+      float sum = 0.f;
+      // its entries in list order: the next one is that with the smallest index above the last
+      for (int last = -1;;) {
+        int next = 0x7fffffff, at = 0;
+        for (int k = 0; k < few; ++k)
+          if (tok[k] == t && idx[k] > last && idx[k] < next) {
+            next = idx[k];
+            at = k;
+          }
+        if (next == 0x7fffffff) break;
+        if (last < 0 && next != me) {  // another thread's token
+          owner = false;
+          break;
+        }
+        sum = __fadd_rn(sum, val[at]);
+        last = next;
+      }
+      if (owner) {
+        special = kNegInf;
+        if (allowed(t)) {
+          special = __fadd_rn(in[t], sum);
+          const uint32_t w = seen ? seen[t] : 0u;
+          if (w) special = penalised(special, w, c);
+        }
+      }
+    }
+    __syncthreads();  // in[] has been read where out is the same
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
     const int i0 = place(q, 0);
     if (Vec && i0 + 4 <= n) {
       *reinterpret_cast<float4*>(out + i0) = *reinterpret_cast<const float4*>(x[q]);
@@ -139,6 +230,13 @@ __global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar
       for (int e = 0; e < 4; ++e)
         if (place(q, e) < n) out[place(q, e)] = x[q][e];
     }
+  }
+  __syncthreads();  // the list is complete, and its logits are stored as they were before
+  for (int k = tid; k < min(listed, kListed); k += kThreads)
+    out[list_at[k] & 0xFFFFu] = penalised(list_x[k], list_at[k] >> 16, c);
+  if (few > 0) {
+    __syncthreads();
+    if (owner) out[tok[tid]] = special;
   }
 }
 
