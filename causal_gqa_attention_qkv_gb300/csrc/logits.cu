@@ -12,7 +12,10 @@ namespace gb300 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the kernels for seen tokens
+constexpr int kAdjust = 128;   // of a run of logits
+constexpr int kSteps = 2;      // of four logits per thread
+constexpr int kFew = kAdjust;  // biases of a run that are handled one per thread
 
 struct AdjustPar {
   const float* logits;
@@ -36,15 +39,13 @@ __device__ __forceinline__ float penalised(float x, uint32_t word, const Penalti
   return x;
 }
 
-constexpr int kListed = 1024;
-
 // The row's biases for the tokens of a run in list order, summed into bias[] (kRun floats): each
 // token's by one thread.  For rows with many of them.
 __device__ void sum_biases(const attn_logits_rules_t& r, int e0, int e1, int v0, int n, int run, float* bias, int* tok,
                            float* val, int* cnt) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int k = tid; k < run; k += kThreads) bias[k] = 0.f;
-  for (int e = e0; e < e1; e += kThreads) {
+  for (int k = tid; k < run; k += kAdjust) bias[k] = 0.f;
+  for (int e = e0; e < e1; e += kAdjust) {
     const int i = e + tid;
     const int t = i < e1 ? __ldg(r.bias_token + i) : -1;
     const bool mine = t >= v0 && t < v0 + n;
@@ -52,7 +53,7 @@ __device__ void sum_biases(const attn_logits_rules_t& r, int e0, int e1, int v0,
     if (lane == 0) cnt[warp] = __popc(all);
     __syncthreads();
     int at = 0, m = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kAdjust / 32; ++w) {
       if (w < warp) at += cnt[w];
       m += cnt[w];
     }
@@ -63,163 +64,175 @@ __device__ void sum_biases(const attn_logits_rules_t& r, int e0, int e1, int v0,
     }
     __syncthreads();
     for (int k = 0; k < m; ++k)
-      if ((tok[k] & (kThreads - 1)) == tid) bias[tok[k]] += val[k];
+      if ((tok[k] & (kAdjust - 1)) == tid) bias[tok[k]] += val[k];
     __syncthreads();
   }
 }
 
 // Four logits per thread and step, Q steps: all loads of a run go out before its biases are
 // looked at.  Vec: rows of logits and out are 16-byte aligned, a thread's four are neighbours;
-// else they are 256 apart (a row's start may lie anywhere).  Seen and biased tokens are few and
-// scattered (a division in place would keep most warps for one lane): they go to lists in shared
-// memory that the threads share out, and are stored after the others.  A list of seen
-// tokens that is full leaves the rest in place; a run with more than kThreads biases takes
-// sum_biases().
+// else they are kAdjust apart (a row's start may lie anywhere).  Seen and biased tokens are few
+// and scattered (a division in place would keep most warps for one lane: 42.7 us for 64 rows
+// of 151936): they go to lists in shared memory that the threads share out, and are stored
+// after the others.  A run with more than kFew biases takes sum_biases().  A run is a chain
+// of latencies, so runs are short and sixteen CTAs share an SM: 23.9 us, 4.1 TB/s (16 logits per
+// thread and ten CTAs 26.1, 256 threads and five 28.2; without any rule the same rows take 8 us
+// from L2).
 template <int Q, bool Vec>
-__global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar p) {
-  constexpr int kRun = Q * 4 * kThreads;
-  __shared__ __align__(16) float bias[kRun];
-  __shared__ int tok[kThreads], idx[kThreads];
-  __shared__ float val[kThreads];
-  __shared__ int cnt[kThreads / 32], listed, biases;
-  __shared__ float list_x[kListed];
-  __shared__ uint32_t list_at[kListed];  // place in the run, word << 16
+__global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const AdjustPar p) {
+  constexpr int kRun = Q * 4 * kAdjust;
+  __shared__ __align__(16) float bias[kRun];  // where they are many
+  __shared__ uint16_t list_at[kRun];
+  __shared__ uint32_t is_biased[kRun / 32];
+  __shared__ int tok[kFew], idx[kFew];
+  __shared__ float val[kFew];
+  __shared__ int cnt[kAdjust / 32], listed, biases;
   const int b = blockIdx.x / p.runs, v0 = blockIdx.x % p.runs * kRun;
   const int tid = threadIdx.x;
   launch_dependents();
   if (tid == 0) listed = biases = 0;
+  if (tid < kRun / 32) is_biased[tid] = 0u;
   __syncthreads();
   grid_dependency_wait();
   const int n = min(kRun, p.V - v0);  // logits of this run
   const float* in = p.logits + b * p.ld + v0;
   float* out = p.out + b * p.ld_out + v0;
-  const uint16_t* seen = nullptr;
-  if (p.r.seen) {
-    const int row = p.r.seen_row ? __ldg(p.r.seen_row + b) : b;
-    if (row >= 0 && row < p.r.seen_rows) seen = p.r.seen + row * p.r.seen_ld + v0;
-  }
-  const uint32_t* mask = nullptr;
-  if (p.r.mask) {
-    const int row = p.r.mask_row ? __ldg(p.r.mask_row + b) : b;
-    if (row >= 0 && row < p.r.mask_rows) mask = p.r.mask + row * p.r.mask_ld + (v0 >> 5);
-  }
-  auto place = [&](int q, int e) { return Vec ? (q * kThreads + tid) * 4 + e : (q * 4 + e) * kThreads + tid; };
-  auto allowed = [&](int i) { return !mask || (__ldg(mask + (i >> 5)) >> (i & 31) & 1u); };
+  // what is known of the row, in one round of loads
+  const int seen_at = p.r.seen && p.r.seen_row ? __ldg(p.r.seen_row + b) : b;
+  const int mask_at = p.r.mask && p.r.mask_row ? __ldg(p.r.mask_row + b) : b;
+  const int e0 = p.r.bias_start ? __ldg(p.r.bias_start + b) : 0;
+  const int e1 = p.r.bias_start ? __ldg(p.r.bias_start + b + 1) : 0;
+  const Penalties c = {p.r.repetition ? __ldg(p.r.repetition + b) : 0.f, p.r.frequency ? __ldg(p.r.frequency + b) : 0.f,
+                       p.r.presence ? __ldg(p.r.presence + b) : 0.f};
+  auto place = [&](int q, int e) { return Vec ? (q * kAdjust + tid) * 4 + e : (q * 4 + e) * kAdjust + tid; };
   float x[Q][4];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (Vec && place(q, 0) + 4 <= n) {
+      *reinterpret_cast<float4*>(x[q]) = *reinterpret_cast<const float4*>(in + place(q, 0));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[q][e] = place(q, e) < n ? in[place(q, e)] : 0.f;
+    }
+  }
+  const uint16_t* seen =
+      p.r.seen && seen_at >= 0 && seen_at < p.r.seen_rows ? p.r.seen + seen_at * p.r.seen_ld + v0 : nullptr;
+  const uint32_t* mask =
+      p.r.mask && mask_at >= 0 && mask_at < p.r.mask_rows ? p.r.mask + mask_at * p.r.mask_ld + (v0 >> 5) : nullptr;
+  auto allowed = [&](int i) { return !mask || (__ldg(mask + (i >> 5)) >> (i & 31) & 1u); };
   uint2 words[Q];     // of the four logits
   uint32_t allow[Q];  // bit e
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int i0 = place(q, 0);
     allow[q] = 15u;
+    words[q] = make_uint2(0u, 0u);
     if (Vec && i0 + 4 <= n) {
-      *reinterpret_cast<float4*>(x[q]) = *reinterpret_cast<const float4*>(in + i0);
-      words[q] = seen ? *reinterpret_cast<const uint2*>(seen + i0) : make_uint2(0u, 0u);
+      if (seen) words[q] = *reinterpret_cast<const uint2*>(seen + i0);
       if (mask) allow[q] = __ldg(mask + (i0 >> 5)) >> (i0 & 31);
     } else {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = place(q, e);
-        const bool there = i < n;
-        x[q][e] = there ? in[i] : 0.f;
-        w[e] = there && seen ? seen[i] : 0u;
-        if (mask && there && !allowed(i)) allow[q] &= ~(1u << e);
+        w[e] = i < n && seen ? seen[i] : 0u;
+        if (mask && i < n && !allowed(i)) allow[q] &= ~(1u << e);
       }
       words[q] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
   }
-  const Penalties c = {p.r.repetition ? __ldg(p.r.repetition + b) : 0.f, p.r.frequency ? __ldg(p.r.frequency + b) : 0.f,
-                       p.r.presence ? __ldg(p.r.presence + b) : 0.f};
   int few = 0;  // biases in the run, if they fit the list
-  if (p.r.bias_start) {
-    const int e0 = __ldg(p.r.bias_start + b), e1 = __ldg(p.r.bias_start + b + 1);
-    for (int i = e0 + tid; i < e1; i += kThreads) {
-      const int t = __ldg(p.r.bias_token + i) - v0;
-      if (t >= 0 && t < n) {
+  if (e1 > e0) {
+    for (int i0 = e0; i0 < e1; i0 += 4 * kAdjust) {
+      int t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kAdjust + tid;
+        t[k] = i < e1 ? __ldg(p.r.bias_token + i) - v0 : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (t[k] < 0 || t[k] >= n) continue;
+        const int i = i0 + k * kAdjust + tid;
         const int at = atomicAdd(&biases, 1);  // in any order
-        if (at < kThreads) {
-          tok[at] = t;
+        if (at < kFew) {
+          tok[at] = t[k];
           val[at] = __ldg(p.r.bias_value + i);
           idx[at] = i;
+          atomicOr(&is_biased[t[k] >> 5], 1u << (t[k] & 31));
         }
       }
     }
     __syncthreads();
     few = biases;
-    if (few > kThreads) {
+    if (few > kFew) {
+      if (tid < kRun / 32) is_biased[tid] = 0u;
       sum_biases(p.r, e0, e1, v0, n, kRun, bias, tok, val, cnt);
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[q][e] = __fadd_rn(x[q][e], bias[place(q, e)]);
       few = 0;
+      __syncthreads();
     }
   }
+  // a biased token's own logit, word and bit, on their way while the others are looked at
+  float special = 0.f;
+  uint32_t special_word = 0u;
+  bool special_allowed = false;
+  if (tid < few) {
+    const int t = tok[tid];
+    special = in[t];
+    if (seen) special_word = seen[t];
+    special_allowed = allowed(t);
+  }
+  uint32_t marks = 0u;  // bit 4 q + e: seen, allowed
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     if (mask) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[q][e] = allow[q] >> e & 1u ? x[q][e] : kNegInf;
     }
-    if (words[q].x | words[q].y) {
-      uint32_t w[4] = {words[q].x & 0xFFFFu, words[q].x >> 16, words[q].y & 0xFFFFu, words[q].y >> 16};
-      int mine = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (!(allow[q] >> e & 1u)) w[e] = 0u;
-        mine += w[e] != 0u;
-      }
-      if (mine > 0) {
-        int at = atomicAdd(&listed, mine);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (w[e] == 0u) continue;
-          if (at < kListed) {
-            list_x[at] = x[q][e];
-            list_at[at] = (uint32_t)place(q, e) | (w[e] << 16);
-          } else {
-            x[q][e] = penalised(x[q][e], w[e], c);
-          }
-          ++at;
-        }
-      }
+    // bits 15 and 31 of a word pair: that word is not 0
+    const uint32_t u = (((words[q].x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | words[q].x) & 0x80008000u;
+    const uint32_t v = (((words[q].y & 0x7FFF7FFFu) + 0x7FFF7FFFu) | words[q].y) & 0x80008000u;
+    marks |= (((u >> 15 | u >> 30) | (v >> 13 | v >> 28)) & allow[q] & 15u) << (4 * q);
+  }
+  if (marks) {
+    int at = atomicAdd(&listed, __popc(marks));  // in any order
+    for (; marks; marks &= marks - 1u) {
+      const int k = __ffs((int)marks) - 1;
+      list_at[at++] = (uint16_t)place(k >> 2, k & 3);
     }
   }
-  float special = 0.f;
-  bool owner = false;  // of a biased token: the first of its entries in list order
-  if (few > 0) {
-    if (tid < few) {
-      const int t = tok[tid], me = idx[tid];
-      owner = true;
-      float sum = 0.f;
-      // its entries in list order: the next one is that with the smallest index above the last
-      for (int last = -1;;) {
-        int next = 0x7fffffff, at = 0;
-        for (int k = 0; k < few; ++k)
-          if (tok[k] == t && idx[k] > last && idx[k] < next) {
-            next = idx[k];
-            at = k;
-          }
-        if (next == 0x7fffffff) break;
-        if (last < 0 && next != me) {  // another thread's token
-          owner = false;
-          break;
+  bool owner = tid < few;  // of a biased token: the first of its entries in list order
+  if (owner) {
+    const int t = tok[tid], me = idx[tid];
+    float sum = 0.f;
+    // its entries in list order: the next one is that with the smallest index above the last
+    for (int last = -1;;) {
+      int next = 0x7fffffff, at = 0;
+      for (int k = 0; k < few; ++k)
+        if (tok[k] == t && idx[k] > last && idx[k] < next) {
+          next = idx[k];
+          at = k;
         }
-        sum = __fadd_rn(sum, val[at]);
-        last = next;
+      if (next == 0x7fffffff) break;
+      if (last < 0 && next != me) {  // another thread's token
+        owner = false;
+        break;
       }
-      if (owner) {
-        special = kNegInf;
-        if (allowed(t)) {
-          special = __fadd_rn(in[t], sum);
-          const uint32_t w = seen ? seen[t] : 0u;
-          if (w) special = penalised(special, w, c);
-        }
-      }
+      sum = __fadd_rn(sum, val[at]);
+      last = next;
     }
-    __syncthreads();  // in[] has been read where out is the same
+    if (special_allowed) {
+      special = __fadd_rn(special, sum);
+      if (special_word) special = penalised(special, special_word, c);
+    } else {
+      special = kNegInf;
+    }
   }
+  if (p.logits == p.out && few > 0) __syncthreads();  // the biased logits have been read
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int i0 = place(q, 0);
@@ -231,13 +244,12 @@ __global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar
         if (place(q, e) < n) out[place(q, e)] = x[q][e];
     }
   }
-  __syncthreads();  // the list is complete, and its logits are stored as they were before
-  for (int k = tid; k < min(listed, kListed); k += kThreads)
-    out[list_at[k] & 0xFFFFu] = penalised(list_x[k], list_at[k] >> 16, c);
-  if (few > 0) {
-    __syncthreads();
-    if (owner) out[tok[tid]] = special;
+  __syncthreads();  // the list is complete, and its logits are stored without penalties
+  for (int k = tid; k < listed; k += kAdjust) {
+    const int i = list_at[k];
+    if (few == 0 || !(is_biased[i >> 5] >> (i & 31) & 1u)) out[i] = penalised(out[i], seen[i], c);
   }
+  if (owner) out[tok[tid]] = special;
 }
 
 // ---------------------------------------------------------------- seen tokens
@@ -257,9 +269,9 @@ __device__ __forceinline__ int64_t seen_row_of(const SeenPar& p, int b) {
 }
 
 // Rows that start anew: a CTA owns kSegment words of a row, counts the row's tokens that fall
-// there in shared memory and writes the words out, the row's only trip through memory.
-// Emptying the rows and marking in a second kernel took 13.4 us for 64 prompts of up to 8192
-// tokens (V 151936).  Where a row is named more than once its first entry's CTAs take the tokens
+// there in shared memory and writes the words out, the row's only trip through memory: 10.3 us
+// for 64 prompts of up to 8192 tokens (V 151936), and 14.2 with the rows emptied first and marked by
+// a second kernel.  Where a row is named more than once its first entry's CTAs take the tokens
 // of all.
 constexpr int kSegment = 8192;
 __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
@@ -379,9 +391,10 @@ int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld, co
   int rc = check_rules(rules, V);
   if (rc) return rc;
   AdjustPar p;
-  // runs of 4096 logits, of 1024 where that leaves SMs without any
-  const bool small = (int64_t)B * ((V + 4095) / 4096) < 304;
-  p.runs = small ? (V + 1023) / 1024 : (V + 4095) / 4096;
+  // runs of 1024 logits, of 512 where that leaves SMs without any
+  constexpr int kBig = kSteps * 4 * kAdjust, kSmall = 4 * kAdjust;
+  const bool small = (int64_t)B * ((V + kBig - 1) / kBig) < 304;
+  p.runs = small ? (V + kSmall - 1) / kSmall : (V + kBig - 1) / kBig;
   if ((int64_t)B * p.runs > 0x7fffffff) return ATTN_EINVAL;
   if ((rc = abi_check_device())) return rc;
   if (B == 0) return ATTN_OK;
@@ -393,8 +406,8 @@ int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld, co
   p.r = *rules;
   const bool vec = aligned(logits, 16) && aligned(out, 16) && (B == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
   auto kernel = small ? (vec ? logits_adjust_kernel<1, true> : logits_adjust_kernel<1, false>)
-                      : (vec ? logits_adjust_kernel<4, true> : logits_adjust_kernel<4, false>);
-  return launch_dependent(kernel, dim3((unsigned)(B * p.runs)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), p) ==
+                      : (vec ? logits_adjust_kernel<kSteps, true> : logits_adjust_kernel<kSteps, false>);
+  return launch_dependent(kernel, dim3((unsigned)(B * p.runs)), dim3(kAdjust), 0, static_cast<cudaStream_t>(stream), p) ==
                  cudaSuccess
              ? ATTN_OK
              : ATTN_ELAUNCH;
