@@ -600,9 +600,10 @@ def _requests(cu_seqlens, kv: KVCache, n=None):
 
 
 def _prepared_q(cfg: AttnConfig, q, kv: KVCache):
-    """The address of a prepared Q [N, Hq, D] for this cache, and N."""
-    want = torch.bfloat16 if kv.kv_dtype == ATTN_KV_BF16 else torch.float16
-    assert q.dtype == want and q.is_cuda and q.is_contiguous(), "q"
+    """The address of a prepared Q [N, Hq, D] for this cache, and N.  Next to codes it holds
+    f16 values, also where the tensor is the bf16 one that prefill_prepare takes."""
+    assert q.dtype == torch.bfloat16 or (q.dtype == torch.float16 and kv.kv_dtype != ATTN_KV_BF16), "q"
+    assert q.is_cuda and q.is_contiguous(), "q"
     N, H, D = q.shape
     assert H == cfg.num_q_heads and D == cfg.head_dim, "q"
     return q.data_ptr(), N

@@ -386,7 +386,7 @@ extern "C" {
 
 int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld, const attn_logits_rules_t* rules,
                        float* out, int64_t ld_out, void* stream) {
-  if (!logits || !rules || !out || !aligned(logits, 4) || !aligned(out, 4)) return ATTN_EINVAL;
+  if (!rules || (B != 0 && (!logits || !out)) || !aligned(logits, 4) || !aligned(out, 4)) return ATTN_EINVAL;
   if (B < 0 || V < 1 || V > (1 << 23) || ld < V || ld_out < V || (logits == out && ld != ld_out)) return ATTN_EINVAL;
   int rc = check_rules(rules, V);
   if (rc) return rc;

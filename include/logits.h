@@ -56,11 +56,10 @@ typedef struct attn_logits_rules {
 /* out [B, ld_out] (fp32) = the rules applied to logits [B, ld], V logits per row; out
  * may be logits itself with ld_out == ld (else the two must not overlap).  A row
  * whose mask allows nothing comes out as -inf throughout (attn_sample_tokens wants one
- * finite logit).  ATTN_EINVAL: NULL logits, rules or out, B < 0, V < 1, V > 2^23,
- * ld or ld_out < V, out == logits with another ld, a misaligned pointer, a table or
- * mask with a row shorter than V or no rows, seen_ld not a multiple of 8,
- * bias_start without bias_token and bias_value, a table without any penalty's
- * array is allowed. */
+ * finite logit).  ATTN_EINVAL: NULL rules, NULL logits or out with B != 0, B < 0, V < 1,
+ * V > 2^23, ld or ld_out < V, out == logits with another ld, a misaligned pointer, a table
+ * or mask with a row shorter than V or without rows, seen_ld not a multiple of 8,
+ * bias_start without bias_token and bias_value. */
 ATTN_API int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld,
                                 const attn_logits_rules_t* rules, float* out, int64_t ld_out, void* stream);
 
@@ -69,7 +68,7 @@ ATTN_API int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64
  * (NULL: b).  Without ATTN_SEEN_PROMPT the generated counts rise by one per token
  * listed, with it the prompt bit is set.  ATTN_SEEN_CLEAR empties the rows of the
  * call first.  Rows outside [0, num_rows) and tokens outside [0, V) are skipped; a row
- * may be named more than once.  ATTN_EINVAL: NULL seen or tokens, negative sizes,
+ * may be named more than once.  ATTN_EINVAL: NULL seen, NULL tokens with N != 0, negative sizes,
  * V < 1, V > 2^23, ld < V or not a multiple of 8, num_rows < 1, a misaligned
  * pointer, cu_seqlens NULL with N != B, other flags. */
 ATTN_API int attn_tokens_seen(uint16_t* seen, int64_t ld, int32_t num_rows, int32_t V, const int32_t* rows,

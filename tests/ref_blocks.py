@@ -173,7 +173,7 @@ class Cache:
         self.kv = attn.KVCache(k.cuda(), v.cuda(), torch.tensor(base).cuda(), i32(cached), i32(cap),
                                None if table is None else i32(table), page, K_SCALE, V_SCALE,
                                *[None if s is None else s.cuda() for s in scales])
-        self.bounds = torch.full((c["rows"], hkv, 2, d), 777.0, dtype=torch.bfloat16).cuda()
+        self.bounds = torch.full((c["rows"], hkv, 2, d), 776.0, dtype=torch.bfloat16).cuda()
         self.blocks = attn.BlockBounds(self.bounds, block, None if row_base is None else torch.tensor(row_base).cuda())
         self.N = sum(new)
         self.cu = i32(np.concatenate(([0], np.cumsum(new))))
