@@ -108,11 +108,12 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
   const int b = Blocks ? blockIdx.x / p.max_splits : blockIdx.z;
-  launch_dependents();  // the merge kernel may be scheduled as CTAs finish
+  if (!Blocks) launch_dependents();  // the merge kernel may be scheduled as CTAs finish
   ReqInfo r;
   int k0 = 0, k1, n_splits;
   if constexpr (Blocks) {
     grid_dependency_wait();  // the list
+    launch_dependents();  // behind the wait: a decode kernel reads the lengths before its own
     if (!blocks_begin(p, split, kh, b, s_block, &s_count, &r, &k1)) return;
     n_splits = p.max_splits;
   } else {

@@ -5,6 +5,8 @@
 // 4 bytes read and 4 written per logit, 2 of the table, an eighth of a byte of the mask.
 // A CTA takes a run of one row and filters the row's biases, few and in any order, for it;
 // those of one token are summed by one thread in list order (the order decides the rounding).
+//
+// Dependents start only behind these kernels' own wait (see blocks.cu).
 #include "kernels.cuh"
 #include "../../include/logits.h"
 
@@ -89,11 +91,11 @@ __global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const Adjust
   __shared__ int cnt[kAdjust / 32], listed, biases;
   const int b = blockIdx.x / p.runs, v0 = blockIdx.x % p.runs * kRun;
   const int tid = threadIdx.x;
-  launch_dependents();
   if (tid == 0) listed = biases = 0;
   if (tid < kRun / 32) is_biased[tid] = 0u;
   __syncthreads();
   grid_dependency_wait();
+  launch_dependents();
   const int n = min(kRun, p.V - v0);  // logits of this run
   const float* in = p.logits + b * p.ld + v0;
   float* out = p.out + b * p.ld_out + v0;
@@ -278,41 +280,39 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
   __shared__ __align__(16) uint32_t count[kSegment];
   const int b = blockIdx.x / p.parts, v0 = blockIdx.x % p.parts * kSegment;
   const int tid = threadIdx.x;
-  launch_dependents();
   grid_dependency_wait();
+  launch_dependents();
   const int64_t row = seen_row_of(p, b);
+  int t0 = b, t1 = min(b + 1, p.N);
+  if (p.cu_seqlens) {
+    t0 = max(__ldg(p.cu_seqlens + b), 0);
+    t1 = min(__ldg(p.cu_seqlens + b + 1), p.N);
+  }
   if (row < 0) return;
-  bool before = false;
+  bool before = false, after = false;  // other entries with this row
   if (p.rows)
-    for (int i = tid; i < b; i += kThreads) before |= __ldg(p.rows + i) == row;
+    for (int i = tid; i < p.B; i += kThreads) {
+      const bool same = __ldg(p.rows + i) == row;
+      before |= same && i < b;
+      after |= same && i > b;
+    }
   for (int i = tid; i < kSegment / 4; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
   if (__syncthreads_or(before)) return;
-  for (int i = b; i < p.B; ++i) {
-    if (i > b) {  // the next entry with this row
-      if (!p.rows) break;
-      int next = p.B;
-      for (int k0 = i; k0 < p.B && next == p.B; k0 += kThreads) {
-        const bool same = k0 + tid < p.B && __ldg(p.rows + k0 + tid) == row;
-        __shared__ int first;
-        if (tid == 0) first = p.B;
-        __syncthreads();
-        if (same) atomicMin(&first, k0 + tid);
-        __syncthreads();
-        next = first;
-        __syncthreads();
-      }
-      i = next;
-      if (i >= p.B) break;
-    }
-    int t0 = i, t1 = min(i + 1, p.N);
-    if (p.cu_seqlens) {
-      t0 = max(__ldg(p.cu_seqlens + i), 0);
-      t1 = min(__ldg(p.cu_seqlens + i + 1), p.N);
-    }
+  const bool again = __syncthreads_or(after);
+  for (int i = b;;) {
 #pragma unroll 8
     for (int t = t0 + tid; t < t1; t += kThreads) {
       const int v = __ldg(p.tokens + t);
       if (v >= 0 && v < p.V && v >= v0 && v < v0 + kSegment) atomicAdd(&count[v - v0], 1u);
+    }
+    if (!again) break;
+    do ++i; while (i < p.B && __ldg(p.rows + i) != row);  // the next one, the same for every thread
+    if (i >= p.B) break;
+    t0 = i;
+    t1 = min(i + 1, p.N);
+    if (p.cu_seqlens) {
+      t0 = max(__ldg(p.cu_seqlens + i), 0);
+      t1 = min(__ldg(p.cu_seqlens + i + 1), p.N);
     }
   }
   __syncthreads();
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
 }
 
 __global__ void __launch_bounds__(kThreads) seen_mark_kernel(const SeenPar p) {
-  launch_dependents();
   grid_dependency_wait();
+  launch_dependents();
   const int t = blockIdx.x * kThreads + threadIdx.x;
   if (t >= p.N) return;
   int b = t;
