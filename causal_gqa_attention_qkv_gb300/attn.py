@@ -603,7 +603,7 @@ def _prepared_q(cfg: AttnConfig, q, kv: KVCache):
     """The address of a prepared Q [N, Hq, D] for this cache, and N.  Next to codes it holds
     f16 values, also where the tensor is the bf16 one that prefill_prepare takes."""
     assert q.dtype == torch.bfloat16 or (q.dtype == torch.float16 and kv.kv_dtype != ATTN_KV_BF16), "q"
-    assert q.is_cuda and q.is_contiguous(), "q"
+    assert q.is_cuda and q.is_contiguous() and q.dim() == 3, "q"
     N, H, D = q.shape
     assert H == cfg.num_q_heads and D == cfg.head_dim, "q"
     return q.data_ptr(), N
@@ -629,6 +629,7 @@ def block_select(cfg: AttnConfig, q, cu_seqlens, max_kv_len: int, kv: KVCache, b
     behind them.  q: the prepared Q [N, Hq, D] of prefill_prepare."""
     qp, N = _prepared_q(cfg, q, kv)
     cu, B = _requests(cu_seqlens, kv, N)
+    assert out_list.dim() == 3, "out_list"
     n, H, keep = out_list.shape
     assert n == N and H == cfg.num_kv_heads, "out_list"
     s, k = kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
@@ -642,6 +643,7 @@ def block_attend(cfg: AttnConfig, q, cu_seqlens, kv: KVCache, block_size: int, b
     ``block_list`` (int32 [N, Hkv, keep]) into ``out`` (bf16 [N, Hq*D])."""
     qp, N = _prepared_q(cfg, q, kv)
     cu, B = _requests(cu_seqlens, kv, N)
+    assert block_list.dim() == 3, "block_list"
     n, H, keep = block_list.shape
     assert n == N and H == cfg.num_kv_heads, "block_list"
     assert out.numel() >= q.numel(), "out"
@@ -723,17 +725,25 @@ class LogitsRules:
                                0 if m is None else m.shape[1], 0 if m is None else m.shape[0], _ptr(self.mask_row))
 
 
+def _rows_f32(t, B, V) -> int:
+    """The row stride of fp32 rows on the device."""
+    ld, inner = t.stride()
+    assert t.dtype == torch.float32 and t.is_cuda and (inner == 1 or V <= 1), "logits"
+    return ld if B > 1 else V
+
+
 def logits_adjust(logits, rules: LogitsRules, out=None, stream=None):
     """The rules applied to fp32 logits [B, V] (rows may be strided), into ``out``
     (None: in place).  Returns the tensor written."""
-    if out is None:
-        out = logits
-    for t in (logits, out):
-        assert t.dtype == torch.float32 and t.is_cuda and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "logits"
+    assert logits.dim() == 2, "logits"
     B, V = logits.shape
-    assert out.shape == logits.shape, "out"
-    lds = [t.stride(0) if B > 1 else V for t in (logits, out)]
-    _check(load().attn_logits_adjust(_ptr(logits), B, V, lds[0], ctypes.byref(rules.struct(B)), _ptr(out), lds[1],
+    ld = _rows_f32(logits, B, V)
+    if out is None or out is logits:
+        out, ld_out = logits, ld
+    else:
+        assert out.shape == logits.shape, "out"
+        ld_out = _rows_f32(out, B, V)
+    _check(load().attn_logits_adjust(logits.data_ptr(), B, V, ld, ctypes.byref(rules.struct(B)), out.data_ptr(), ld_out,
                                      _stream(stream)))
     return out
 

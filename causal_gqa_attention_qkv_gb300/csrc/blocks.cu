@@ -136,13 +136,14 @@ __device__ __forceinline__ uint32_t higher(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// One warp per (block, KV head), a lane 16 bytes of a key, 8 loads (or those of 64 keys) in flight.
+// One warp per (block, KV head), a lane 16 bytes of a key, 16 loads (or those of 64 keys) in
+// flight: 32768 bf16 tokens (Hkv 8, D 128) 13.8 us, 5.0 TB/s (8 loads 14.8, 32 loads 17.3).
 template <int D, int KV>
-__global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BlocksPar p) {
+__global__ void __launch_bounds__(kThreads, 2) block_bounds_kernel(const BlocksPar p) {
   constexpr bool F16 = KV != ATTN_KV_BF16;
   constexpr int kBytes = KV == ATTN_KV_BF16 ? 2 * D : KV == ATTN_KV_E4M3 ? D : D / 2;  // of a key
   constexpr int L = kBytes / 16, KPW = 32 / L;   // lanes per key, keys per warp and load
-  constexpr int U = 64 / KPW < 8 ? 64 / KPW : 8;
+  constexpr int U = 64 / KPW < 16 ? 64 / KPW : 16;
   constexpr int P = Chunk<KV>::kPairs;
   const int b = blockIdx.x / p.ctas_per_request, part = blockIdx.x % p.ctas_per_request;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -947,7 +948,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
 // together (lengths, q, page numbers, then the bounds), scores are pushed rather than fetched,
 // and the other CTAs leave when theirs have arrived.
 template <int D>
-__global__ void __launch_bounds__(kThreads) block_pick_kernel(const BlocksPar p) {
+__global__ void __launch_bounds__(kThreads, 4) block_pick_kernel(const BlocksPar p) {
   __shared__ SelectSmem<D> sm;
   __shared__ __align__(16) float coef[2 * D];
   __shared__ uint32_t bits[kHeldAll / 32];
@@ -1142,7 +1143,7 @@ int attn_block_bounds(const attn_config_t* cfg, const attn_kv_t* kv, const attn_
   p.k_block_scale = static_cast<const uint8_t*>(c.k_block_scale);
   p.k_scale = c.k_scale;
   // how many blocks become full is on the device: a grid that fills the card walks them
-  p.ctas_per_request = std::max(1, std::min(4096, 1216 / B));
+  p.ctas_per_request = std::max(1, 608 / B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cfg->head_dim == 128 ? launch_bounds_d<128>(p, c.kv_dtype, s) : launch_bounds_d<64>(p, c.kv_dtype, s);
 }
