@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   uint64_t* empty = full + S;
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
-  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_count;
+  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_slot[Blocks ? kMaxSplitBlocks : 1], s_count;
 
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
@@ -162,12 +162,12 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   if constexpr (Blocks) {
     grid_dependency_wait();  // the list
     launch_dependents();  // behind the wait: a decode kernel reads the lengths before its own
-    if (!blocks_begin(p, split, kh, b, s_block, &s_count, &r, &k1)) return;
+    if (!blocks_begin(p, split, kh, b, s_block, s_slot, &s_count, &r, &k1)) return;
     n_splits = p.max_splits;
   } else {
     if (!decode_begin<D, ATTN_KV_E2M1, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
   }
-  Tiles<Blocks> tiles{k0, s_block, p.log2_bs - 6, 0};
+  Tiles<Blocks> tiles{k0, s_block, s_slot, p.log2_bs - 6, 0};
   tiles.n = Blocks ? s_count << tiles.sh : (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
   const int npass = (tiles.n + 1) / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     const int ntiles = tiles.n;
     // A page outside the cache reads as zeros; its scales are not read.
     auto tile_slot = [&](int t) -> int64_t {
+      if constexpr (Blocks) return t < ntiles ? tiles.slot(t) : 0;
       return t < ntiles ? cache_slot(p.kv, r, tiles.pos(t, 0), -kKeysPerTile) : 0;
     };
     int w0 = 0;
