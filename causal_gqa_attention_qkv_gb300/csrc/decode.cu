@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   __shared__ int s_abort;       // written by the producer only
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
-  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_slot[Blocks ? kMaxSplitBlocks : 1], s_count;
+  __shared__ SplitBlocks<Blocks> s_list;
 
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
@@ -114,14 +114,13 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   if constexpr (Blocks) {
     grid_dependency_wait();  // the list
     launch_dependents();  // behind the wait: a decode kernel reads the lengths before its own
-    if (!blocks_begin(p, split, kh, b, s_block, s_slot, &s_count, &r, &k1)) return;
+    if (!blocks_begin(p, split, kh, b, s_list, &r, &k1)) return;
     n_splits = p.max_splits;
   } else {
     if (!decode_begin<D, KV, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
   }
   const bool append = !Blocks && p.k_norm_w != nullptr;
-  Tiles<Blocks> tiles{k0, s_block, s_slot, p.log2_bs - 6, 0};
-  tiles.n = Blocks ? s_count << tiles.sh : (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
+  const Tiles<Blocks> tiles = split_tiles<Blocks>(p, s_list, k0, k1);
   const int ntiles = tiles.n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -154,8 +153,13 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         uint8_t* kt = smem + st * Lay::kStageBytes;
         uint8_t* vt = kt + Lay::kTileBytes;
         // a 64-key tile lies in one page; a page outside the cache reads as zeros
-        const int64_t slot = Blocks ? tiles.slot(i) : cache_slot(p.kv, r, tiles.pos(i, 0), -kKeysPerTile);
-        if (!Blocks && slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
+        int64_t slot;
+        if constexpr (Blocks) {
+          slot = tiles.slot(i);
+        } else {
+          slot = cache_slot(p.kv, r, tiles.pos(i, 0), -kKeysPerTile);
+          if (slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
+        }
 #pragma unroll
         for (int rg = 0; rg < Lay::kRegions; ++rg) {  // x: 64 bf16 (128 B) per box, or 0
           tma_load_3d(kt + rg * Lay::kRegionBytes, &kmap, &full[st], rg * 64, kh, (int)slot);

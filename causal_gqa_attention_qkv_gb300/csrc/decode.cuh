@@ -44,24 +44,37 @@ struct DecodePar {
 
 constexpr int kMaxSplitBlocks = 1024;  // entries of a list that one split may take
 
-// The tiles of 64 keys of a split: consecutive from k0, or those of listed blocks.
+// What a split over listed blocks keeps of them in shared memory: the blocks that hold a
+// visible key and their first slots.
+template <bool Blocks>
+struct SplitBlocks {};
+template <>
+struct SplitBlocks<true> {
+  int block[kMaxSplitBlocks], slot[kMaxSplitBlocks], count;
+};
+
+// The tiles of 64 keys of a split: consecutive from k0 ...
 template <bool Blocks>
 struct Tiles {
-  int k0;            // consecutive
-  const int* block;  // listed (shared memory): the blocks and their first slots
-  const int* slots;
-  int sh;            // log2 of the tiles per block
+  int k0, n;
+  // First position of tile i.
+  __device__ __forceinline__ int pos(int i, int) const { return k0 + i * kKeysPerTile; }
+};
+// ... or those of listed blocks.
+template <>
+struct Tiles<true> {
+  const SplitBlocks<true>& list;
+  int sh;  // log2 of the tiles per block
   int n;
-  // First slot of listed tile i < n, -64 for a page outside the cache.
-  __device__ __forceinline__ int slot(int i) const {
-    const int s = slots[i >> sh];
-    return s < 0 ? -kKeysPerTile : s + ((i & ((1 << sh) - 1)) << 6);
-  }
   // First position of tile i; of a tile past the last (one that was not loaded) `past`.
   __device__ __forceinline__ int pos(int i, int past) const {
-    if constexpr (!Blocks) return k0 + i * kKeysPerTile;
     if (i >= n) return past;
-    return (block[i >> sh] << (sh + 6)) + ((i & ((1 << sh) - 1)) << 6);
+    return (list.block[i >> sh] << (sh + 6)) + ((i & ((1 << sh) - 1)) << 6);
+  }
+  // First slot of tile i < n, -64 for a page outside the cache.
+  __device__ __forceinline__ int slot(int i) const {
+    const int s = list.slot[i >> sh];
+    return s < 0 ? -kKeysPerTile : s + ((i & ((1 << sh) - 1)) << 6);
   }
 };
 
@@ -140,6 +153,13 @@ __device__ __forceinline__ void append_new_kv(const DecodePar& p, const ReqInfo&
   __syncwarp();
 }
 
+// The tiles of a split, which decode_begin() or blocks_begin() has set out.
+template <bool Blocks>
+__device__ __forceinline__ Tiles<Blocks> split_tiles(const DecodePar& p, const SplitBlocks<Blocks>& list, int k0, int k1) {
+  if constexpr (Blocks) return Tiles<true>{list, p.log2_bs - 6, list.count << (p.log2_bs - 6)};
+  else return Tiles<false>{k0, (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile};
+}
+
 // The part of request b's keys that split `split` takes, [k0, k1), and how many
 // splits the request spans; false: nothing to do (a request that is skipped, or
 // past the host bound, whose new K/V are still appended).
@@ -177,11 +197,11 @@ __device__ __forceinline__ bool decode_begin(const DecodePar& p, int split, int 
 }
 
 // The same for token t over its listed blocks: the entries of the split that hold a
-// visible key go to `block` (shared memory, kMaxSplitBlocks), their first slots to `slots` (no
-// page-table read stands before a tile's load then: one token over 65000 keys 9.0 -> 8.6 us),
-// *count of them; k1 is the end of the visible positions.  False: a token without output.
-__device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int kh, int t, int* block, int* slots,
-                                             int* count, ReqInfo* req, int* k1) {
+// visible key go to `mine` with their first slots (no page-table read stands before a tile's load
+// then: one token over 65000 keys 9.0 -> 8.6 us); k1 is the end of the visible positions.
+// False: a token without output.
+__device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int kh, int t, SplitBlocks<true>& mine,
+                                             ReqInfo* req, int* k1) {
   const int lane = threadIdx.x & 31;
   const int32_t* list = p.list + ((int64_t)t * p.Hkv + kh) * p.keep;
   const int first = split * p.split_len, e1 = min(first + p.split_len, p.keep);
@@ -206,14 +226,14 @@ __device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int 
       if (live) {
         const int to = at + __popc(all & ((1u << lane) - 1u));
         const int slot = (int)cache_slot(p.kv, r, entry << p.log2_bs);
-        block[to] = entry;
-        slots[to] = slot;
+        mine.block[to] = entry;
+        mine.slot[to] = slot;
         if (slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);
       }
       at += __popc(all);
       entry = e0 + 32 + lane < e1 ? __ldcg(list + e0 + 32 + lane) : -1;
     }
-    if (lane == 0) *count = at;
+    if (lane == 0) mine.count = at;
   }
   __syncthreads();
   *req = r;

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   uint64_t* empty = full + S;
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
-  __shared__ int s_block[Blocks ? kMaxSplitBlocks : 1], s_slot[Blocks ? kMaxSplitBlocks : 1], s_count;
+  __shared__ SplitBlocks<Blocks> s_list;
 
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
@@ -162,14 +162,13 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   if constexpr (Blocks) {
     grid_dependency_wait();  // the list
     launch_dependents();  // behind the wait: a decode kernel reads the lengths before its own
-    if (!blocks_begin(p, split, kh, b, s_block, s_slot, &s_count, &r, &k1)) return;
+    if (!blocks_begin(p, split, kh, b, s_list, &r, &k1)) return;
     n_splits = p.max_splits;
   } else {
     if (!decode_begin<D, ATTN_KV_E2M1, Axes>(p, split, kh, b, &r, &k0, &k1, &n_splits)) return;
   }
-  Tiles<Blocks> tiles{k0, s_block, s_slot, p.log2_bs - 6, 0};
-  tiles.n = Blocks ? s_count << tiles.sh : (k1 - k0 + kKeysPerTile - 1) / kKeysPerTile;
-  const int npass = (tiles.n + 1) / 2;
+  const Tiles<Blocks> tiles = split_tiles<Blocks>(p, s_list, k0, k1);
+  const int npass = Blocks ? (tiles.n + 1) / 2 : (k1 - k0 + 2 * kKeysPerTile - 1) / (2 * kKeysPerTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     // A page outside the cache reads as zeros; its scales are not read.
     auto tile_slot = [&](int t) -> int64_t {
       if constexpr (Blocks) return t < ntiles ? tiles.slot(t) : 0;
-      return t < ntiles ? cache_slot(p.kv, r, tiles.pos(t, 0), -kKeysPerTile) : 0;
+      else return t < ntiles ? cache_slot(p.kv, r, tiles.pos(t, 0), -kKeysPerTile) : 0;
     };
     int w0 = 0;
     int64_t slot_now = tile_slot(lane), slot_next = tile_slot(32 + lane);
@@ -366,13 +365,15 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
         }
       }
     }
-    // the warp's first keys in the halves
-    const int kt[2] = {tiles.pos(2 * i, k1) + warp * 16, tiles.pos(2 * i + 1, k1) + warp * 16};
-    const bool partial = kt[1] + 16 > k1 || (Blocks && kt[0] + 16 > k1);
+    // the warp's first key of the first half, and in either half
+    const int kt0 = Blocks ? tiles.pos(2 * i, k1) + warp * 16 : k0 + i * 2 * kKeysPerTile + warp * 16;
+    const int kt1 = Blocks ? tiles.pos(2 * i + 1, k1) + warp * 16 : kt0 + kKeysPerTile;
+    auto first_key = [&](int t) { return Blocks && t == 1 ? kt1 : kt0 + t * kKeysPerTile; };
+    const bool partial = Blocks ? max(kt0, kt1) + 16 > k1 : kt0 + kKeysPerTile + 16 > k1;
     if (partial) {  // keys past the end: arbitrary bits, no part in the softmax
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = kt[t] + key_g;
+        const int key = first_key(t) + key_g;
         if (key >= k1) s[t][0] = s[t][1] = kNegInf;
         if (key + 8 >= k1) s[t][2] = s[t][3] = kNegInf;
       }
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       if (partial) {  // keys past the end hold arbitrary bits: a scale of 0 makes their entries 0 (codes are finite)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int ka = kt[t] + key_a + 8 * h, kc = kt[t] + key_b + 8 * h;
+          const int ka = first_key(t) + key_a + 8 * h, kc = first_key(t) + key_b + 8 * h;
           if constexpr (Wide) {
             sc[2 * h] &= (ka < k1 ? 0xFFu : 0u) | (kc < k1 ? 0xFF00u : 0u);
           } else {
