@@ -309,11 +309,16 @@ __device__ __forceinline__ Range no_scores() { return {0.f, ~0u, 0u}; }
 // and 5 between lanes, 17 half steps of 2^-24.
 constexpr float kFp32Error = 24.f * 5.9604645e-8f;
 // On the tensor cores: a coefficient is the sum of two bf16 to within 2^-16; products are
-// exact and added with at least fp32's precision in chains of 64, and with any rounding, 2^-23
-// each; then the four chains, the two parts, and the 7 additions in M or P.
-constexpr float kMmaError = 1.52587891e-5f + 80.f * 1.1920929e-7f;
-constexpr float kErrorFloor = 1e-40f;
-constexpr float kSubnormals = 4.8e-38f;  // 4 * 2^-126: a factor that is flushed, or its product
+// exact and added with at least fp32's precision in two chains of 128, and with any rounding,
+// 2^-23 each; then the chains, the two parts, and the 7 additions in M or P.  The sums of
+// magnitudes come the same way, 1.001 for their own rounding.
+constexpr float kMmaError = 1.52587891e-5f + 144.f * 1.1920929e-7f;
+constexpr float kErrorFloor = 1e-37f;
+// There subnormal factors may be flushed, 2^-126 of the other factor each: a magnitude counts as
+// 2^-110 at least (times kMmaError, 2^-125), and what parts of coefficients lose is taken with the
+// largest magnitude.
+constexpr uint32_t kLeast = 0x08800880u;  // a pair of bf16 2^-110
+constexpr float kSubnormals = 2.4e-38f;
 
 // Scores of the blocks [i0, i1) of a request for one token, by the CTA: a warp takes 8 blocks
 // (D = 64: 16) at a time, lane l of the D / 4 lanes of a block holds 8 components of lo (the
@@ -438,14 +443,16 @@ __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, in
 // m16n8k16: row g of A holds the upper, row g + 8 the lower bf16 part of token g's coefficients,
 // a column of B a block.  Which component a k slot holds is free as long as A and B agree: quad
 // member q takes the 16-byte chunks q, q + 4, ... of its block's row, each good for two products.
-// 55 tokens of 12 requests over up to 100000 keys: 37 us with the selection (on the fp32 units, 48).
+// A comes from shared memory, so a warp takes two tiles of 8 blocks for each of its reads (one tile
+// was bound by them).  The sums of magnitudes are a product too: M <= 0 <= P, so they are those of
+// the blocks' largest magnitudes, negated for lo.  55 tokens of 12 requests over up to 100000
+// keys: 33.6 us with the selection (sums on the fp32 units, 48).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
   constexpr int C = D / 16;      // 16-byte chunks of a block's row per lane
   __shared__ __align__(16) float coef[kTokens][2 * D];  // M, P
   __shared__ __align__(16) uint4 frag[2 * C * 32];
-  __shared__ float ceiling[kWarps][2 * D];              // the warps' largest magnitudes
-  __shared__ uint32_t kmin[kTokens], kmax[kTokens];
+  __shared__ uint32_t kmin[kTokens], kmax[kTokens], magnitude[kTokens], huge;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int kh = blockIdx.x / p.chunks % p.Hkv, c = blockIdx.x % p.chunks;
   grid_dependency_wait();
@@ -461,19 +468,37 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
   }
   const int run = min(min(n - j, kTokens), p.N - t);  // tokens past N have no list
   if (t < 0 || run <= 0) return;
+  if (threadIdx.x < kTokens) {
+    kmin[threadIdx.x] = ~0u;
+    kmax[threadIdx.x] = magnitude[threadIdx.x] = 0u;
+    huge = 0u;
+  }
   const ReqInfo r = load_request(p.kv, b, n);
   const int most = r.valid ? ((r.cached + j + run - 1) >> p.log2_bs) + 1 : 0;  // blocks that the last token sees
   const int i0 = p.first + c * p.chunk, i1 = min(min(i0 + p.chunk, most - p.last), p.max_blocks);
   if (most <= p.keep || i0 >= i1) return;
-  for (int i = threadIdx.x; i < kTokens * D; i += kThreads) {
-    float m = 0.f, x = 0.f;
-    if (i / D < run) coefficients(p, t + i / D, kh, D, i % D, &m, &x);
-    coef[i / D][i % D] = m;
-    coef[i / D][D + i % D] = x;
-  }
-  if (threadIdx.x < kTokens) {
-    kmin[threadIdx.x] = ~0u;
-    kmax[threadIdx.x] = 0u;
+  for (int i = threadIdx.x; i < kTokens * (D / 8); i += kThreads) {  // eight components of a token
+    const int k = i / (D / 8), d = i % (D / 8) * 8;
+    float m[8] = {}, x[8] = {};
+    if (k < run) {
+      const uint16_t* row = p.q + ((int64_t)(t + k) * p.Hkv + kh) * p.G * D + d;
+#pragma unroll 8
+      for (int h = 0; h < p.G; ++h) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + h * D));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // as in coefficients()
+          const float y = q_value((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, p.q_f16);
+          m[e] += y > 0.f ? 0.f : y;
+          x[e] += y < 0.f ? 0.f : y;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      coef[k][d + e] = m[e];
+      coef[k][D + d + e] = x[e];
+    }
   }
   __syncthreads();
   // the A operand of each product, as the lanes want it
@@ -482,6 +507,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
     const float4 w = *reinterpret_cast<const float4*>(&coef[tok][8 * (4 * (s >> 1) + (i & 3)) + 4 * (s & 1)]);
     const uint32_t u = pack_bf16(w.x, w.y), v = pack_bf16(w.z, w.w);
     frag[i] = make_uint4(u, bf16_rest(w.x, w.y, u), v, bf16_rest(w.z, w.w, v));
+    // bf16 may round a larger one to infinity: then there is no bound
+    if (!(fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))) < 3e38f)) huge = 1u;
   }
   __syncthreads();
   const int64_t list = (int64_t)t * p.Hkv + kh;
@@ -490,104 +517,88 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
   const uint4* rows = reinterpret_cast<const uint4*>(p.bounds) + kh * (D / 4) + q;
   uint4 big[C];
 #pragma unroll
-  for (int k = 0; k < C; ++k) big[k] = make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < C; ++k) big[k] = make_uint4(kLeast, kLeast, kLeast, kLeast);
   float lowest = -kNegInf, highest = kNegInf;
   bool outside = false;
-  // the next pass's entries and the row after them are on their way while one is summed
   auto row_at = [&](int i) {
     int64_t row = -1;
-    if (i + g < i1) {
-      row = bounds_row(p, r, b, i + g);
+    if (i < i1) {
+      row = bounds_row(p, r, b, i);
       outside |= row < 0;
     }
     return row;
   };
-  auto load = [&](int64_t row, uint4 (&x)[C]) {
-#pragma unroll
-    for (int k = 0; k < C; ++k) x[k] = row < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + row * (p.Hkv * (D / 4)) + 4 * k);
+  auto larger = [](const uint4& a, const uint4& x) {
+    return make_uint4(max2(a.x, x.x & 0x7FFF7FFFu), max2(a.y, x.y & 0x7FFF7FFFu), max2(a.z, x.z & 0x7FFF7FFFu),
+                      max2(a.w, x.w & 0x7FFF7FFFu));
   };
-  constexpr int kPass = kWarps * 8;
-  uint4 next[C];
-  int i = i0 + warp * 8;
-  load(row_at(i), next);
-  int64_t row = row_at(i + kPass);
-  for (; i < i1; i += kPass) {
-    uint4 x[C];
+  // columns 2 q, 2 q + 1 of token g: four chains, the upper and the lower part
+  auto total = [](const float (&d)[2][4], int e) { return (d[0][e] + d[1][e]) + (d[0][2 + e] + d[1][2 + e]); };
+  for (int i = i0 + warp * 16; i < i1; i += kWarps * 16) {
+    const int64_t row[2] = {row_at(i + g), row_at(i + 8 + g)};
+    uint4 x[2][C];
 #pragma unroll
-    for (int k = 0; k < C; ++k) x[k] = next[k];
-    if (i + kPass < i1) {
-      load(row, next);
-      row = row_at(i + 2 * kPass);
-    }
-    float d[4][4] = {};
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        x[u][k] = row[u] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + row[u] * (p.Hkv * (D / 4)) + 4 * k);
+    float d[2][2][4] = {};  // [tile][chain]
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      big[k] = make_uint4(max2(big[k].x, x[k].x & 0x7FFF7FFFu), max2(big[k].y, x[k].y & 0x7FFF7FFFu),
-                          max2(big[k].z, x[k].z & 0x7FFF7FFFu), max2(big[k].w, x[k].w & 0x7FFF7FFFu));
-      const uint4 u = frag[2 * k * 32 + lane], v = frag[(2 * k + 1) * 32 + lane];
-      const uint32_t au[4] = {u.x, u.y, u.z, u.w}, av[4] = {v.x, v.y, v.z, v.w};
-      mma_bf16_16816(d[k & 3], au, x[k].x, x[k].y);
-      mma_bf16_16816(d[k & 3], av, x[k].z, x[k].w);
-    }
-    // blocks 2 q, 2 q + 1 of token g: the upper and the lower part
-    float s[2];
+      big[k] = larger(larger(big[k], x[0][k]), x[1][k]);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      s[e] = ((d[0][e] + d[1][e]) + (d[2][e] + d[3][e])) + ((d[0][2 + e] + d[1][2 + e]) + (d[2][2 + e] + d[3][2 + e]));
-      const int at = i + 2 * q + e;
-      if (g < run && at < i1) {
-        to[at] = s[e];
-        lowest = fminf(lowest, s[e]);
-        highest = fmaxf(highest, s[e]);
+      for (int h = 0; h < 2; ++h) {
+        const uint4 f = frag[(2 * k + h) * 32 + lane];
+        const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          mma_bf16_16816(d[u][h], a, h ? x[u][k].z : x[u][k].x, h ? x[u][k].w : x[u][k].y);
       }
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float s = total(d[u], e);
+        const int at = i + 8 * u + 2 * q + e;
+        if (g < run && at < i1) {
+          to[at] = s;
+          lowest = fminf(lowest, s);
+          highest = fmaxf(highest, s);
+        }
+      }
   }
   if (outside) set_status(p.status, ATTN_STATUS_CAPACITY);
-  // the largest magnitude of each component: over the warp's blocks (lanes of equal q), then over the warps
+  float d[2][4] = {};
+  uint32_t top2 = 0u;
 #pragma unroll
   for (int k = 0; k < C; ++k) {
-    uint32_t v[4] = {big[k].x, big[k].y, big[k].z, big[k].w};
+    const uint32_t sign = k < C / 2 ? 0x80008000u : 0u;
+    const uint32_t y[4] = {big[k].x | sign, big[k].y | sign, big[k].z | sign, big[k].w | sign};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4; ++e) top2 = max2(top2, y[e] & 0x7FFF7FFFu);
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) v[e] = max2(v[e], __shfl_xor_sync(0xffffffffu, v[e], off));
-      if (g == 0) {
-        ceiling[warp][8 * (4 * k + q) + 2 * e] = bf16_lo(v[e]);
-        ceiling[warp][8 * (4 * k + q) + 2 * e + 1] = bf16_hi(v[e]);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint4 f = frag[(2 * k + h) * 32 + lane];
+      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+      mma_bf16_16816(d[h], a, y[2 * h], y[2 * h + 1]);
     }
   }
+  float top = max_nan(bf16_lo(top2), bf16_hi(top2));  // of the lane's column
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (g < run) {
+    const float sum = max_nan(total(d, 0), total(d, 1));
+    // NaN and infinity are the largest as words, and a sum of magnitudes has no sign
+    atomicMax(&magnitude[g], __float_as_uint(fabsf(fmaf(top, 2 * D * kSubnormals / kMmaError, sum))));
     atomicMin(&kmin[g], order_key(lowest));
     atomicMax(&kmax[g], order_key(highest));
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
-    float m = ceiling[0][d];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = max_nan(m, ceiling[w][d]);
-    ceiling[0][d] = m;
-  }
-  __syncthreads();
-  if (warp < run) {  // a warp per token: its bound
-    float sum = 0.f, tiny = 0.f, top = 0.f;
-    for (int d = lane; d < 2 * D; d += 32) {
-      const float w = fabsf(coef[warp][d]), y = ceiling[0][d];
-      sum = fmaf(w, y, sum);
-      tiny += w + y;
-      top = max_nan(top, w);
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      tiny += __shfl_xor_sync(0xffffffffu, tiny, off);
-      top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    }
-    if (lane == 0) {
-      // a coefficient that bf16 would round to infinity leaves the scores without a bound
-      const float err = top < 3e38f ? fmaf(sum, kMmaError, fmaf(tiny, kSubnormals, kErrorFloor)) : -kNegInf;
-      p.ranges[(list + (int64_t)warp * p.Hkv) * p.chunks + c] = Range{err, kmin[warp], kmax[warp]};
-    }
+  if ((int)threadIdx.x < run) {
+    const float a = __uint_as_float(magnitude[threadIdx.x]);
+    const float err = huge ? -kNegInf : fmaf(a, kMmaError * 1.001f, kErrorFloor);
+    p.ranges[(list + (int64_t)threadIdx.x * p.Hkv) * p.chunks + c] = Range{err, kmin[threadIdx.x], kmax[threadIdx.x]};
   }
 }
 
@@ -660,8 +671,8 @@ __device__ __forceinline__ double exact_score(const BlocksPar& p, const ReqInfo&
 // One CTA chooses the K largest of the m = n - first - last candidates of token t and KV head
 // kh and writes the list.  at(i): candidate i's score (read once for the first kHeldAll, again
 // and again for others), range: of them all; bits: ceil(m / 32) words; keys: m words of 64
-// bits.  sm.bins, sm.open_n and sm.bin_n are zero.
-template <int D, typename At>
+// bits.  sm.bins, sm.open_n and sm.bin_n are zero; Coef: sm.coef is there already.
+template <int D, bool Coef, typename At>
 __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t, int kh, int n, At&& at, const Range& range,
                               uint32_t* bits, unsigned long long* keys, SelectSmem<D>& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -792,7 +803,8 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
   const int words = (m + 31) >> 5;
   if (all_exact || open != need) {
     __syncthreads();
-    for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
+    if constexpr (!Coef)
+      for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
     if (!all_exact && open <= kMaxOpen) {
       each([&](int i, uint32_t k) {
         const float x = key_value(k);
@@ -922,6 +934,8 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   const int t = blockIdx.x / p.Hkv, kh = blockIdx.x % p.Hkv;
   grid_dependency_wait();
   launch_dependents();
+  // most lists have a few scores to sum again: the coefficients' loads go out with the others
+  for (int d = threadIdx.x; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
   ReqInfo r;
   int b;
   const int n = query_blocks(p, t, &r, &b, kh == 0 && threadIdx.x == 0);
@@ -938,7 +952,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   range = join_lanes(range);
   clear_select(sm);
   __syncthreads();
-  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, range, bits,
+  select_blocks<D, true>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, range, bits,
                    p.keys + list * p.max_blocks, sm);
 }
 
@@ -1009,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_pick_kernel(const BlocksPar
   Range range = no_scores();
   for (int w = lane; w < p.chunks * kWarps; w += 32) range = join(range, told[w]);
   range = join_lanes(range);
-  select_blocks<D>(p, r, b, t, kh, n, [&](int i) { return scores[i]; }, range, bits, keys, sm);
+  select_blocks<D, false>(p, r, b, t, kh, n, [&](int i) { return scores[i]; }, range, bits, keys, sm);
 }
 
 // ---------------------------------------------------------------- host

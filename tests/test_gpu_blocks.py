@@ -260,8 +260,9 @@ def test_bounds_that_are_not_finite_rank_as_stated():
     check_select(s, 0, 1, 12)
 
 
-def test_scores_beyond_fp32():
-    s = Cache("bf16", 4, 1, 128, [64 * 300], [1], 0, 64)
+@pytest.mark.parametrize("new", [1, 3])
+def test_scores_beyond_fp32(new):
+    s = Cache("bf16", 4, 1, 128, [64 * 300], [new], 0, 64)
     fill_bounds(s)
     s.bounds.mul_(1e37)
     s.q.mul_(1e3)
@@ -269,6 +270,10 @@ def test_scores_beyond_fp32():
     fill_bounds(s)
     s.bounds.mul_(1e-38)
     s.q.mul_(1e-6)
+    check_select(s, 0, 1, 25)
+    s.q.fill_(3.0)  # subnormal bounds, which a tensor core may take for zeros
+    check_select(s, 0, 1, 25)
+    s.q[:, 1].fill_(3.38e38)  # a coefficient next to the largest number
     check_select(s, 0, 1, 25)
 
 
