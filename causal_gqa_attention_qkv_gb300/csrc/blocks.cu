@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
 // together (lengths, q, page numbers, then the bounds), scores are pushed rather than fetched,
 // and the other CTAs leave when theirs have arrived.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) block_pick_kernel(const BlocksPar p) {
+__global__ void __launch_bounds__(kThreads) block_pick_kernel(const BlocksPar p) {
   __shared__ SelectSmem<D> sm;
   __shared__ __align__(16) float coef[2 * D];
   __shared__ uint32_t bits[kHeldAll / 32];
