@@ -25,7 +25,7 @@ struct AdjustPar {
   const float* logits;
   float* out;
   int64_t ld, ld_out;
-  int32_t V, runs;
+  int32_t V;
   attn_logits_rules_t r;
 };
 
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const Adjust
   __shared__ int tok[kFew], idx[kFew];
   __shared__ float val[kFew];
   __shared__ int cnt[kAdjust / 32], listed, biases;
-  const int b = blockIdx.x / p.runs, v0 = blockIdx.x % p.runs * kRun;
+  const int b = blockIdx.x, v0 = blockIdx.y * kRun;  // low tokens, the most often seen ones, first
   const int tid = threadIdx.x;
   if (tid == 0) listed = biases = 0;
   if (tid < kRun / 32) is_biased[tid] = 0u;
@@ -395,14 +395,13 @@ int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld, co
   if (B < 0 || V < 1 || V > (1 << 23) || ld < V || ld_out < V || (logits == out && ld != ld_out)) return ATTN_EINVAL;
   int rc = check_rules(rules, V);
   if (rc) return rc;
-  AdjustPar p;
   // runs of 1024 logits, of 512 where that leaves SMs without any
   constexpr int kBig = kSteps * 4 * kAdjust, kSmall = 4 * kAdjust;
   const bool small = (int64_t)B * ((V + kBig - 1) / kBig) < 304;
-  p.runs = small ? (V + kSmall - 1) / kSmall : (V + kBig - 1) / kBig;
-  if ((int64_t)B * p.runs > 0x7fffffff) return ATTN_EINVAL;
+  const int runs = small ? (V + kSmall - 1) / kSmall : (V + kBig - 1) / kBig;  // at most 2^14
   if ((rc = abi_check_device())) return rc;
   if (B == 0) return ATTN_OK;
+  AdjustPar p;
   p.logits = logits;
   p.out = out;
   p.ld = ld;
@@ -412,7 +411,7 @@ int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld, co
   const bool vec = aligned(logits, 16) && aligned(out, 16) && (B == 1 || (ld % 4 == 0 && ld_out % 4 == 0));
   auto kernel = small ? (vec ? logits_adjust_kernel<1, true> : logits_adjust_kernel<1, false>)
                       : (vec ? logits_adjust_kernel<kSteps, true> : logits_adjust_kernel<kSteps, false>);
-  return launch_dependent(kernel, dim3((unsigned)(B * p.runs)), dim3(kAdjust), 0, static_cast<cudaStream_t>(stream), p) ==
+  return launch_dependent(kernel, dim3((unsigned)B, (unsigned)runs), dim3(kAdjust), 0, static_cast<cudaStream_t>(stream), p) ==
                  cudaSuccess
              ? ATTN_OK
              : ATTN_ELAUNCH;
