@@ -59,7 +59,7 @@ class AttnLogitsRules(ctypes.Structure):
     _fields_ = [("seen", ctypes.c_void_p), ("seen_ld", ctypes.c_int64), ("seen_rows", ctypes.c_int32),
                 ("seen_row", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
                 ("frequency", ctypes.c_void_p), ("bias_start", ctypes.c_void_p), ("bias_token", ctypes.c_void_p),
-                ("bias_value", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_ld", ctypes.c_int64),
+                ("bias_value", ctypes.c_void_p), ("num_biases", ctypes.c_int32), ("mask", ctypes.c_void_p), ("mask_ld", ctypes.c_int64),
                 ("mask_rows", ctypes.c_int32), ("mask_row", ctypes.c_void_p)]
 
 
@@ -633,8 +633,8 @@ def block_select(cfg: AttnConfig, q, cu_seqlens, max_kv_len: int, kv: KVCache, b
     n, H, keep = out_list.shape
     assert n == N and H == cfg.num_kv_heads, "out_list"
     s, k = kv.struct_for(cfg, exact=True), blocks.struct(cfg, B)
-    _check(load().attn_block_select(ctypes.byref(cfg), qp, cu, B, N, max_kv_len, ctypes.byref(s), ctypes.byref(k), first,
-                                    last, keep, _i32(out_list, "out_list"), workspace.data_ptr(), workspace.numel(),
+    _check(load().attn_block_select(ctypes.byref(cfg), qp, cu, B, N, int(max_kv_len), ctypes.byref(s), ctypes.byref(k),
+                                    int(first), int(last), keep, _i32(out_list, "out_list"), workspace.data_ptr(), workspace.numel(),
                                     _stream(stream)))
 
 
@@ -648,7 +648,7 @@ def block_attend(cfg: AttnConfig, q, cu_seqlens, kv: KVCache, block_size: int, b
     assert n == N and H == cfg.num_kv_heads, "block_list"
     assert out.numel() >= q.numel(), "out"
     s = kv.struct_for(cfg, exact=True)
-    _check(load().attn_block_attend(ctypes.byref(cfg), qp, cu, B, N, ctypes.byref(s), block_size,
+    _check(load().attn_block_attend(ctypes.byref(cfg), qp, cu, B, N, ctypes.byref(s), int(block_size),
                                     _i32(block_list, "block_list"), keep, _bf16(out, "out"), workspace.data_ptr(),
                                     workspace.numel(), _stream(stream)))
 
@@ -721,7 +721,8 @@ class LogitsRules:
         s, m = self.seen, self.mask
         return AttnLogitsRules(_ptr(s), 0 if s is None else s.shape[1], 0 if s is None else s.shape[0],
                                _ptr(self.seen_row), _ptr(self.repetition), _ptr(self.presence), _ptr(self.frequency),
-                               _ptr(self.bias_start), _ptr(self.bias_token), _ptr(self.bias_value), _ptr(m),
+                               _ptr(self.bias_start), _ptr(self.bias_token), _ptr(self.bias_value),
+                               0 if self.bias_start is None else self.bias_token.numel(), _ptr(m),
                                0 if m is None else m.shape[1], 0 if m is None else m.shape[0], _ptr(self.mask_row))
 
 

@@ -60,7 +60,7 @@ struct BlocksPar {
   const uint16_t* q;         // [N, Hq, D]
   int32_t q_f16, N, G, first, last, keep, max_blocks, chunk, chunks;
   float* scores;             // [N, Hkv, max_blocks]
-  Range* ranges;      // [N, Hkv, chunks]
+  Range* ranges;             // [N, Hkv, chunks]
   unsigned long long* keys;  // [N, Hkv, max_blocks] exact scores, where they are needed
   int32_t* list;             // [N, Hkv, keep]
 };
@@ -70,7 +70,7 @@ struct BlocksPar {
 __device__ __forceinline__ int64_t bounds_row(const BlocksPar& p, const ReqInfo& r, int b, int i) {
   int64_t row;
   if (r.pages) {
-    const int64_t slot = cache_slot(p.kv, r, i << p.log2_bs);
+    const int64_t slot = block_slot(p.kv, r, i << p.log2_bs);
     row = slot < 0 ? -1 : slot >> p.log2_bs;
   } else {
     row = __ldg(p.row_base + b) + i;
@@ -86,8 +86,8 @@ __device__ __forceinline__ int64_t bounds_row_at(const BlocksPar& p, int b, int 
     const int64_t pg = pos >> p.kv.log2_page;
     if (pg >= p.kv.pages_per_req) return -1;
     const int64_t page = __ldg(p.kv.page_table + (int64_t)b * p.kv.pages_per_req + pg);
-    const int64_t slot = (page << p.kv.log2_page) + (pos & ((1 << p.kv.log2_page) - 1));
-    row = page >= 0 && slot < p.kv.num_slots ? slot >> p.log2_bs : -1;
+    if (page < 0 || page >= p.kv.num_slots >> p.kv.log2_page) return -1;
+    row = ((page << p.kv.log2_page) + (pos & ((1 << p.kv.log2_page) - 1))) >> p.log2_bs;
   } else {
     row = __ldg(p.row_base + b) + i;
   }
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_bounds_kernel(const BlocksP
   const int li = lane % L, sub = lane / L;
   for (int64_t it = (int64_t)part * kWarps + warp; it < items; it += (int64_t)p.ctas_per_request * kWarps) {
     const int i = from + (int)(it / p.Hkv), kh = (int)(it % p.Hkv);
-    const int64_t slot = cache_slot(p.kv, r, i << p.log2_bs);
+    const int64_t slot = block_slot(p.kv, r, i << p.log2_bs);
     const int64_t row = bounds_row(p, r, b, i);
     if ((slot < 0 || row < 0) && lane == 0) set_status(p.status, ATTN_STATUS_CAPACITY);
     if (row < 0) continue;

@@ -225,7 +225,7 @@ __device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int 
       const uint32_t all = __ballot_sync(0xffffffffu, live);
       if (live) {
         const int to = at + __popc(all & ((1u << lane) - 1u));
-        const int slot = (int)cache_slot(p.kv, r, entry << p.log2_bs);
+        const int slot = (int)block_slot(p.kv, r, entry << p.log2_bs);
         mine.block[to] = entry;
         mine.slot[to] = slot;
         if (slot < 0) set_status(p.status, ATTN_STATUS_CAPACITY);

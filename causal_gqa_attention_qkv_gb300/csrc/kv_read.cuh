@@ -33,6 +33,16 @@ __device__ __forceinline__ uint4 read8(const void* cache, const uint8_t* bscale,
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Slot of the first entry of a block (64 positions or more within a page) at position pos of a
+// request, -1 where its page is not one of the cache's: unlike cache_slot(), whose callers read
+// entry by entry or by tiles that end with the cache, a page that the cache's end cuts is none.
+__device__ __forceinline__ int64_t block_slot(const KvIndex& kv, const ReqInfo& r, int pos) {
+  if (!r.pages) return r.slot0 + pos;
+  const int64_t pg = __ldg(r.pages + (pos >> kv.log2_page));
+  if (pg < 0 || pg >= kv.num_slots >> kv.log2_page) return -1;
+  return (pg << kv.log2_page) + (pos & ((1 << kv.log2_page) - 1));
+}
+
 // The request of packed token t, the number of its new tokens and the token's place j
 // among them; cu == NULL: one token per request.  False for a token of no request.  The lanes
 // of a warp search together, 32 requests a step: all of them call this with the same t.

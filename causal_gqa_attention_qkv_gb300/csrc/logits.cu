@@ -49,8 +49,8 @@ __device__ void sum_biases(const attn_logits_rules_t& r, int e0, int e1, int v0,
                            float* val, int* cnt) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int k = tid; k < run; k += kAdjust) bias[k] = 0.f;
-  for (int e = e0; e < e1; e += kAdjust) {
-    const int i = e + tid;
+  for (int64_t e = e0; e < e1; e += kAdjust) {
+    const int64_t i = e + tid;
     const int t = i < e1 ? __ldg(r.bias_token + i) : -1;
     const bool mine = t >= v0 && t < v0 + n;
     const uint32_t all = __ballot_sync(0xffffffffu, mine);
@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const Adjust
   // what is known of the row, in one round of loads
   const int seen_at = p.r.seen && p.r.seen_row ? __ldg(p.r.seen_row + b) : b;
   const int mask_at = p.r.mask && p.r.mask_row ? __ldg(p.r.mask_row + b) : b;
-  const int e0 = p.r.bias_start ? __ldg(p.r.bias_start + b) : 0;
-  const int e1 = p.r.bias_start ? __ldg(p.r.bias_start + b + 1) : 0;
+  const int e0 = p.r.bias_start ? max(__ldg(p.r.bias_start + b), 0) : 0;
+  const int e1 = p.r.bias_start ? min(__ldg(p.r.bias_start + b + 1), p.r.num_biases) : 0;
   const Penalties c = {p.r.repetition ? __ldg(p.r.repetition + b) : 0.f, p.r.frequency ? __ldg(p.r.frequency + b) : 0.f,
                        p.r.presence ? __ldg(p.r.presence + b) : 0.f};
   auto place = [&](int q, int e) { return Vec ? (q * kAdjust + tid) * 4 + e : (q * 4 + e) * kAdjust + tid; };
@@ -147,17 +147,17 @@ __global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const Adjust
   }
   int few = 0;  // biases in the run, if they fit the list
   if (e1 > e0) {
-    for (int i0 = e0; i0 < e1; i0 += 4 * kAdjust) {
+    for (int64_t i0 = e0; i0 < e1; i0 += 4 * kAdjust) {
       int t[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kAdjust + tid;
+        const int64_t i = i0 + k * kAdjust + tid;
         t[k] = i < e1 ? __ldg(p.r.bias_token + i) - v0 : -1;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (t[k] < 0 || t[k] >= n) continue;
-        const int i = i0 + k * kAdjust + tid;
+        const int i = (int)i0 + k * kAdjust + tid;  // an entry: below e1
         const int at = atomicAdd(&biases, 1);  // in any order
         if (at < kFew) {
           tok[at] = t[k];
@@ -373,7 +373,7 @@ int check_rules(const attn_logits_rules_t* r, int32_t V) {
   if (r->seen) {
     if (!aligned(r->seen, 16) || r->seen_rows < 1 || r->seen_ld < V || r->seen_ld % 8 != 0) return ATTN_EINVAL;
   }
-  if (r->bias_start && (!r->bias_token || !r->bias_value)) return ATTN_EINVAL;
+  if (r->bias_start && (r->num_biases < 0 || (r->num_biases > 0 && (!r->bias_token || !r->bias_value)))) return ATTN_EINVAL;
   if (r->mask && (r->mask_rows < 1 || r->mask_ld < (V + 31) / 32)) return ATTN_EINVAL;
   for (const void* p : {(const void*)r->seen_row, (const void*)r->repetition, (const void*)r->presence,
                         (const void*)r->frequency, (const void*)r->bias_start, (const void*)r->bias_token,

@@ -65,6 +65,7 @@ typedef struct attn_blocks {
 
 /* Workspace bytes for the calls below with at most max_tokens tokens, max_kv_len
  * keys per request (c_b + n_b) and lists of `keep` blocks; covers smaller calls too.
+ * It holds a 256-byte header (status word) and the scores of attn_block_select.
  * 256-byte aligned, caller-owned, initialised by attn_workspace_init.  0 for invalid
  * arguments. */
 ATTN_API size_t attn_block_workspace_size(const attn_config_t* cfg, int32_t max_tokens, int32_t max_kv_len,
@@ -104,7 +105,8 @@ ATTN_API int attn_block_select(const attn_config_t* cfg, const void* q, const in
  *   list[t, h / (Hq / Hkv), :]
  * out: bf16 [N, Hq * D], 16-byte aligned.  Entries of the list may come in any order;
  * a negative one and one past the query's own block are skipped, and a block listed
- * twice counts twice.  A query whose list leaves no key gets zeros.  Every query
+ * twice counts twice.  A query whose list leaves no key gets zeros.  The workspace needs
+ * only its 256-byte header.  Every query
  * reads its own blocks, so long chunks of prompts over short caches are faster
  * through attn_prefill_attend. */
 ATTN_API int attn_block_attend(const attn_config_t* cfg, const void* q, const int32_t* cu_seqlens, int32_t B,

@@ -45,8 +45,9 @@ typedef struct attn_logits_rules {
   const float* presence;
   const float* frequency;
   const int32_t* bias_start; /* [B + 1], or NULL: no biases.  Row b's entries: bias_start[b] .. bias_start[b + 1] - 1 */
-  const int32_t* bias_token; /* tokens outside [0, V) are skipped */
-  const float* bias_value;
+  const int32_t* bias_token; /* [num_biases]; tokens outside [0, V) are skipped */
+  const float* bias_value;   /* [num_biases] */
+  int32_t num_biases;        /* entries of bias_start outside [0, num_biases) are skipped */
   const uint32_t* mask;      /* [mask_rows, mask_ld], bit v % 32 of word v / 32: token v is allowed; NULL: no masks */
   int64_t mask_ld;           /* words per row, >= ceil(V / 32) */
   int32_t mask_rows;
@@ -59,7 +60,7 @@ typedef struct attn_logits_rules {
  * finite logit).  ATTN_EINVAL: NULL rules, NULL logits or out with B != 0, B < 0, V < 1,
  * V > 2^23, ld or ld_out < V, out == logits with another ld, a misaligned pointer, a table
  * or mask with a row shorter than V or without rows, seen_ld not a multiple of 8,
- * bias_start without bias_token and bias_value. */
+ * bias_start with num_biases < 0, or > 0 without bias_token and bias_value. */
 ATTN_API int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64_t ld,
                                 const attn_logits_rules_t* rules, float* out, int64_t ld_out, void* stream);
 

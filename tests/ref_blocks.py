@@ -129,7 +129,7 @@ class Cache:
     """A cache with random entries, requests of the given cached and new lengths (the cache
     holds both), and bounds."""
 
-    def __init__(self, kind, hq, hkv, d, cached, new, page, block, seed=0, spare=1, extra_rows=0):
+    def __init__(self, kind, hq, hkv, d, cached, new, page, block, seed=0, spare=1, extra_rows=0, extra_slots=0):
         from causal_gqa_attention_qkv_gb300 import attn
         self.kind, self.hq, self.hkv, self.d = kind, hq, hkv, d
         rng = np.random.RandomState(seed)
@@ -145,7 +145,7 @@ class Cache:
             for b in range(B):
                 at = sum(need[:b])
                 table[b, :need[b]] = perm[at:at + need[b]]
-            base, cap, slots = np.zeros(B, np.int64), np.full(B, table.shape[1] * page), total * page
+            base, cap, slots = np.zeros(B, np.int64), np.full(B, table.shape[1] * page), total * page + extra_slots
             c["rows"] = slots // block + extra_rows
             row_base = None
         else:

@@ -193,7 +193,7 @@ def test_block_workspace_size(lib):
 def test_logits_adjust_checks_its_arguments(lib):
     from causal_gqa_attention_qkv_gb300 import attn
     full = dict(seen=FAKE, seen_ld=1000, seen_rows=4, seen_row=FAKE, repetition=FAKE, presence=FAKE, frequency=FAKE,
-                bias_start=FAKE, bias_token=FAKE, bias_value=FAKE, mask=FAKE, mask_ld=32, mask_rows=2, mask_row=FAKE)
+                bias_start=FAKE, bias_token=FAKE, bias_value=FAKE, num_biases=9, mask=FAKE, mask_ld=32, mask_rows=2, mask_row=FAKE)
 
     def call(x=F, B=2, V=1000, ld=1000, out=ctypes.c_void_p(2 * FAKE), ldo=1000, no_rules=False, **kw):
         r = attn.AttnLogitsRules(*{**full, **kw}.values())
@@ -202,11 +202,12 @@ def test_logits_adjust_checks_its_arguments(lib):
     assert ok() and ok(B=0) and ok(out=F) and ok(ld=1001) and ok(V=1)
     for name in ("seen", "seen_row", "repetition", "presence", "frequency", "mask", "mask_row", "bias_start"):
         assert ok(**{name: None}), name
+    assert ok(num_biases=0, bias_token=None, bias_value=None) and ok(bias_start=None, num_biases=-1)
     assert ok(seen=None, seen_ld=0, seen_rows=0) and ok(mask=None, mask_ld=0, mask_rows=0)
     for kw in (dict(x=None), dict(out=None), dict(no_rules=True), dict(B=-1), dict(V=0), dict(V=(1 << 23) + 1, ld=1 << 24,
                ldo=1 << 24), dict(ld=999), dict(ldo=999), dict(out=F, ldo=1001), dict(x=ODD), dict(out=ODD),
                dict(seen=FAKE + 8), dict(seen_ld=992), dict(seen_ld=1001), dict(seen_rows=0), dict(bias_token=None),
-               dict(bias_value=None), dict(mask_ld=31), dict(mask_rows=0), dict(repetition=FAKE + 2), dict(mask=FAKE + 1),
+               dict(bias_value=None), dict(num_biases=-1), dict(mask_ld=31), dict(mask_rows=0), dict(repetition=FAKE + 2), dict(mask=FAKE + 1),
                dict(seen_row=FAKE + 2), dict(bias_start=FAKE + 2), dict(mask_row=FAKE + 2)):
         assert call(**kw) == -1, kw
 

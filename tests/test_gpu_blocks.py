@@ -468,6 +468,31 @@ def test_attend_problems_set_the_status(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page,block,extra", [(128, 128, 100), (256, 64, 130), (256, 256, 1)])
+def test_a_page_that_the_cache_s_end_cuts(kind, page, block, extra):
+    """Its number lies outside the cache: it has no bounds, scores as zeros and reads as zeros."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    s = Cache(kind, 4, 2, 64, [page * 9 + 3], [page], page, block, extra_slots=extra)
+    cut = s.c["slots"] // page
+    for i in (2, 8):
+        s.kv.page_table[0, i] = cut
+        s.c["table"][0, i] = cut
+    ws = s.workspace(4)
+    attn.block_bounds(s.cfg, s.kv, s.blocks, s.cu, ws, start=i32([0]))
+    assert status(ws) == CAP
+    got, want = s.bounds.double().cpu().numpy(), rb.bounds(s.c, s.entries("k"), [0])
+    for row in range(s.c["rows"]):
+        assert np.array_equal(got[row], want.get(row, np.full_like(got[row], 776.0)))
+    fill_bounds(s)
+    lists, st = run_select(s, 1, 1, 4)
+    assert st == CAP and np.array_equal(lists, rb.select(s.c, s.q64(), s.bounds.double().cpu().numpy(), 1, 1, 4))
+    lists[:, :, 1] = 2 * page // block
+    out, st = run_attend(s, lists)
+    want, tol = rb.attend(s.c, s.q64(), lists, s.entries("k"), s.entries("v"), kind != "bf16")
+    assert st == CAP and (np.abs(out - want) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_attend_in_a_cache_past_two_to_the_32_bytes(kind):
     from causal_gqa_attention_qkv_gb300 import attn
     hkv, d, ps = 8, 128, 64

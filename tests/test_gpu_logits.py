@@ -153,6 +153,18 @@ def test_tokens_and_rows_outside():
     check(w)
 
 
+def test_biases_named_outside_the_list():
+    """bias_start that begins before the list, ends past it or runs backwards."""
+    w = Rows(4, 1500, biases=9)
+    r = w.rules()
+    r.bias_start = dev([-5, 18, 30, 27, 10 ** 9], torch.int32)
+    w.bias = [w.bias[0] + w.bias[1], w.bias[2] + w.bias[3][:3], [], w.bias[3]]
+    check(w, r)
+    r.bias_start = dev([40, 2 ** 31 - 1, -2 ** 31, -1, 0], torch.int32)
+    w.bias = [[]] * 4
+    check(w, r)
+
+
 def test_rows_by_their_own_number():
     """No row numbers: row b of the table and of the masks."""
     w = Rows(3, 777, mask=0.4, shuffle=False, table_rows=3)
