@@ -336,19 +336,25 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
   uint64_t w[4];  // pairs of coefficients
   *reinterpret_cast<ulonglong2*>(w) = *reinterpret_cast<const ulonglong2*>(coef + 8 * li);
   *reinterpret_cast<ulonglong2*>(w + 2) = *reinterpret_cast<const ulonglong2*>(coef + 8 * li + 4);
-  for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
-    // rows of the warp's blocks, one per lane
+  // rows of the warp's blocks, one per lane; those of the next pass are looked up a pass ahead
+  auto look_up = [&](int i) {
     int64_t row = -1;
     if (lane < 8 * BPW && i + lane < i1) {
       row = row_of(i + lane);
       outside |= row < 0;
     }
+    return row;
+  };
+  int64_t next = look_up(i0 + warp * 8 * BPW);
+  for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
+    const int64_t row = next;
     uint4 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t rk = __shfl_sync(0xffffffffu, row, k * BPW + sub);
       x[k] = rk < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + rk * (p.Hkv * (D / 4)));
     }
+    next = look_up(i + kWarps * 8 * BPW);
     float s[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

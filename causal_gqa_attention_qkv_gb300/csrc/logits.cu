@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
   const bool again = __syncthreads_or(after);
   for (int i = b;;) {
 #pragma unroll 8
-    for (int t = t0 + tid; t < t1; t += kThreads) {
+    for (int64_t t = t0 + tid; t < t1; t += kThreads) {
       const int v = __ldg(p.tokens + t);
       if (v >= 0 && v < p.V && v >= v0 && v < v0 + kSegment) {
         if constexpr (Prompt) mark[v - v0] = 1;
@@ -339,9 +339,9 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
 __global__ void __launch_bounds__(kThreads) seen_mark_kernel(const SeenPar p) {
   grid_dependency_wait();
   launch_dependents();
-  const int t = blockIdx.x * kThreads + threadIdx.x;
+  const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (t >= p.N) return;
-  int b = t;
+  int b = (int)t;
   if (p.cu_seqlens) {
     int lo = 0, hi = p.B;  // largest b with cu[b] <= t
     while (hi - lo > 1) {
