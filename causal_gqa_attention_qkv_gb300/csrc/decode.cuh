@@ -42,7 +42,7 @@ struct DecodePar {
   int32_t B, keep, log2_bs;
 };
 
-constexpr int kMaxSplitBlocks = 1024;  // entries of a list that one split may take
+constexpr int kMaxSplitBlocks = 512;  // entries of a list that one split may take (4096 in at most 16 splits)
 
 // What a split over listed blocks keeps of them in shared memory: the blocks that hold a
 // visible key and their first slots.
