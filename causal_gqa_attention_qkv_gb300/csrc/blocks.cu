@@ -1100,14 +1100,19 @@ int launch_bounds_d(const BlocksPar& p, int kv_dtype, cudaStream_t s) {
   }
 }
 
-// Tokens of one request next to each other share the reading of the bounds in the two kernels; a
-// token per request takes the one that spares a launch and the scores' way through memory.
+// One kernel or two: tokens of one request next to each other share the reading of the bounds
+// in the two, and the one spares a launch and the scores' way through memory.  16 requests of
+// up to 30000 keys: 16.9 us (one kernel), 20.8 (two) with a token each, 19.4 and 22.3 with 24
+// tokens, 29.9 and 24.7 with 40, 35.5 and 30.3 with 80.
+// Clusters where there are few lists (us with 1, 2, 4, 8, 16 CTAs each): 8 lists of 1016 blocks
+// 20.7, 13.7, 9.8, 7.9, 7.4; 32 of 1016 23.0, 17.0, 13.2, 12.5, 12.6; 64 of 470 12.8, 11.2, 10.6, 12.7,
+// 20.1; 128 of 256 11.6, 15.1, 15.3, 19.0, 34.6; 256 of 470 23.0, 29.2, 29.6, 39.3, 80.7.
 template <int D>
 int launch_select_t(BlocksPar& p, cudaStream_t s) {
   const int64_t lists = (int64_t)p.N * p.Hkv;
   if (p.N < 2 * (int64_t)p.B && p.max_blocks <= kHeldAll) {
     int c = 1;
-    while (c < 16 && lists * c < 304 && p.max_blocks > 64 * c) c *= 2;
+    while (lists <= 64 && c < 16 && lists * c < 256 && p.max_blocks > 64 * c) c *= 2;
     p.chunks = c;
     p.chunk = 64;
     while (p.chunk * c < p.max_blocks) p.chunk *= 2;
