@@ -11,10 +11,10 @@
 // one dot product of 2 D terms per block and KV head, however many heads the group
 // has, and it is bound by reading the bounds (4 D bytes).  A list must not depend on the
 // order of fp32 sums, so a kernel takes the scores in fp32 with a bound on
-// their error, and a second one decides: a threshold t with K scores above it, E the largest
-// bound; a score above t + 2 E belongs to the K largest whatever the errors
-// are, one below t - 2 E does not, and only those between are summed again in fp64.
-// (At least K exact scores are >= t - E and fewer than K of the others exceed t + E.)
+// their error E, and a second one decides: t the K-th score, u the one after it; a score above
+// u + 2 E belongs to the K largest whatever the errors are, one below t - 2 E does not, and
+// only those between, if any, are summed again in fp64.  (Of the others only K - 1 can exceed
+// u + E, and at least K exact scores are >= t - E.  A threshold between t and u will do for both.)
 //
 // The kernels let dependents start only behind their own wait: a decode kernel reads the
 // requests' lengths before its wait, and a call that writes them may come before these.
@@ -252,19 +252,58 @@ __device__ __forceinline__ int query_blocks(const BlocksPar& p, int t, ReqInfo* 
   return visible_blocks(p, *r, j, report);
 }
 
-// M and P of token t and KV head kh, for component d; a NaN enters both.
-template <typename T>
-__device__ __forceinline__ void coefficients(const BlocksPar& p, int t, int kh, int D, int d, T* m, T* q) {
+// f(component d of each head of token t in KV head kh's group): the loads of eight heads go out
+// together, whatever the group's size (absent ones count as 0).
+template <typename F>
+__device__ __forceinline__ void each_head(const BlocksPar& p, int t, int kh, int D, int d, F&& f) {
   const uint16_t* row = p.q + ((int64_t)t * p.Hkv + kh) * p.G * D + d;
-  T lo = 0, hi = 0;
-#pragma unroll 8
-  for (int h = 0; h < p.G; ++h) {
-    const float x = q_value(__ldg(row + h * D), p.q_f16);
-    lo += x > 0.f ? T(0) : (T)x;
-    hi += x < 0.f ? T(0) : (T)x;
+  for (int h = 0; h < p.G; h += 8) {
+    uint16_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = h + e < p.G ? __ldg(row + (h + e) * D) : (uint16_t)0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f(q_value(v[e], p.q_f16));
   }
+}
+
+// M and P of token t and KV head kh, for component d; a NaN enters both.
+__device__ __forceinline__ void coefficients(const BlocksPar& p, int t, int kh, int D, int d, float* m, float* q) {
+  float lo = 0.f, hi = 0.f;
+  each_head(p, t, kh, D, d, [&](float x) {
+    lo += x > 0.f ? 0.f : x;
+    hi += x < 0.f ? 0.f : x;
+  });
   *m = lo;
   *q = hi;
+}
+
+// s + x = the new s + what is added to rest, exactly where nothing overflows (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(float& s, float& rest, float x) {
+  const float u = s + x, v = u - s;
+  rest += (s - (u - v)) + (x - v);
+  s = u;
+}
+// The same in 64 bits.  fp64 units are few (a list's 2 D G additions took 1500 cycles there): two fp32
+// words hold the sums, exactly if the entries' magnitudes are within 2^36 of each other, to
+// 2^-47 of them otherwise; fp64 takes those that are huge or not finite.
+__device__ __forceinline__ void coefficients(const BlocksPar& p, int t, int kh, int D, int d, double* m, double* q) {
+  float lo = 0.f, lo_rest = 0.f, hi = 0.f, hi_rest = 0.f;
+  each_head(p, t, kh, D, d, [&](float x) {
+    two_sum(lo, lo_rest, x > 0.f ? 0.f : x);
+    two_sum(hi, hi_rest, x < 0.f ? 0.f : x);
+  });
+  if (hi - lo < 1e38f) {
+    *m = (double)lo + (double)lo_rest;
+    *q = (double)hi + (double)hi_rest;
+    return;
+  }
+  double a = 0.0, b = 0.0;
+  each_head(p, t, kh, D, d, [&](float x) {
+    a += x > 0.f ? 0.0 : (double)x;
+    b += x < 0.f ? 0.0 : (double)x;
+  });
+  *m = a;
+  *q = b;
 }
 
 // Two fp32 operations in one instruction, each rounded to nearest even.
@@ -631,7 +670,7 @@ struct SelectSmem {
   uint32_t bin_key[kMaxOpen];
   int open_n, bin_n;
   int bin, above, inside;  // the bin with the K-th key: keys above it, keys in it
-  uint32_t thr;
+  uint32_t thr, next;  // the K-th key, the one after it
   int sums[kWarps];
 };
 
@@ -657,15 +696,20 @@ struct Counter {
   }
 };
 
-// Score of a block in fp64, summed by one warp in the same order for every block.
+// This lane's entries of a block's bounds, and the block's score in fp64, summed by one warp in the
+// same order for every block.
 template <int D>
-__device__ __forceinline__ double exact_score(const BlocksPar& p, const ReqInfo& r, int b, int kh, int i,
-                                              const double* coef, int lane) {
-  const int64_t row = bounds_row(p, r, b, i);
+__device__ __forceinline__ uint4 bounds_entries(const BlocksPar& p, const ReqInfo& r, int b, int kh, int i, int lane) {
+  const int64_t row = lane < D / 4 ? bounds_row(p, r, b, i) : -1;
+  if (row < 0) return make_uint4(0, 0, 0, 0);
+  return __ldg(reinterpret_cast<const uint4*>(p.bounds + (row * p.Hkv + kh) * (2 * D)) + lane);
+}
+template <int D>
+__device__ __forceinline__ double exact_score(const uint4& entries, const double* coef, int lane) {
   double s = 0.0;
-  if (row >= 0 && lane < D / 4) {
+  if (lane < D / 4) {
     float y[8];
-    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.bounds + (row * p.Hkv + kh) * (2 * D)) + lane), y);
+    unpack_bf16x8(entries, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = fma(coef[8 * lane + e], (double)y[e], s);
   }
@@ -750,7 +794,7 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     }
     __syncthreads();
     const int inside = sm.inside, want = K - sm.above;
-    uint32_t thr = kmin + ((uint32_t)sm.bin << shift);
+    uint32_t thr = kmin + ((uint32_t)sm.bin << shift), next = thr;  // next: K + 1 keys there, or no more than thr
     if (inside > want && inside <= kMaxOpen) {
       const uint32_t bin = sm.bin;
       each([&](int i, uint32_t k) {
@@ -765,9 +809,11 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
           same += sm.bin_key[o] == k;
         }
         if (larger < want && larger + same >= want) sm.thr = k;  // equal keys write the same
+        if (larger <= want && larger + same > want) sm.next = k;
       }
       __syncthreads();
       thr = sm.thr;
+      next = sm.next;
     } else if (inside > want) {
       // a crowded bin (a few scores far from all others): bit by bit below the bin's edge, two
       // at a time; it is enough that exactly K keys are at or above
@@ -786,10 +832,11 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
         if (take & 1) thr += lo;
         if (take != 0 && n3[take - 1] == K) break;
       }
+      next = thr;
     }
-    const float tau = key_value(thr), width = 2.02f * range.err;
-    low = tau - width;
-    high = tau + width;
+    const float width = 2.02f * range.err;
+    low = key_value(thr) - width;
+    high = key_value(next) + width;
     int so[2] = {0, 0};  // per warp
     each([&](int i, uint32_t k) {
       const float x = key_value(k);
@@ -808,9 +855,12 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
   const int need = K - sure;  // of the open ones
   const int words = (m + 31) >> 5;
   if (all_exact || open != need) {
+    auto make_coef = [&] {
+      if constexpr (!Coef)
+        for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
+      __syncthreads();
+    };
     __syncthreads();
-    if constexpr (!Coef)
-      for (int d = tid; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
     if (!all_exact && open <= kMaxOpen) {
       each([&](int i, uint32_t k) {
         const float x = key_value(k);
@@ -819,12 +869,20 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
         if (i < m && x >= low && !(x > high)) sm.open_idx[atomicAdd(&sm.open_n, 1)] = i;  // in any order
       });
       __syncthreads();
-      for (int o = warp; o < open; o += kWarps) {
-        const double s = exact_score<D>(p, r, b, kh, p.first + sm.open_idx[o], sm.coef, lane);
-        if (lane == 0) sm.open_key[o] = order_key64(s);
+      if (need > 0) {  // (K are sure otherwise)
+        auto entries = [&](int o) {
+          return bounds_entries<D>(p, r, b, kh, p.first + sm.open_idx[min(o, open - 1)], lane);
+        };
+        uint4 y = entries(warp);  // on their way while the coefficients are made
+        make_coef();
+        for (int o = warp; o < open; o += kWarps) {
+          const double s = exact_score<D>(y, sm.coef, lane);
+          if (lane == 0) sm.open_key[o] = order_key64(s);
+          if (o + kWarps < open) y = entries(o + kWarps);
+        }
       }
       __syncthreads();
-      if (tid < open) {
+      if (tid < open && need > 0) {
         const unsigned long long mine = sm.open_key[tid];
         const int idx = sm.open_idx[tid];
         int better = 0;
@@ -836,9 +894,9 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
     } else {
       // many equal scores, or some that are not finite: every candidate's key in 64 bits and a
       // search by bits
-      __syncthreads();
+      make_coef();
       for (int i = warp; i < m; i += kWarps) {
-        const double s = exact_score<D>(p, r, b, kh, p.first + i, sm.coef, lane);
+        const double s = exact_score<D>(bounds_entries<D>(p, r, b, kh, p.first + i, lane), sm.coef, lane);
         if (lane == 0) keys[i] = order_key64(s);
       }
       __syncthreads();
