@@ -39,6 +39,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The larger of magnitudes a >= 0 and those of x.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t x) {
+  const __nv_bfloat162 y = __habs2(*reinterpret_cast<__nv_bfloat162*>(&x));
+  return max2(a, *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ uint4 larger(const uint4& a, const uint4& x) {
+  return make_uint4(larger(a.x, x.x), larger(a.y, x.y), larger(a.z, x.z), larger(a.w, x.w));
+}
+
 struct Range;
 
 struct BlocksPar {
@@ -75,7 +84,7 @@ __device__ __forceinline__ int64_t bounds_row(const BlocksPar& p, const ReqInfo&
   } else {
     row = __ldg(p.row_base + b) + i;
   }
-  return row < p.num_rows ? row : -1;
+  return row >= 0 && row < p.num_rows ? row : -1;
 }
 
 // The same from the arguments alone; any i >= 0.
@@ -91,7 +100,7 @@ __device__ __forceinline__ int64_t bounds_row_at(const BlocksPar& p, int b, int 
   } else {
     row = __ldg(p.row_base + b) + i;
   }
-  return row < p.num_rows ? row : -1;
+  return row >= 0 && row < p.num_rows ? row : -1;
 }
 
 // ---------------------------------------------------------------- bounds
@@ -252,18 +261,18 @@ __device__ __forceinline__ int query_blocks(const BlocksPar& p, int t, ReqInfo* 
   return visible_blocks(p, *r, j, report);
 }
 
-// f(component d of each head of token t in KV head kh's group): the loads of eight heads go out
-// together, whatever the group's size (absent ones count as 0).
+constexpr int kMaxGroup = 8;
+
+// f(component d of each head of token t in KV head kh's group): all loads go out together,
+// whatever the group's size (absent heads count as 0; one after another they took 2400 cycles).
 template <typename F>
 __device__ __forceinline__ void each_head(const BlocksPar& p, int t, int kh, int D, int d, F&& f) {
   const uint16_t* row = p.q + ((int64_t)t * p.Hkv + kh) * p.G * D + d;
-  for (int h = 0; h < p.G; h += 8) {
-    uint16_t v[8];
+  uint16_t v[kMaxGroup];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = h + e < p.G ? __ldg(row + (h + e) * D) : (uint16_t)0;
+  for (int h = 0; h < kMaxGroup; ++h) v[h] = h < p.G ? __ldg(row + h * D) : (uint16_t)0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f(q_value(v[e], p.q_f16));
-  }
+  for (int h = 0; h < kMaxGroup; ++h) f(q_value(v[h], p.q_f16));
 }
 
 // M and P of token t and KV head kh, for component d; a NaN enters both.
@@ -375,30 +384,28 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
   uint64_t w[4];  // pairs of coefficients
   *reinterpret_cast<ulonglong2*>(w) = *reinterpret_cast<const ulonglong2*>(coef + 8 * li);
   *reinterpret_cast<ulonglong2*>(w + 2) = *reinterpret_cast<const ulonglong2*>(coef + 8 * li + 4);
-  // rows of the warp's blocks, one per lane; those of the next pass are looked up a pass ahead
+  // rows of the warp's blocks, one per lane; those of the next pass are looked up a pass ahead.
+  // Lanes past the last block repeat it; a block of no row reads the first row and counts as 0.
   auto look_up = [&](int i) {
-    int64_t row = -1;
-    if (lane < 8 * BPW && i + lane < i1) {
-      row = row_of(i + lane);
+    int row = 0;
+    if (lane < 8 * BPW && i < i1) {
+      row = (int)row_of(min(i + lane, i1 - 1));
       outside |= row < 0;
     }
     return row;
   };
-  int64_t next = look_up(i0 + warp * 8 * BPW);
+  int next = look_up(i0 + warp * 8 * BPW);
   for (int i = i0 + warp * 8 * BPW; i < i1; i += kWarps * 8 * BPW) {
-    const int64_t row = next;
+    const int row = next, there = max(row, 0);
     uint4 x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t rk = __shfl_sync(0xffffffffu, row, k * BPW + sub);
-      x[k] = rk < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + rk * (p.Hkv * (D / 4)));
-    }
+    for (int k = 0; k < 8; ++k)
+      x[k] = __ldg(rows + (int64_t)__shfl_sync(0xffffffffu, there, k * BPW + sub) * (p.Hkv * (D / 4)));
     next = look_up(i + kWarps * 8 * BPW);
     float s[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      big = make_uint4(max2(big.x, x[k].x & 0x7FFF7FFFu), max2(big.y, x[k].y & 0x7FFF7FFFu),
-                       max2(big.z, x[k].z & 0x7FFF7FFFu), max2(big.w, x[k].w & 0x7FFF7FFFu));
+      big = larger(big, x[k]);
       uint64_t acc = mul_f32x2(w[0], bf16x2_to_f32x2(x[k].x));
       acc = fma_f32x2(w[1], bf16x2_to_f32x2(x[k].y), acc);
       acc = fma_f32x2(w[2], bf16x2_to_f32x2(x[k].z), acc);
@@ -418,6 +425,7 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
 #pragma unroll
     for (int off = 8; off < L; off <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
     const int at = i + (lane & 7) * BPW + sub;
+    if (__shfl_sync(0xffffffffu, row, (lane & 7) * BPW + sub) < 0) s[0] = 0.f;
     if (li < 8 && at < i1) {
       put(at, s[0]);
       lowest = fminf(lowest, s[0]);
@@ -527,10 +535,13 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
     float m[8] = {}, x[8] = {};
     if (k < run) {
       const uint16_t* row = p.q + ((int64_t)(t + k) * p.Hkv + kh) * p.G * D + d;
-#pragma unroll 8
-      for (int h = 0; h < p.G; ++h) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + h * D));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint4 v[kMaxGroup];
+#pragma unroll
+      for (int h = 0; h < kMaxGroup; ++h)
+        v[h] = h < p.G ? __ldg(reinterpret_cast<const uint4*>(row + h * D)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < kMaxGroup; ++h) {
+        const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {  // as in coefficients()
           const float y = q_value((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, p.q_f16);
@@ -565,28 +576,29 @@ __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPa
   for (int k = 0; k < C; ++k) big[k] = make_uint4(kLeast, kLeast, kLeast, kLeast);
   float lowest = -kNegInf, highest = kNegInf;
   bool outside = false;
+  // columns past the last block repeat it; a block of no row counts as 0
   auto row_at = [&](int i) {
-    int64_t row = -1;
-    if (i < i1) {
-      row = bounds_row(p, r, b, i);
-      outside |= row < 0;
-    }
+    const int row = (int)bounds_row(p, r, b, min(i, i1 - 1));
+    outside |= row < 0;
     return row;
-  };
-  auto larger = [](const uint4& a, const uint4& x) {
-    return make_uint4(max2(a.x, x.x & 0x7FFF7FFFu), max2(a.y, x.y & 0x7FFF7FFFu), max2(a.z, x.z & 0x7FFF7FFFu),
-                      max2(a.w, x.w & 0x7FFF7FFFu));
   };
   // columns 2 q, 2 q + 1 of token g: four chains, the upper and the lower part
   auto total = [](const float (&d)[2][4], int e) { return (d[0][e] + d[1][e]) + (d[0][2 + e] + d[1][2 + e]); };
   for (int i = i0 + warp * 16; i < i1; i += kWarps * 16) {
-    const int64_t row[2] = {row_at(i + g), row_at(i + 8 + g)};
+    const int row[2] = {row_at(i + g), row_at(i + 8 + g)};
     uint4 x[2][C];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int k = 0; k < C; ++k)
-        x[u][k] = row[u] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(rows + row[u] * (p.Hkv * (D / 4)) + 4 * k);
+        x[u][k] = __ldg(rows + (int64_t)max(row[u], 0) * (p.Hkv * (D / 4)) + 4 * k);
+    if (__any_sync(0xffffffffu, min(row[0], row[1]) < 0)) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          if (row[u] < 0) x[u][k] = make_uint4(0, 0, 0, 0);
+    }
     float d[2][2][4] = {};  // [tile][chain]
 #pragma unroll
     for (int k = 0; k < C; ++k) {
@@ -1104,7 +1116,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool ws_fits(const void* ws, size_t bytes, size_t need) { return ws && aligned(ws, 256) && bytes >= need; }
 
 int check_blocks(const attn_kv_t* kv, const attn_blocks_t* blocks) {
-  if (!blocks || !blocks->bounds || !aligned(blocks->bounds, 16) || blocks->num_rows <= 0) return ATTN_EINVAL;
+  if (!blocks || !blocks->bounds || !aligned(blocks->bounds, 16) || blocks->num_rows <= 0 || blocks->num_rows > 0x7fffffff) return ATTN_EINVAL;
   if (!block_size_ok(blocks->block_size)) return ATTN_EINVAL;
   if (kv->page_table) {
     if (blocks->block_size > kv->page_size || blocks->num_rows < kv->num_slots / blocks->block_size) return ATTN_EINVAL;

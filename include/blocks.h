@@ -52,6 +52,7 @@ extern "C" {
  *                     num_slots / block_size: pages that requests share have their
  *                     bounds in common; row_base is not used (may be NULL);
  *   contiguous cache: row_base[b] + i (int64 [B] on the device).
+ * num_rows is below 2^31.
  * Only blocks that are full have bounds: a query always takes the block of its own
  * position.  attn_pages_fork, _copy and _compact move entries and not bounds: make
  * those anew with `start` (below; after a fork from the first position of the copied

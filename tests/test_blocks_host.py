@@ -133,6 +133,12 @@ def refused(lib, names, code=-1, **kw):
             assert rc in PAST_CHECKS, (name, kw, rc)
 
 
+def test_row_numbers_have_32_bits(lib):
+    refused(lib, set(), blocks={"num_rows": 2 ** 31 - 1})
+    refused(lib, {"bounds", "select"}, blocks={"num_rows": 2 ** 31})
+    refused(lib, {"bounds", "select"}, blocks={"num_rows": 2 ** 32 + 16})
+
+
 def test_block_calls_check_their_arguments(lib):
     from causal_gqa_attention_qkv_gb300 import attn
     every = {"bounds", "select", "attend"}

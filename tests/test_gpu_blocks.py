@@ -173,6 +173,61 @@ def test_select_several_tokens(kind, hq, hkv, d, page, block):
         check_select(s, first, last, keep)
 
 
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (6, 3), (4, 1), (24, 3)])
+@pytest.mark.parametrize("new", [1, 6])
+def test_select_for_groups_of_any_size(hq, hkv, new):
+    s = Cache("bf16", hq, hkv, 64, [3000, 900, 64 * 64], [new] * 3, 64, 64, seed=hq)
+    fill_bounds(s)
+    for first, last, keep in ((1, 1, 12), (0, 1, 2)):
+        check_select(s, first, last, keep)
+
+
+@pytest.mark.parametrize("new", [1, 6])
+def test_blocks_of_no_page_count_as_zero(new):
+    s = Cache("bf16", 8, 2, 128, [3000, 2000], [new, new], 128, 64, seed=3)
+    fill_bounds(s)
+    zero = s.bounds.double().cpu().numpy()
+    for b, page, bad in ((0, 3, -1), (0, 11, 10 ** 6), (1, 7, -2 ** 31), (0, 17, s.c["slots"] // 128)):
+        row = int(s.c["table"][b, page]) * 2
+        zero[row:row + 2] = 0.0
+        s.kv.page_table[b, page] = bad
+    got, st = run_select(s, 1, 1, 9)
+    assert st == CAP
+    assert np.array_equal(got, rb.select(s.c, s.q64(), zero, 1, 1, 9))
+
+
+@pytest.mark.parametrize("base", [-2 ** 33 + 5, -2 ** 40, 2 ** 33 + 1, -1000, 2 ** 62])
+@pytest.mark.parametrize("new", [1, 6])
+def test_rows_far_outside_the_bounds(base, new):
+    """None of them is read: every block counts as 0, and ties go to the lower ones."""
+    s = Cache("bf16", 8, 2, 128, [3000], [new], 0, 64)
+    fill_bounds(s)
+    s.blocks.row_base = torch.tensor([base]).cuda()
+    got, st = run_select(s, 1, 2, 9)
+    assert st == CAP
+    n = [(3000 + j) // 64 + 1 for j in range(new)]
+    want = np.array([list(range(7)) + [k - 2, k - 1] for k in n])
+    assert np.array_equal(got, np.repeat(want[:, None], 2, 1))
+
+
+def lattice_bounds(s, step, seed=0):
+    """Bounds whose scores are multiples of a small step: many are equal, or a step apart."""
+    rng = torch.Generator().manual_seed(seed)
+    mid = torch.randint(-3, 4, (s.c["rows"], s.hkv, s.d), generator=rng).float()
+    s.bounds.copy_(torch.stack((mid - 1, mid + 1), 2).bfloat16())
+    s.bounds[:, :, 0, 0] = (-step * torch.randint(0, 3, (s.c["rows"], s.hkv), generator=rng)).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("step", [0.0, 2.0 ** -9, 2.0 ** -30])
+@pytest.mark.parametrize("new", [1, 6])
+def test_scores_that_are_close_around_the_last_one_taken(step, new):
+    s = Cache("bf16", 8, 2, 128, [64 * 120, 64 * 300 + 5], [new, new], 0, 64, seed=int(step * 512))
+    s.q.copy_(torch.randint(-2, 3, s.q.shape, generator=torch.Generator().manual_seed(1)).to(s.q))
+    lattice_bounds(s, step)
+    for keep in (2, 3, 7, 20, 64, 100):
+        check_select(s, 0, 1, keep)
+
+
 def test_select_many_requests():
     s = Cache("bf16", 2, 1, 64, [700 + 3 * i for i in range(700)], [1] * 700, 64, 64)
     fill_bounds(s)
