@@ -370,7 +370,9 @@ constexpr float kSubnormals = 2.4e-38f;
 
 // Scores of the blocks [i0, i1) of a request for one token, by the CTA: a warp takes 8 blocks
 // (D = 64: 16) at a time, lane l of the D / 4 lanes of a block holds 8 components of lo (the
-// first half of the lanes) or hi.  coef: M, P; row_of(i): the row of block i; put(block, score);
+// first half of the lanes) or hi.  Three CTAs per SM are bound by issue slots (240 instructions for 8
+// blocks; as a product on the tensor cores, whose 16 rows one token leaves nearly empty, the
+// registers leave room for two CTAs per SM instead of three: 16.4 us against 13.9).  coef: M, P; row_of(i): the row of block i; put(block, score);
 // tell(range of this warp's scores), by one lane.  Returns whether a row lay outside.
 template <int D, typename Row, typename Put, typename Tell>
 __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0, int i1, const float* coef, Row&& row_of,
@@ -499,7 +501,7 @@ __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, in
 // A comes from shared memory, so a warp takes two tiles of 8 blocks for each of its reads (one tile
 // was bound by them).  The sums of magnitudes are a product too: M <= 0 <= P, so they are those of
 // the blocks' largest magnitudes, negated for lo.  55 tokens of 12 requests over up to 100000
-// keys: 33.6 us with the selection (sums on the fp32 units, 48).
+// keys: 26.0 us with the selection (33.6 when sums on the fp32 units took 48).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
   constexpr int C = D / 16;      // 16-byte chunks of a block's row per lane
@@ -1145,7 +1147,7 @@ BlocksPar blocks_par(const attn_config_t* cfg, const attn_kv_t& kv, const attn_b
 int blocks_of(int32_t max_kv_len, int32_t block_size) { return (int)(((int64_t)max_kv_len + block_size - 1) / block_size); }
 
 // Blocks per CTA of the two-kernel selection: 55 tokens of 12 requests over up to 100000 keys take
-// 40.7, 37.1, 42.0, 49.2 us with 256, 512, 768, 1024 (each CTA has its coefficients to make first).
+// 28.3, 25.9, 28.3, 32.0 us with 256, 512, 768, 1024 (each CTA has its coefficients to make first).
 constexpr int kChunk = 512;
 
 // Behind the header: exact scores, scores, ranges.
@@ -1172,17 +1174,21 @@ int launch_bounds_d(const BlocksPar& p, int kv_dtype, cudaStream_t s) {
 
 // One kernel or two: tokens of one request next to each other share the reading of the bounds
 // in the two, and the one spares a launch and the scores' way through memory.  16 requests of
-// up to 30000 keys: 16.9 us (one kernel), 20.8 (two) with a token each, 19.4 and 22.3 with 24
-// tokens, 29.9 and 24.7 with 40, 35.5 and 30.3 with 80.
-// Clusters where there are few lists (us with 1, 2, 4, 8, 16 CTAs each): 8 lists of 1016 blocks
-// 20.7, 13.7, 9.8, 7.9, 7.4; 32 of 1016 23.0, 17.0, 13.2, 12.5, 12.6; 64 of 470 12.8, 11.2, 10.6, 12.7,
-// 20.1; 128 of 256 11.6, 15.1, 15.3, 19.0, 34.6; 256 of 470 23.0, 29.2, 29.6, 39.3, 80.7.
+// up to 30000 keys: 14.3 us (one kernel), 17.7 (two) with a token each, 15.1 and 19.1 with 24
+// tokens, 18.8 and 21.4 with 40, 27.6 and 25.3 with 80; 30 tokens of 12 requests of up to 100000
+// keys 34.1 and 26.6; few lists: 8 tokens of one request of 30000 keys 9.3 and 16.0, of 100000
+// 18.5 and 16.8.
+// Clusters where there are few lists (us with 1, 4, 8, 16 CTAs each; two are never the best):
+// 8 lists of 128 blocks 5.9, 5.4, 5.5, 6.1; 8 of 1016 17.5, 8.4, 6.8, 6.6; 32 of 256 8.3, 8.0, 7.7, 10.0;
+// 64 of 470 12.1, 11.5, 12.6, 16.9; 96 of 313 9.9, 9.7, 12.7, 21.9; 96 of 940 22.9, 15.5, 18.1, 26.1;
+// 128 of 470 13.6, 13.2, 16.3, -; 160 of 470 15.8, 17.0, 21.7, -.
 template <int D>
 int launch_select_t(BlocksPar& p, cudaStream_t s) {
   const int64_t lists = (int64_t)p.N * p.Hkv;
-  if (p.N < 2 * (int64_t)p.B && p.max_blocks <= kHeldAll) {
+  const bool few = lists <= 96;
+  if (p.max_blocks <= kHeldAll && (few || p.N < (p.max_blocks <= 1024 ? 3 : 2) * (int64_t)p.B)) {
     int c = 1;
-    while (lists <= 64 && c < 16 && lists * c < 256 && p.max_blocks > 64 * c) c *= 2;
+    while (few && c < 16 && lists * c <= 192 && p.max_blocks > 32 * c) c *= 2;
     p.chunks = c;
     p.chunk = 64;
     while (p.chunk * c < p.max_blocks) p.chunk *= 2;

@@ -144,11 +144,15 @@ def run_select(s, first, last, keep, cu=True, max_len=None):
     return lists.cpu().numpy(), status(ws)
 
 
+FORMS = (None, 1 << 20)  # bounds on the lengths: with the second, scores go through the workspace
+
+
 def check_select(s, first, last, keep, cu=True, max_len=None):
-    got, st = run_select(s, first, last, keep, cu, max_len)
-    assert st == 0
     want = rb.select(s.c, s.q64(), s.bounds.double().cpu().numpy(), first, last, keep)
-    assert np.array_equal(got, want)
+    for bound in FORMS if max_len is None else (max_len,):
+        got, st = run_select(s, first, last, keep, cu, bound)
+        assert st == 0
+        assert np.array_equal(got, want)
 
 
 @pytest.mark.parametrize("kind,hq,hkv,d", [("bf16", 8, 2, 128), ("e4m3", 8, 8, 64), ("e2m1", 16, 2, 128), ("bf16", 8, 1, 64),
@@ -191,9 +195,10 @@ def test_blocks_of_no_page_count_as_zero(new):
         row = int(s.c["table"][b, page]) * 2
         zero[row:row + 2] = 0.0
         s.kv.page_table[b, page] = bad
-    got, st = run_select(s, 1, 1, 9)
-    assert st == CAP
-    assert np.array_equal(got, rb.select(s.c, s.q64(), zero, 1, 1, 9))
+    for bound in FORMS:
+        got, st = run_select(s, 1, 1, 9, max_len=bound)
+        assert st == CAP
+        assert np.array_equal(got, rb.select(s.c, s.q64(), zero, 1, 1, 9))
 
 
 @pytest.mark.parametrize("base", [-2 ** 33 + 5, -2 ** 40, 2 ** 33 + 1, -1000, 2 ** 62])
@@ -203,11 +208,12 @@ def test_rows_far_outside_the_bounds(base, new):
     s = Cache("bf16", 8, 2, 128, [3000], [new], 0, 64)
     fill_bounds(s)
     s.blocks.row_base = torch.tensor([base]).cuda()
-    got, st = run_select(s, 1, 2, 9)
-    assert st == CAP
     n = [(3000 + j) // 64 + 1 for j in range(new)]
     want = np.array([list(range(7)) + [k - 2, k - 1] for k in n])
-    assert np.array_equal(got, np.repeat(want[:, None], 2, 1))
+    for bound in FORMS:
+        got, st = run_select(s, 1, 2, 9, max_len=bound)
+        assert st == CAP
+        assert np.array_equal(got, np.repeat(want[:, None], 2, 1))
 
 
 def lattice_bounds(s, step, seed=0):
@@ -236,6 +242,16 @@ def test_select_many_requests():
     s = Cache("bf16", 2, 1, 64, [900 + i for i in range(300)], [i % 5 for i in range(300)], 64, 64)
     fill_bounds(s)
     check_select(s, 1, 1, 6)
+
+
+@pytest.mark.parametrize("batch,new", [(1, 1), (2, 1), (9, 1), (16, 1), (48, 1), (49, 1), (10, 3), (24, 2), (25, 2), (20, 3),
+                                       (2, 24), (1, 50)])
+@pytest.mark.parametrize("blocks", [31, 33, 70, 140, 300, 1030])
+def test_select_around_the_choice_of_kernels(batch, new, blocks):
+    """Numbers of lists and candidates where the split over CTAs changes."""
+    s = Cache("bf16", 4, 2, 64, [64 * blocks - 1 - i % 7 for i in range(batch)], [new] * batch, 0, 64, seed=blocks)
+    fill_bounds(s)
+    check_select(s, 1, 1, 9)
 
 
 @pytest.mark.parametrize("cached", [64 * 2047, 64 * 2048 + 5, 64 * 2050, 64 * 5000])
