@@ -1010,13 +1010,15 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   extern __shared__ uint32_t bits[];
   __shared__ SelectSmem<D> sm;
   const int t = blockIdx.x / p.Hkv, kh = blockIdx.x % p.Hkv;
-  grid_dependency_wait();
-  launch_dependents();
-  // most lists have a few scores to sum again: the coefficients' loads go out with the others
+  // Before the wait: q, the lengths and the page table, which were there when the kernel of the scores
+  // passed its own wait.  Most lists have a few scores to sum again and need the coefficients.
   for (int d = threadIdx.x; d < D; d += kThreads) coefficients(p, t, kh, D, d, &sm.coef[d], &sm.coef[D + d]);
+  clear_select(sm);
   ReqInfo r;
   int b;
   const int n = query_blocks(p, t, &r, &b, kh == 0 && threadIdx.x == 0);
+  grid_dependency_wait();
+  launch_dependents();
   if (n == 0) return;
   if (n <= p.keep) {
     whole_list(p, t, kh, n);
@@ -1028,7 +1030,6 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlocksPar 
   const int lane = threadIdx.x & 31;
   for (int c = lane; p.first + c * p.chunk < n - p.last; c += 32) range = join(range, p.ranges[list * p.chunks + c]);
   range = join_lanes(range);
-  clear_select(sm);
   __syncthreads();
   select_blocks<D, true>(p, r, b, t, kh, n, [&](int i) { return __ldcg(scores + i); }, range, bits,
                    p.keys + list * p.max_blocks, sm);
