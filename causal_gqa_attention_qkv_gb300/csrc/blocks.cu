@@ -501,7 +501,7 @@ __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, in
 // A comes from shared memory, so a warp takes two tiles of 8 blocks for each of its reads (one tile
 // was bound by them).  The sums of magnitudes are a product too: M <= 0 <= P, so they are those of
 // the blocks' largest magnitudes, negated for lo.  55 tokens of 12 requests over up to 100000
-// keys: 26.0 us with the selection (33.6 when sums on the fp32 units took 48).
+// keys: 25.5 us with the selection (fp32 units took 48 where a first form of this took 33.6).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) block_score_kernel(const BlocksPar p) {
   constexpr int C = D / 16;      // 16-byte chunks of a block's row per lane
