@@ -883,7 +883,7 @@ __device__ void select_blocks(const BlocksPar& p, const ReqInfo& r, int b, int t
         if (i < m && x >= low && !(x > high)) sm.open_idx[atomicAdd(&sm.open_n, 1)] = i;  // in any order
       });
       __syncthreads();
-      if (need > 0) {  // (K are sure otherwise)
+      if (need > 0 && open > 0) {  // (K are sure, or scores were left unwritten)
         auto entries = [&](int o) {
           return bounds_entries<D>(p, r, b, kh, p.first + sm.open_idx[min(o, open - 1)], lane);
         };
