@@ -159,23 +159,25 @@ __global__ void __launch_bounds__(kAdjust, 16) logits_adjust_kernel(const Adjust
         if (t[k] < 0 || t[k] >= n) continue;
         const int i = (int)i0 + k * kAdjust + tid;  // an entry: below e1
         const int at = atomicAdd(&biases, 1);  // in any order
+        atomicOr(&is_biased[t[k] >> 5], 1u << (t[k] & 31));
         if (at < kFew) {
           tok[at] = t[k];
           val[at] = __ldg(p.r.bias_value + i);
           idx[at] = i;
-          atomicOr(&is_biased[t[k] >> 5], 1u << (t[k] & 31));
         }
       }
     }
     __syncthreads();
     few = biases;
     if (few > kFew) {
-      if (tid < kRun / 32) is_biased[tid] = 0u;
       sum_biases(p.r, e0, e1, v0, n, kRun, bias, tok, val, cnt);
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[q][e] = __fadd_rn(x[q][e], bias[place(q, e)]);
+        for (int e = 0; e < 4; ++e) {
+          const int i = place(q, e);  // a logit without a bias stays as it is: -0 + 0 would be 0
+          if (is_biased[i >> 5] >> (i & 31) & 1u) x[q][e] = __fadd_rn(x[q][e], bias[i]);
+        }
       few = 0;
       __syncthreads();
     }

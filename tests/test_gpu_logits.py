@@ -223,6 +223,18 @@ def test_logits_that_are_not_finite():
     check(w)
 
 
+@pytest.mark.parametrize("V,biases", [(1000, 0), (1000, 100), (500, 128), (500, 129), (1000, 300), (5000, 3000)])
+def test_zeros_keep_their_sign(V, biases):
+    """Bit for bit, -0 among them: a logit without a bias does not depend on how many of its
+    neighbours have one (a run's biases are summed in another way from 129 on)."""
+    w = Rows(3, V, seed=biases, seen=0.2, biases=biases, dup=biases // 10, mask=0.7)
+    w.x[np.random.RandomState(7).rand(3, V) < 0.6] = -0.0
+    w.bias = [[(t, np.float32(-0.0) if t % 3 == 0 else v) for t, v in x] for x in w.bias]
+    for x, out in ((dev(w.x, torch.float32), None), (dev(w.x, torch.float32), torch.empty(3, V, device="cuda"))):
+        got, want = run(x, w.rules(), out), w.want()
+        assert np.signbit(want).any() and np.array_equal(got.view(np.int32), want.view(np.int32))
+
+
 def test_masks_that_allow_nothing():
     w = Rows(3, 2000, biases=5, mask=0.0)
     w.mask_row[:] = 0
