@@ -67,7 +67,7 @@ struct BlocksPar {
   int32_t ctas_per_request;
   // selection
   const uint16_t* q;         // [N, Hq, D]
-  int32_t q_f16, N, G, first, last, keep, max_blocks, chunk, chunks;
+  int32_t q_f16, N, G, first, last, keep, max_kv_len, max_blocks, chunk, chunks;
   float* scores;             // [N, Hkv, max_blocks]
   Range* ranges;             // [N, Hkv, chunks]
   unsigned long long* keys;  // [N, Hkv, max_blocks] exact scores, where they are needed
@@ -244,12 +244,11 @@ __device__ __forceinline__ int visible_blocks(const BlocksPar& p, const ReqInfo&
     if (report) set_status(p.status, ATTN_STATUS_CAPACITY);
     return 0;
   }
-  const int blocks = ((r.cached + j) >> p.log2_bs) + 1;
-  if (blocks > p.max_blocks) {
+  if (r.cached + r.n_new > p.max_kv_len) {
     if (report) set_status(p.status, ATTN_STATUS_BOUNDS);
     return 0;
   }
-  return blocks;
+  return ((r.cached + j) >> p.log2_bs) + 1;  // at most max_blocks
 }
 __device__ __forceinline__ int query_blocks(const BlocksPar& p, int t, ReqInfo* r, int* b, bool report) {
   int n, j;
@@ -1272,6 +1271,7 @@ int attn_block_select(const attn_config_t* cfg, const void* q, const int32_t* cu
   p.first = first;
   p.last = last;
   p.keep = keep;
+  p.max_kv_len = max_kv_len;
   p.max_blocks = max_blocks;
   const size_t slots = (size_t)N * p.Hkv * max_blocks;
   p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + kWsHeader);

@@ -371,6 +371,25 @@ def test_select_problems_set_the_status():
     assert st & SEQ and (got[5] == -7).all()
 
 
+@pytest.mark.parametrize("new", [1, 8])
+def test_a_request_one_position_past_the_host_bound(new):
+    """None of its lists is written, those of tokens before the bound and of a bound within the
+    last block among them; at the bound all are."""
+    s = Cache("bf16", 2, 1, 64, [3005, 64 * 40 - 3 - new, 1000], [new] * 3, 64, 64)
+    fill_bounds(s)
+    want = rb.select(s.c, s.q64(), s.bounds.double().cpu().numpy(), 1, 1, 6)
+    got, st = run_select(s, 1, 1, 6, max_len=3005 + new)
+    assert st == 0 and np.array_equal(got, want)
+    got, st = run_select(s, 1, 1, 6, max_len=3005 + new - 1)
+    assert st == BOUNDS and (got[:new] == -7).all() and np.array_equal(got[new:], want[new:])
+    # the same in the two-kernel form (more tokens per request)
+    s = Cache("bf16", 4, 4, 64, [3005, 64 * 40 - 3 - 9 * new], [9 * new, 9 * new], 0, 64)
+    fill_bounds(s)
+    want = rb.select(s.c, s.q64(), s.bounds.double().cpu().numpy(), 1, 1, 6)
+    got, st = run_select(s, 1, 1, 6, max_len=3005 + 9 * new - 1)
+    assert st == BOUNDS and (got[:9 * new] == -7).all() and np.array_equal(got[9 * new:], want[9 * new:])
+
+
 def test_select_over_rows_past_two_to_the_31_bytes():
     """Bounds of more than 4 GB: rows are found by 64-bit offsets."""
     s = Cache("bf16", 8, 8, 128, [64 * 90], [1], 0, 64)
