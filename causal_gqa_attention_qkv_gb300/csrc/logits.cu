@@ -7,6 +7,7 @@
 // those of one token are summed by one thread in list order (the order decides the rounding).
 //
 // Dependents start only behind these kernels' own wait (see blocks.cu).
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -284,7 +285,9 @@ template <bool Prompt>
 __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
   using Mark = std::conditional_t<Prompt, uint8_t, uint32_t>;  // there or not; how often
   __shared__ __align__(16) Mark mark[kSegment];
-  const int b = blockIdx.x / p.parts, v0 = blockIdx.x % p.parts * kSegment;
+  const int b = blockIdx.x / p.parts;
+  const int64_t v0 = (int64_t)(blockIdx.x % p.parts) * kSegment;  // rows may be longer than 2^31 words
+  const int lo = (int)min(v0, (int64_t)p.V);  // no token reaches a segment past the vocabulary
   const int tid = threadIdx.x;
   grid_dependency_wait();
   launch_dependents();
@@ -309,9 +312,9 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
 #pragma unroll 8
     for (int64_t t = t0 + tid; t < t1; t += kThreads) {
       const int v = __ldg(p.tokens + t);
-      if (v >= 0 && v < p.V && v >= v0 && v < v0 + kSegment) {
-        if constexpr (Prompt) mark[v - v0] = 1;
-        else atomicAdd(&mark[v - v0], 1u);
+      if (v >= 0 && v < p.V && v >= lo && v < lo + kSegment) {
+        if constexpr (Prompt) mark[v - lo] = 1;
+        else atomicAdd(&mark[v - lo], 1u);
       }
     }
     if (!again) break;
@@ -428,8 +431,8 @@ int attn_tokens_seen(uint16_t* seen, int64_t ld, int32_t num_rows, int32_t V, co
   if (V < 1 || V > (1 << 23) || ld < V || ld % 8 != 0 || num_rows < 1) return ATTN_EINVAL;
   if (flags & ~(ATTN_SEEN_PROMPT | ATTN_SEEN_CLEAR)) return ATTN_EINVAL;
   SeenPar p;
-  const int64_t parts = (ld + kSegment - 1) / kSegment;
-  if (B * parts > 0x7fffffff) return ATTN_EINVAL;
+  const int64_t parts = ld / kSegment + (ld % kSegment != 0);
+  if ((flags & ATTN_SEEN_CLEAR) && parts > 0x7fffffff / std::max(B, 1)) return ATTN_EINVAL;  // CTAs of the call
   p.parts = (int)parts;
   int rc = abi_check_device();
   if (rc) return rc;

@@ -71,7 +71,8 @@ ATTN_API int attn_logits_adjust(const float* logits, int32_t B, int32_t V, int64
  * call first.  Rows outside [0, num_rows) and tokens outside [0, V) are skipped; a row
  * may be named more than once.  ATTN_EINVAL: NULL seen, NULL tokens with N != 0, negative sizes,
  * V < 1, V > 2^23, ld < V or not a multiple of 8, num_rows < 1, a misaligned
- * pointer, cu_seqlens NULL with N != B, other flags. */
+ * pointer, cu_seqlens NULL with N != B, other flags, ATTN_SEEN_CLEAR with
+ * B * ceil(ld / 8192) above 2^31 - 1. */
 ATTN_API int attn_tokens_seen(uint16_t* seen, int64_t ld, int32_t num_rows, int32_t V, const int32_t* rows,
                               const int32_t* cu_seqlens, const int32_t* tokens, int32_t B, int32_t N,
                               int32_t flags, void* stream);

@@ -227,3 +227,16 @@ def test_tokens_seen_checks_its_arguments(lib):
                dict(V=1001), dict(row=ODD), dict(cu=ODD), dict(tok=ODD), dict(tok=None), dict(B=-1), dict(N=-1),
                dict(cu=None), dict(flags=4), dict(flags=-1), dict(V=(1 << 23) + 1, ld=1 << 24)):
         assert call(**kw) == -1, kw
+
+
+def test_tokens_seen_takes_rows_of_any_length(lib):
+    """What the grid of a call that empties rows cannot hold is refused, however large the product;
+    the other calls do not touch whole rows."""
+    def call(ld, B, flags):
+        return lib.attn_tokens_seen(F, ld, 4, 1000, F, F, F, B, 5, flags, None)
+    for ld, B in ((1 << 62, 1 << 15), ((1 << 63) - 8, 1), (1 << 45, 1), (1 << 23, 1 << 21), (8200, 1 << 30)):
+        assert call(ld, B, 2) == call(ld, B, 3) == -1, (ld, B)
+        assert call(ld, B, 0) in PAST_CHECKS and call(ld, B, 1) in PAST_CHECKS, (ld, B)
+    for ld, B in ((1 << 43, 1), (1 << 32, 4000), (1 << 23, (1 << 21) - 1), (8192, 2 ** 31 - 1)):
+        assert call(ld, B, 3) in PAST_CHECKS, (ld, B)
+    assert call((1 << 44) - (1 << 13), 1, 3) in PAST_CHECKS and call(1 << 44, 1, 3) == -1

@@ -320,6 +320,21 @@ def test_a_table_past_two_to_the_32_bytes():
     assert x[0, 5] == -1 and x[0, 151935] == 0 and x[0, 7] == 1
 
 
+@pytest.mark.parametrize("prompt", [False, True])
+def test_rows_of_more_than_two_to_the_31_words(prompt):
+    """Emptied whole, each segment in its place, and nothing before them."""
+    from causal_gqa_attention_qkv_gb300 import attn
+    ld = (1 << 31) + 3 * 8192 + 16
+    seen = torch.full((2, ld), 5, dtype=torch.int16, device="cuda")
+    attn.tokens_seen(seen, 9000, dev([1], torch.int32), dev([7, 8999, 7, 9000, -1], torch.int32), dev([0, 5], torch.int32),
+                     prompt=prompt, clear=True)
+    assert seen[1, 7] == (-32768 if prompt else 2) and seen[1, 8999] == (-32768 if prompt else 1)
+    seen[1, 7] = seen[1, 8999] = 0
+    for row, value in ((0, 5), (1, 0)):
+        for part in seen[row].split(1 << 28):
+            assert (part == value).all()
+
+
 # ------------------------------------------------------------------ refusals of the bindings
 def test_bindings_refuse_what_does_not_fit():
     from causal_gqa_attention_qkv_gb300 import attn
