@@ -285,9 +285,7 @@ template <bool Prompt>
 __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
   using Mark = std::conditional_t<Prompt, uint8_t, uint32_t>;  // there or not; how often
   __shared__ __align__(16) Mark mark[kSegment];
-  const int b = blockIdx.x / p.parts;
-  const int64_t v0 = (int64_t)(blockIdx.x % p.parts) * kSegment;  // rows may be longer than 2^31 words
-  const int lo = (int)min(v0, (int64_t)p.V);  // no token reaches a segment past the vocabulary
+  const int b = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int tid = threadIdx.x;
   grid_dependency_wait();
   launch_dependents();
@@ -311,10 +309,10 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
   for (int i = b;;) {
 #pragma unroll 8
     for (int64_t t = t0 + tid; t < t1; t += kThreads) {
-      const int v = __ldg(p.tokens + t);
-      if (v >= 0 && v < p.V && v >= lo && v < lo + kSegment) {
-        if constexpr (Prompt) mark[v - lo] = 1;
-        else atomicAdd(&mark[v - lo], 1u);
+      const uint32_t v = (uint32_t)__ldg(p.tokens + t);
+      if (v < (uint32_t)p.V && v / kSegment == (uint32_t)part) {
+        if constexpr (Prompt) mark[v % kSegment] = 1;
+        else atomicAdd(&mark[v % kSegment], 1u);
       }
     }
     if (!again) break;
@@ -328,6 +326,7 @@ __global__ void __launch_bounds__(kThreads) seen_fill_kernel(const SeenPar p) {
     }
   }
   __syncthreads();
+  const int64_t v0 = (int64_t)part * kSegment;  // rows may be longer than 2^31 words
   const int n = (int)min((int64_t)kSegment, p.ld - v0);  // a multiple of 8
   uint4* dst = reinterpret_cast<uint4*>(p.seen + row * p.ld + v0);
   for (int i = tid; i < n / 8; i += kThreads) {
