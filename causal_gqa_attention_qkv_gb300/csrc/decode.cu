@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
   __shared__ SplitBlocks<Blocks> s_list;
+  __shared__ SplitSums<Blocks> s_sums;
 
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
@@ -442,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
 
   // ---------------- merge the four warps' partial softmax states
   named_sync_consumers();  // every consumer is done with the stage buffers
-  if (!Blocks && s_cons_abort) return;  // same value for every consumer thread
+  if (s_cons_abort) {  // same value for every consumer thread
+    if constexpr (Blocks) block_merge_none(p, s_sums);
+    return;
+  }
   float* mo = reinterpret_cast<float*>(smem);                 // [warps][G][D]
   float* mm = mo + kConsumerWarps * G * D;                      // [warps][G]
   float* ml = mm + kConsumerWarps * G;                          // [warps][G]
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
   }
   named_sync_consumers();
   if constexpr (Blocks) {
-    block_merge<D>(p, mo, mm, ml, kh, b);
+    block_merge<D>(p, mo, mm, ml, s_sums, kh, b);
     return;
   }
   const bool direct = n_splits == 1;

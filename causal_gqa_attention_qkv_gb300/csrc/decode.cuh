@@ -244,18 +244,26 @@ __device__ __forceinline__ bool blocks_begin(const DecodePar& p, int split, int 
 // ---------------------------------------------------------------- merge of listed blocks
 // The splits of a list are one cluster and merge through distributed shared memory: no
 // partial results in memory and no second launch.
-constexpr int kMaxSplits = 16;        // of a list: the largest cluster
-constexpr int kMergeBytes = 2 * 8 * 4;  // behind the warps' partial results: this CTA's maxima and sums
+constexpr int kMaxSplits = 16;  // of a list: the largest cluster
+
+// A split's maxima and sums, for its peers: at the same place in every CTA, and not among the
+// stage buffers, where copies may still land when a wait has run out.
+template <bool Blocks>
+struct SplitSums {};
+template <>
+struct SplitSums<true> {
+  float max[8], sum[8];  // a sum below 0: this split gave up
+};
 
 // The output rows of token t's group from the warps' partial results mo [warps][G][D], mm
 // and ml [warps][G] (maximum, sum) of every split.  All consumer threads call this;
 // the producer warp calls block_merge_rest().  A list may leave a warp, a split or the token
-// without a key: their maxima are -inf, and no key at all gives zeros.
+// without a key: their maxima are -inf, and no key at all gives zeros.  Where a split gave up
+// (block_merge_none()) none of them stores.
 template <int D>
-__device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const float* mm, float* ml, int kh, int t) {
+__device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const float* mm, const float* ml,
+                                            SplitSums<true>& mine, int kh, int t) {
   const int G = p.G, splits = p.max_splits;
-  float* cm = ml + kConsumerWarps * G;  // [G]
-  float* cl = cm + G;
   uint16_t* out = p.out + ((int64_t)t * p.Hq + kh * G) * D;
   auto store = [&](int idx, float acc, float L) {
     const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
@@ -278,8 +286,8 @@ __device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const
     } else {
       mo[idx] = acc;  // read by this thread only
       if (idx % D == 0) {
-        cm[row] = M;
-        cl[row] = L;
+        mine.max[row] = M;
+        mine.sum[row] = L;
       }
     }
   }
@@ -294,8 +302,9 @@ __device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) v[s] = s < splits ? peer_f32(smem_u32(mo + idx), s) : 0.f;
     const bool there = lane < splits;
-    const float ms = there ? peer_f32(smem_u32(cm + row), lane) : kNegInf;
-    float L = there ? peer_f32(smem_u32(cl + row), lane) : 0.f, M = ms;
+    const float ms = there ? peer_f32(smem_u32(mine.max + row), lane) : kNegInf;
+    float L = there ? peer_f32(smem_u32(mine.sum + row), lane) : 0.f, M = ms;
+    const bool gone = __any_sync(0xffffffffu, L < 0.f);
 #pragma unroll
     for (int off = 8; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     const float w = M == kNegInf ? 0.f : fast_exp2(ms - M);
@@ -306,7 +315,8 @@ __device__ __forceinline__ void block_merge(const DecodePar& p, float* mo, const
       if (s < splits) acc += __shfl_sync(0xffffffffu, w, s) * v[s];
 #pragma unroll
     for (int off = 8; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    store(idx, acc, __shfl_sync(0xffffffffu, L, 0));
+    L = __shfl_sync(0xffffffffu, L, 0);
+    if (!gone) store(idx, acc, L);
   }
   cluster_sync();  // no CTA leaves while another reads from it
 }
@@ -314,6 +324,11 @@ __device__ __forceinline__ void block_merge_rest(const DecodePar& p) {
   if (p.max_splits == 1) return;
   cluster_sync();
   cluster_sync();
+}
+// The consumer threads of a split whose wait ran out call this instead of block_merge().
+__device__ __forceinline__ void block_merge_none(const DecodePar& p, SplitSums<true>& mine) {
+  if (threadIdx.x < 8) mine.sum[threadIdx.x] = -1.f;
+  block_merge_rest(p);
 }
 
 // The kernels' form of a call's arguments.

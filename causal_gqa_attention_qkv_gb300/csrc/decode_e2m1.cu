@@ -62,7 +62,7 @@ struct E2m1Layout {
   static constexpr int kQOffset = kStages * kStageBytes;            // prepared Q: 8 heads x D f16
   static constexpr int kBarOffset = kQOffset + 8 * D * 2;
   static constexpr int kSmemBytes = kBarOffset + 2 * kStages * 8 + 1024;  // + alignment slack
-  static_assert(kQOffset >= kConsumerWarps * 8 * D * 4 + 2 * kConsumerWarps * 8 * 4 + kMergeBytes, "the warps' partial results fit the stages");
+  static_assert(kQOffset >= kConsumerWarps * 8 * D * 4 + 2 * kConsumerWarps * 8 * 4, "the warps' partial results fit the stages");
 };
 
 // Byte offset of `byte` of key row `key` in a tile of codes (D = 128: the 16-byte
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
   __shared__ int s_cons_abort;  // written by consumers only, read after their barrier
 
   __shared__ SplitBlocks<Blocks> s_list;
+  __shared__ SplitSums<Blocks> s_sums;
 
   // b: the request, or the token (Blocks)
   const int split = Blocks ? blockIdx.x % p.max_splits : blockIdx.x, kh = blockIdx.y;
@@ -509,7 +510,10 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
 
   // ---------------- merge the warps' partial softmax states
   named_sync_consumers();  // every consumer is done with the stage buffers
-  if (!Blocks && s_cons_abort) return;  // same value for every consumer thread
+  if (s_cons_abort) {  // same value for every consumer thread
+    if constexpr (Blocks) block_merge_none(p, s_sums);
+    return;
+  }
   float* mo = reinterpret_cast<float*>(smem);  // [warps][G][D]
   float* mm = mo + kConsumerWarps * G * D;         // [warps][G]
   float* ml = mm + kConsumerWarps * G;                 // [warps][G]
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
     }
   named_sync_consumers();
   if constexpr (Blocks) {
-    block_merge<D>(p, mo, mm, ml, kh, b);
+    block_merge<D>(p, mo, mm, ml, s_sums, kh, b);
     return;
   }
   const bool direct = n_splits == 1;

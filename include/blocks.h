@@ -31,7 +31,9 @@
  * hold c_b + n_b entries (skipped: nothing of it is written) and for a page outside
  * the cache (it reads as zeros) or a row outside the bounds (not written, reads as
  * zeros); ATTN_STATUS_SEQLENS for tokens of no request; ATTN_STATUS_BOUNDS for a
- * request longer than max_kv_len (attn_block_select: its lists are left unwritten).
+ * request longer than max_kv_len (attn_block_select: its lists are left unwritten);
+ * ATTN_STATUS_TIMEOUT for a pipeline wait that gave up (attn_block_attend: an internal
+ * error, the token's output for that KV head is left unwritten).
  */
 #ifndef GB300_BLOCKS_H
 #define GB300_BLOCKS_H
