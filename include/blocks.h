@@ -91,7 +91,10 @@ ATTN_API int attn_block_bounds(const attn_config_t* cfg, const attn_kv_t* kv, co
  * the others the keep - first - last with the largest score
  *   sum over d < D of M_d * lo_d + P_d * hi_d,
  *   M_d, P_d: the sums of min(q_hd, 0) and max(q_hd, 0) over the group's query heads h,
- * an upper bound of the heads' summed q . k over the block's keys.  Blocks of equal
+ * an upper bound of the heads' summed q . k over the block's keys as attn_kv_gather gives
+ * them.  (Codes times a k_scale that is no power of two are rounded to bf16 there and in
+ * the bounds, so of the values that attention takes it is one to within 2^-8 of the
+ * products' magnitudes.)  Blocks of equal
  * score: the lower one first; a score that is no number counts as the largest.  The
  * scores are compared as 64-bit arithmetic gives them (fp32 sums with a bound on their error
  * decide, and what that leaves open is summed in fp64), so a list does not depend on

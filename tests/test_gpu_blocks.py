@@ -100,6 +100,47 @@ def test_bounds_of_code_that_is_no_number(code):
     assert got[1, :, 3].isnan().all() and int(got.isnan().sum()) == 2
 
 
+@pytest.mark.parametrize("kind,page,block", [("e4m3", 64, 64), ("e2m1", 256, 128), ("e4m3", 0, 256), ("e2m1", 0, 64)])
+@pytest.mark.parametrize("scale", [0.037, 1 / 3, 1e-38, 2.5e37])
+def test_bounds_under_scales_that_round(kind, page, block, scale):
+    """k_scale no power of two: the bounds are those of the entries that attn_kv_gather gives, bit for
+    bit, and the score bounds q . k of those; of the codes' own values it does to within 2^-8 of the
+    products' magnitudes, which rounding an entry to bf16 moves by at most that."""
+    import ref64
+    from causal_gqa_attention_qkv_gb300 import attn
+    scale = float(np.float32(scale))
+    s = Cache(kind, 4, 2, 64, [0, 100], [700, 413], page, block, seed=block)
+    s.kv.k_scale = scale
+    ws = s.workspace(1)
+    attn.block_bounds(s.cfg, s.kv, s.blocks, s.cu, ws, start=i32([0, 0]))
+    assert status(ws) == 0
+    exact = ref64.entries(s.kv.k_cache, kind, scale, s.kv.k_block_scale)
+    got = s.bounds.double().cpu().numpy()
+    want = rb.bounds(s.c, exact, [0, 0])
+    assert len(want) == 700 // block + 513 // block
+    for row in range(s.c["rows"]):
+        assert np.array_equal(got[row], want.get(row, np.full_like(got[row], 776.0)))
+    k = [torch.empty(700 + 513, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    s.kv.cache_lens.copy_(i32([700, 513]))  # all entries are cached by now
+    attn.kv_gather(s.cfg, s.kv, i32([0, 700, 1213]), i32([0, 0]), *k, ws)
+    assert status(ws) == 0
+    read = k[0].double().cpu().numpy()
+    q = np.random.RandomState(1).randn(2, 2, 64)  # [Hkv, G, D]
+    for b, at, n in ((0, 0, 700), (1, 700, 513)):
+        for i in range(n // block):
+            row, here = rb.row_of(s.c, b, i), slice(at + i * block, at + (i + 1) * block)
+            own = exact[rb.slots_of(s.c, b, np.arange(i * block, (i + 1) * block))]
+            assert np.array_equal(got[row], np.stack((read[here].min(0), read[here].max(0)), 1))
+            if scale > 1 or scale < 1e-30:  # overflow, or steps that are no longer relative
+                continue
+            for h in range(2):
+                top = rb.score(q[h], got[row, h, :1], got[row, h, 1:])[0]
+                for keys, off in ((read[here, h], 0.0), (own[:, h], 2.0 ** -8)):
+                    dots = (keys @ q[h].T).sum(1)
+                    slack = off * (np.abs(keys) @ np.abs(q[h]).T).sum(1)
+                    assert (top >= dots - slack - 1e-12 * np.abs(top)).all()
+
+
 def test_bounds_problems_set_the_status():
     from causal_gqa_attention_qkv_gb300 import attn
     s = Cache("bf16", 2, 2, 64, [0, 0, 100], [200, 200, 30], 64, 64)
