@@ -451,7 +451,8 @@ __device__ __forceinline__ bool score_blocks(const BlocksPar& p, int kh, int i0,
 constexpr int kTokens = 8;
 
 // The g-th group of up to kTokens tokens: request *b, its tokens from place *j on.  False past
-// the last one.  All threads of the CTA call this.
+// the last one.  All threads of the CTA call this.  cu_seqlens that are not in order may give
+// any request and place (sums may even pass 32 bits then), but no request outside [0, B).
 __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, int* j) {
   if (!p.cu_seqlens) {
     *b = g;
@@ -460,10 +461,11 @@ __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, in
   }
   __shared__ int sums[kWarps], found[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) found[0] = -1;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int i = b0 + threadIdx.x;
     const int n = i < p.B ? __ldg(p.cu_seqlens + i + 1) - __ldg(p.cu_seqlens + i) : 0;
-    const int mine = (max(n, 0) + kTokens - 1) / kTokens;
+    const int mine = (min(max(n, 0), p.N) + kTokens - 1) / kTokens;
     int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -486,7 +488,7 @@ __device__ __forceinline__ bool find_group(const BlocksPar& p, int g, int* b, in
       __syncthreads();
       *b = found[0];
       *j = found[1];
-      return true;
+      return *b >= 0;
     }
     g -= total;
     __syncthreads();

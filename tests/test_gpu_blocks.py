@@ -431,6 +431,27 @@ def test_a_request_one_position_past_the_host_bound(new):
     assert st == BOUNDS and (got[:9 * new] == -7).all() and np.array_equal(got[9 * new:], want[9 * new:])
 
 
+@pytest.mark.parametrize("B", [3, 40, 300])
+@pytest.mark.parametrize("form", ["up and down", "steps of 2^31 - 1", "backwards", "one far too long", "negative"])
+def test_seqlens_that_are_in_no_order(B, form):
+    """Reported, and no list holds anything but blocks of a request; a batch after it is as ever."""
+    s = Cache("bf16", 4, 4, 64, [64 * 50 + i % 60 for i in range(B)], [3] * B, 0, 64)
+    fill_bounds(s)
+    want = rb.select(s.c, s.q64(), s.bounds.double().cpu().numpy(), 1, 1, 6)
+    cu, n = s.cu.clone(), np.arange(B + 1)
+    big = 2 ** 31 - 1
+    s.cu.copy_(i32({"up and down": np.where(n % 2, s.N, 0), "steps of 2^31 - 1": np.where(n % 2, big, 0),
+                    "backwards": 3 * (B - n), "one far too long": np.where(n == B, big, 3 * n),
+                    "negative": np.where(n % 2, big - 8, -big + n)}[form]))
+    for bound in FORMS:
+        got, st = run_select(s, 1, 1, 6, max_len=bound)
+        assert st and ((got >= 0) & (got < 52) | (got == -7)).all()
+    s.cu.copy_(cu)
+    for bound in FORMS:
+        got, st = run_select(s, 1, 1, 6, max_len=bound)
+        assert st == 0 and np.array_equal(got, want)
+
+
 def test_select_over_rows_past_two_to_the_31_bytes():
     """Bounds of more than 4 GB: rows are found by 64-bit offsets."""
     s = Cache("bf16", 8, 8, 128, [64 * 90], [1], 0, 64)
