@@ -1180,7 +1180,9 @@ int launch_bounds_d(const BlocksPar& p, int kv_dtype, cudaStream_t s) {
 // tokens, 18.8 and 21.4 with 40, 27.6 and 25.3 with 80; 30 tokens of 12 requests of up to 100000
 // keys 34.1 and 26.6; few lists: 8 tokens of one request of 30000 keys 9.3 and 16.0, of 100000
 // 18.5 and 16.8.
-// Clusters where there are few lists (us with 1, 4, 8, 16 CTAs each; two are never the best):
+// Clusters where there are few lists (us with 1, 4, 8, 16 CTAs each; two were not the best at any of these
+// sizes).  A CTA's share is a power of two, 64 blocks at least, so some of a cluster may have none: of the
+// two CTAs for 33 to 64 blocks one, just above a power of two of blocks nearly half.
 // 8 lists of 128 blocks 5.9, 5.4, 5.5, 6.1; 8 of 1016 17.5, 8.4, 6.8, 6.6; 32 of 256 8.3, 8.0, 7.7, 10.0;
 // 64 of 470 12.1, 11.5, 12.6, 16.9; 96 of 313 9.9, 9.7, 12.7, 21.9; 96 of 940 22.9, 15.5, 18.1, 26.1;
 // 128 of 470 13.6, 13.2, 16.3, -; 160 of 470 15.8, 17.0, 21.7, -.
