@@ -171,12 +171,13 @@ __global__ void __launch_bounds__(kThreads, F8 ? DECODE_F8_MIN_BLOCKS : 0)
         issued = i + 1;
       }
       __syncwarp(1);
-      // After a failed wait, let the copies still in flight land before exit.
-      if (s_abort) {
+      // After a failed wait, let the copies still in flight land before exit (Blocks: also where only the
+      // consumers' has failed; else they have landed by the time that the peers of a cluster meet).
+      if (Blocks || s_abort) {
         for (int i = max(0, issued - Lay::kStages); i < issued; ++i)
           (void)mbar_wait(&full[i % Lay::kStages], (i / Lay::kStages) & 1);
-        set_status(p.status, ATTN_STATUS_TIMEOUT);
       }
+      if (s_abort) set_status(p.status, ATTN_STATUS_TIMEOUT);
     }
     if constexpr (Blocks) {
       __syncwarp();

@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kThreads, DECODE_F4_MIN_BLOCKS)
       issued = i + 1;
       if (++st == S) { st = 0; ph ^= 1; }
     }
-    if (!ok) {  // let the copies still in flight land before exit
+    if (Blocks || !ok) {  // let the copies still in flight land before exit (as in decode.cu)
       for (int i = max(0, issued - S); i < issued; ++i) (void)mbar_wait(&full[i % S], (i / S) & 1);
-      if (lane == 0) set_status(p.status, ATTN_STATUS_TIMEOUT);
+      if (!ok && lane == 0) set_status(p.status, ATTN_STATUS_TIMEOUT);
     }
     if constexpr (Blocks) {
       __syncwarp();
