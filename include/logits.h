@@ -29,7 +29,7 @@ enum { ATTN_SEEN_PROMPT = 1, ATTN_SEEN_CLEAR = 2 };
 /* Rules for the B rows of a call (host struct holding device pointers; a pointer
  * that may be NULL leaves its rule out).
  * Each logit x of token v in row b goes through
- *   1. x + (the sum of the row's biases for v, in list order);
+ *   1. x + (the sum of the row's biases for v, in list order), where it has any;
  *   2. if v was seen (its word is not 0): x / r where x > 0, else x * r, with
  *      r = repetition[b]; an r that is not > 0 leaves x;
  *   3. if v was generated, count times: x - frequency[b] * count, then
